@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "oscar_internal.cuh"
+#include "oscar_kv8.cuh"
 
 using namespace oscar;
 
@@ -870,6 +871,138 @@ oscar_status oscar_decode_bf16_history(oscar_ctx* ctx, const oscar_cache* cache,
                                        int batch, oscar_stream_t stream) {
   const CallRange nvtx_range("oscar_decode_bf16_history");
   return decode_common(ctx, 0, cache, q, out, lse, scratch, scratch_bytes, batch, stream, true);
+}
+
+oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* out) {
+  const oscar_status s = check_cfg(cfg);
+  if (s != OSCAR_OK) return s;
+  if (!out) return OSCAR_ERR_INVALID_ARG;
+  const int Hkv = cfg->num_kv_heads, G = cfg->num_q_heads / Hkv, P = cfg->max_pages_per_req;
+  out->head_bytes = KV8_HEAD_BYTES;
+  out->page_bytes = (size_t)KV8_HEAD_BYTES * Hkv;
+  out->off_scales = KV8_OFF_SCALES;
+  out->weights_floats = KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * P;
+  size_t n = kv8_evict_scratch(kv8_evict_requests(cfg->max_batch, Hkv, P), Hkv, P);
+  for (int w = 0; w < 2; ++w) {
+    const size_t d =
+        kv8_decode_scratch(kv8_decode_requests(cfg->max_batch, Hkv, G, P, w), Hkv, G, P, w, KV8_MAX_GRID).total;
+    if (d > n) n = d;
+  }
+  out->scratch_bytes = n;
+  return OSCAR_OK;
+}
+
+// Requests b0 .. of a cache as a cache of their own.
+static CacheView kv8_rows(const oscar_ctx* ctx, const oscar_cache* c, int b0) {
+  CacheView v = make_view(ctx, c, false);
+  const size_t heads = (size_t)b0 * v.Hkv;
+  v.page_table += (size_t)b0 * v.max_pages_per_req;
+  v.sink_k += heads * SINK * D;
+  v.sink_v += heads * SINK * D;
+  v.ring_k += heads * RECENT * D;
+  v.ring_v += heads * RECENT * D;
+  v.seq_lens += b0;
+  v.hist_lens += b0;
+  v.head_bytes = KV8_HEAD_BYTES;
+  v.page_bytes = (long long)KV8_HEAD_BYTES * v.Hkv;
+  return v;
+}
+
+// What the calls on a cache with 8-bit history check alike.
+static oscar_status kv8_check(const oscar_ctx* ctx, const oscar_cache* cache, const float* weights, int batch) {
+  if (!ctx || !cache_ok(cache, true)) return OSCAR_ERR_INVALID_ARG;
+  if (batch < 0 || batch > ctx->cfg.max_batch || !aligned(weights, 16)) return OSCAR_ERR_INVALID_ARG;
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  return dev == ctx->device ? OSCAR_OK : OSCAR_ERR_INVALID_ARG;
+}
+
+static size_t kv8_weights_row(const oscar_ctx* ctx) {
+  return (size_t)ctx->cfg.num_kv_heads * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * ctx->cfg.max_pages_per_req);
+}
+
+oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* k_new,
+                              const void* v_new, int T, float* weights, int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_append_kv8");
+  const oscar_status s = kv8_check(ctx, cache, weights, batch);
+  if (s != OSCAR_OK) return s;
+  if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
+  if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) || T < 0 || T > (1 << 24))
+    return OSCAR_ERR_INVALID_ARG;
+  if (T == 0) return OSCAR_OK;
+  for (int b0 = 0; b0 < batch; b0 += KV8_MAX_REQUESTS) {
+    const int n = batch - b0 < KV8_MAX_REQUESTS ? batch - b0 : KV8_MAX_REQUESTS;
+    Kv8Append a;
+    a.cv = kv8_rows(ctx, cache, b0);
+    const size_t off = (size_t)b0 * T * ctx->cfg.num_kv_heads * D;
+    a.k = (const __nv_bfloat16*)k_new + off;
+    a.v = (const __nv_bfloat16*)v_new + off;
+    a.weights = weights ? weights + b0 * kv8_weights_row(ctx) : nullptr;
+    a.T = T;
+    const cudaError_t e = launch_kv8_append(a, type, n, ctx->num_sms, (cudaStream_t)stream, &ctx->prof);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return OSCAR_OK;
+}
+
+oscar_status oscar_decode_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, void* out,
+                              float* lse, float* weights, float decay, void* scratch, size_t scratch_bytes,
+                              int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_decode_kv8");
+  const oscar_status s = kv8_check(ctx, cache, weights, batch);
+  if (s != OSCAR_OK) return s;
+  if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
+  if (!q || !out || !scratch || !aligned(q, 16) || !aligned(out, 16) || !aligned(scratch, 256) ||
+      (lse && !aligned(lse, 4)) || (weights && !(decay >= 0.f && std::isfinite(decay))))
+    return OSCAR_ERR_INVALID_ARG;
+  if (batch == 0) return OSCAR_OK;
+  const int Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads, P = ctx->cfg.max_pages_per_req;
+  const int grid = ctx->num_sms < KV8_MAX_GRID ? ctx->num_sms : KV8_MAX_GRID;
+  const int per = kv8_decode_requests(batch, Hkv, ctx->G, P, weights != nullptr);
+  const Kv8Scratch sl = kv8_decode_scratch(per, Hkv, ctx->G, P, weights != nullptr, grid);
+  if (scratch_bytes < sl.total) return OSCAR_ERR_INVALID_ARG;
+  for (int b0 = 0; b0 < batch; b0 += per) {
+    Kv8Decode a;
+    a.cv = kv8_rows(ctx, cache, b0);
+    a.q = (const __nv_bfloat16*)q + (size_t)b0 * Hq * D;
+    a.out = (__nv_bfloat16*)out + (size_t)b0 * Hq * D;
+    a.lse = lse ? lse + (size_t)b0 * Hq : nullptr;
+    a.weights = weights ? weights + b0 * kv8_weights_row(ctx) : nullptr;
+    a.decay = decay;
+    a.part = (float*)scratch;
+    a.wsum = (float*)((uint8_t*)scratch + sl.off_wsum);
+    a.wmax = (float*)((uint8_t*)scratch + sl.off_wmax);
+    a.B = batch - b0 < per ? batch - b0 : per;
+    a.grid = grid;
+    a.wait_polls = ctx->wait_polls;
+    const cudaError_t e = launch_kv8_decode(a, type, (cudaStream_t)stream, &ctx->prof);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return OSCAR_OK;
+}
+
+oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* weights, int budget,
+                             void* scratch, size_t scratch_bytes, int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_evict_kv8");
+  const oscar_status s = kv8_check(ctx, cache, weights, batch);
+  if (s != OSCAR_OK) return s;
+  if (!weights || budget < 0 || !scratch || !aligned(scratch, 256)) return OSCAR_ERR_INVALID_ARG;
+  if (batch == 0) return OSCAR_OK;
+  const int Hkv = ctx->cfg.num_kv_heads, P = ctx->cfg.max_pages_per_req;
+  const int per = kv8_evict_requests(batch, Hkv, P);
+  if (scratch_bytes < kv8_evict_scratch(per, Hkv, P)) return OSCAR_ERR_INVALID_ARG;
+  for (int b0 = 0; b0 < batch; b0 += per) {
+    Kv8Evict a;
+    a.cv = kv8_rows(ctx, cache, b0);
+    a.weights = weights + b0 * kv8_weights_row(ctx);
+    a.list = (int32_t*)scratch;
+    a.budget = budget;
+    const int n = batch - b0 < per ? batch - b0 : per;
+    const cudaError_t e = launch_kv8_evict(a, n, ctx->num_sms, (cudaStream_t)stream, &ctx->prof);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return OSCAR_OK;
 }
 
 oscar_status oscar_quantize_rotated_f32(const float* x, int n, int group_size, float clip,

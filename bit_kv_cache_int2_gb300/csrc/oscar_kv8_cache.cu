@@ -1,0 +1,433 @@
+// Writing and evicting in a cache with 8-bit history (sm_103a).
+#include "oscar_kv8.cuh"
+
+namespace oscar {
+
+namespace {
+
+// ------------------------------------------------------------------- append
+constexpr int AW = 16;  // warps per append CTA
+
+// One side of a block, 64 BF16 values per lane in the order of the layout:
+// K: w[c][r][j]  row 8r + gid, channels 32c + 8tq + 2j, + 1
+// V: w[2h + l][i][j]  row 8h + 2tq + l, channels 16gid + 8i + 2j, + 1
+struct SideRows {
+  uint4 w[4][2];
+};
+
+__device__ __forceinline__ uint32_t word(const uint4& x, int j) { return ((const uint32_t*)&x)[j]; }
+
+// Row(t): the address of token t's 128 channels.
+template <typename Row>
+__device__ __forceinline__ void load_side(SideRows& S, int side, int lane, Row row) {
+  const int gid = lane >> 2, tq = lane & 3;
+  if (side == 0) {
+    const uint4* r0 = (const uint4*)(row(gid)) + tq;
+    const uint4* r1 = (const uint4*)(row(8 + gid)) + tq;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      S.w[c][0] = r0[4 * c];
+      S.w[c][1] = r1[4 * c];
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint4* r = (const uint4*)(row(8 * (t >> 1) + 2 * tq + (t & 1))) + 2 * gid;
+      S.w[t][0] = r[0];
+      S.w[t][1] = r[1];
+    }
+  }
+}
+
+// x qmax / am rounded to the nearest 8-bit value, ties to even, exactly.
+// f = qmax / am has one rounding and x f another, so y is within 2^-23 of the
+// quotient.  x and am have 8 significant bits and the midpoints between codes
+// at most 8, so a quotient that is not a midpoint is at least 2^-16 away from
+// it: rounding y to 20 bits first puts every midpoint back in its place and
+// moves nothing across one.
+__device__ __forceinline__ float snap20(float y) {
+  return __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Bytes 0..3 = the codes of a, b, c, d.
+template <int TYPE>
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float f) {
+  a = snap20(a * f);
+  b = snap20(b * f);
+  c = snap20(c * f);
+  d = snap20(d * f);
+  if (TYPE == OSCAR_KV8_E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+  } else {
+    // y + 1.5 2^23 rounds y to an integer, whose low byte is the code
+    const float M = 12582912.f;
+    const uint32_t ab = prmt(__float_as_uint(a + M), __float_as_uint(b + M), 0x0040);
+    const uint32_t cd = prmt(__float_as_uint(c + M), __float_as_uint(d + M), 0x0040);
+    return prmt(ab, cd, 0x5410);
+  }
+}
+
+// A warp quantises one side of a block and writes codes and scale.
+template <int TYPE>
+__device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8_t* block, float* scale, int lane) {
+  const float qmax = TYPE == OSCAR_KV8_E4M3 ? 448.f : 127.f;
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, word(S.w[i][r], j) & 0x7fff7fffu);
+  mx = max(mx >> 16, mx & 0xffffu);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  // an infinity or NaN in the block: NaN as its scale, so that whatever reads the block shows it
+  const bool bad = mx >= 0x7f80u;
+  const float am = fmaxf(__uint_as_float(mx << 16), KV8_TINY);
+  const int e = (int)((__float_as_uint(am) >> 23) & 0xffu) - 127;  // am = 2^e x [1, 2)
+  const float unit = __uint_as_float((__float_as_uint(am) & 0x007fffffu) | 0x3f800000u);
+  const float f = bad ? 0.f : ldexpf(__fdiv_rn(qmax, unit), -e);
+  uint4* dst = (uint4*)(block + side * (KV8_BLK * D)) + lane;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4 o;
+    uint32_t* ow = (uint32_t*)&o;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x, y;
+        float a, b, p, q;
+        if (side == 0) {  // bytes: row 8r + gid, channels + l
+          x = word(S.w[c][0], 2 * s + h);
+          y = word(S.w[c][1], 2 * s + h);
+          a = bf_lo(x), b = bf_hi(x), p = bf_lo(y), q = bf_hi(y);
+        } else {  // bytes: channel + r, token 8h + 2tq + l
+          const int j = 2 * c + s;  // channel pair 16gid + 2j
+          x = word(S.w[2 * h][j >> 2], j & 3);
+          y = word(S.w[2 * h + 1][j >> 2], j & 3);
+          a = bf_lo(x), b = bf_lo(y), p = bf_hi(x), q = bf_hi(y);
+        }
+        ow[2 * s + h] = bad ? 0u : codes4<TYPE>(a, b, p, q, f);
+      }
+    dst[32 * c] = o;
+  }
+  if (lane == 0) *scale = bad ? __uint_as_float(0x7fffffffu) : __fdiv_rn(am, qmax);
+}
+
+// The lengths an append leaves, and whether it can be done at all: `err` is
+// the reason if not.  Every thread of the block calls it.
+struct AppendPlan {
+  int L, H, L1, H1;
+  int err;
+};
+
+__device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, int T) {
+  AppendPlan p;
+  const Kv8Req r = kv8_req(cv, b);
+  p.L = r.L;
+  p.H = r.H;
+  p.err = r.ok ? 0 : OSCAR_ERR_STATE;
+  const long long L1 = (long long)r.L + T;
+  // a window of at most 256 tokens that starts on a block: its last 16 blocks
+  const long long last = L1 > SINK ? (L1 - SINK - 1) / KV8_BLK : -1;
+  long long H1 = (last + 1 - KV8_RING_BLOCKS) * KV8_BLK;
+  if (H1 < r.H) H1 = r.H;
+  if (!p.err && (H1 + PAGE - 1) / PAGE > cv.max_pages_per_req) p.err = OSCAR_ERR_RANGE;
+  p.L1 = (int)L1;
+  p.H1 = (int)H1;
+  int bad = 0;
+  if (!p.err)
+    for (int pg = r.H / PAGE + (int)threadIdx.x; pg < (int)((H1 + PAGE - 1) / PAGE); pg += blockDim.x) {
+      if (H1 == r.H) break;  // no block leaves the window: no page is looked at
+      const int id = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
+      if (id < 0) bad |= 1;
+      if (id >= cv.num_pages) bad |= 2;
+    }
+  const int none = __syncthreads_or(bad & 1), range = __syncthreads_or(bad & 2);
+  if (!p.err && (none || range)) p.err = none ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
+  return p;
+}
+
+// T new tokens of request blockIdx.y.  Work is in units of one block of 16
+// positions, kv head and side, a warp each; unit 0 is the sink.
+//  - A block of new tokens only that falls out of the window at once is
+//    quantised straight from the input.
+//  - A block that stays is written to its ring slots.  The block that had the
+//    slots, if it leaves the window in this call, is quantised first by the
+//    same warp (its tokens from the ring, and from the input those it still
+//    lacked), so no other warp reads what this one overwrites.
+// With one CTA per request (SOLE) the CTA writes the lengths when all its
+// warps are done; else append_lengths_kernel does afterwards.
+template <int TYPE, bool SOLE>
+__global__ void __launch_bounds__(AW * 32) append_kernel(Kv8Append a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheView& cv = a.cv;
+  const int b = blockIdx.y, Hkv = cv.Hkv, T = a.T;
+  const AppendPlan p = append_plan(cv, b, T);
+  if (p.err) {
+    if (SOLE && threadIdx.x == 0) record_error(cv.err, p.err);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int old_last = p.L > SINK ? (p.L - SINK - 1) / KV8_BLK : -1;    // last block with a token before the call
+  const int first = ((p.L > SINK ? p.L : SINK) - SINK) / KV8_BLK;       // first block with a new one
+  const int last = p.L1 > SINK ? (p.L1 - SINK - 1) / KV8_BLK : -1;
+  const int h0 = p.H / KV8_BLK, h1 = p.H1 / KV8_BLK;
+  const long long tasks = (long long)(1 + (last >= first ? last - first + 1 : 0)) * Hkv * 2;
+  const size_t wrow = (size_t)KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req;
+  for (long long w = (long long)blockIdx.x * AW + warp; w < tasks; w += (long long)gridDim.x * AW) {
+    const int side = (int)(w & 1), h = (int)((w >> 1) % Hkv), u = (int)((w >> 1) / Hkv) - 1;
+    const size_t head = (size_t)b * Hkv + h;
+    const __nv_bfloat16* in = (side ? a.v : a.k) + ((size_t)b * T * Hkv + h) * D;  // token t at in + t Hkv D
+    const size_t in_row = (size_t)Hkv * D;
+    __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
+    float* wts = a.weights ? a.weights + head * wrow : nullptr;
+    if (u < 0) {  // the sink
+      __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
+      const int end = p.L1 < SINK ? p.L1 : SINK;
+      for (int t = p.L + (lane >> 4); t < end; t += 2)
+        ((uint4*)(sink + (size_t)t * D))[lane & 15] = ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
+      continue;
+    }
+    const int k = first + u;
+    int go = -1;  // the block to quantise
+    if (k < h1) {
+      if (k > old_last) go = k;
+    } else {
+      const int o = k - ((k - h0) & ~(KV8_RING_BLOCKS - 1));  // the block of [h0, h0 + 16) with k's ring slots
+      if (o < k && o <= old_last) go = o;
+    }
+    if (go >= 0) {
+      SideRows S;
+      const int pos = SINK + go * KV8_BLK;
+      load_side(S, side, lane, [&](int t) {
+        const int q = pos + t;
+        return q < p.L ? (const __nv_bfloat16*)(ring + (size_t)((q - SINK) & (RECENT - 1)) * D)
+                       : in + (size_t)(q - p.L) * in_row;
+      });
+      const int pid = cv.page_table[(size_t)b * cv.max_pages_per_req + go / KV8_PAGE_BLOCKS];
+      uint8_t* base = kv8_head(cv, pid, h);
+      const int sub = go % KV8_PAGE_BLOCKS;
+      quantise_side<TYPE>(S, side, base + sub * KV8_BLOCK_BYTES, (float*)(base + KV8_OFF_SCALES) + 2 * sub + side, lane);
+      if (wts && side == 0 && lane == 0)
+        wts[KV8_RING_BLOCKS + go] = go <= old_last ? wts[go & (KV8_RING_BLOCKS - 1)] : 0.f;
+    }
+    if (k >= h1) {
+      __syncwarp();  // every lane has read its rows of the block that leaves
+      const int p0 = SINK + k * KV8_BLK;
+      const int from = p0 > p.L ? p0 : p.L, to = p0 + KV8_BLK < p.L1 ? p0 + KV8_BLK : p.L1;
+      for (int t = from + (lane >> 4); t < to; t += 2)
+        ((uint4*)(ring + (size_t)((t - SINK) & (RECENT - 1)) * D))[lane & 15] =
+            ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
+      if (wts && side == 0 && lane == 0 && k > old_last) wts[k & (KV8_RING_BLOCKS - 1)] = 0.f;
+    }
+  }
+  if (SOLE) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      cv.seq_lens[b] = p.L1;
+      cv.hist_lens[b] = p.H1;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const AppendPlan p = append_plan(a.cv, blockIdx.x, a.T);
+  if (threadIdx.x != 0) return;
+  if (p.err) {
+    record_error(a.cv.err, p.err);
+  } else {
+    a.cv.seq_lens[blockIdx.x] = p.L1;
+    a.cv.hist_lens[blockIdx.x] = p.H1;
+  }
+}
+
+// ------------------------------------------------------------------ eviction
+constexpr int ET = 1024;  // threads that select the blocks of one (request, kv head)
+
+// Unsigned keys in the order of the floats, NaN last.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  const uint32_t u = __float_as_uint(w);
+  if (w != w) return 0xffffffffu;
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+__device__ __forceinline__ int block_sum(int v, int* red) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, red[threadIdx.x & 31]);
+}
+
+// Number of set flags in lower threads of the block, and of all (ET threads).
+__device__ __forceinline__ int block_rank(bool flag, int* red, int* all) {
+  const uint32_t m = __ballot_sync(0xffffffffu, flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+  if (lane == 0) red[warp] = __popc(m);
+  __syncthreads();
+  const int n = red[lane];
+  *all = __reduce_add_sync(0xffffffffu, n);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + __popc(m & ((1u << lane) - 1u));
+}
+
+// The blocks of one (request, kv head) that go: the e smallest weights, the
+// lower index first among equal ones.  Of the n - e that stay, those beyond
+// place n - e move into the places below it that become free; both lists are
+// in ascending order and equally long.
+__global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
+  __shared__ int red[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheView& cv = a.cv;
+  const int b = blockIdx.x / cv.Hkv, tid = threadIdx.x;
+  int32_t* list = a.list + (size_t)blockIdx.x * kv8_evict_stride(cv.max_pages_per_req);
+  const Kv8Req r = kv8_req(cv, b);
+  const int n = r.H / KV8_BLK;
+  // whole turns of the ring, so that the window's tokens keep their slots
+  int e = r.H > a.budget ? (r.H - a.budget) / RECENT * KV8_RING_BLOCKS : 0;
+  int err = r.ok ? 0 : OSCAR_ERR_STATE;
+  if (e) {
+    int bad = 0;
+    for (int pg = tid; pg < (r.H + PAGE - 1) / PAGE; pg += ET) {
+      const int id = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
+      if (id < 0) bad |= 1;
+      if (id >= cv.num_pages) bad |= 2;
+    }
+    const int none = __syncthreads_or(bad & 1), range = __syncthreads_or(bad & 2);
+    if (none || range) err = none ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
+  }
+  if (err) e = 0;
+  if (tid == 0) {
+    if (err) record_error(cv.err, err);
+    list[1] = e * KV8_BLK;
+    if (!e) list[0] = 0;
+  }
+  if (!e) return;
+  const float* w = a.weights + (size_t)blockIdx.x * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) +
+                   KV8_RING_BLOCKS;
+  // the e-th smallest key, bit by bit: the largest value with fewer than e keys below it
+  uint32_t cut = 0;
+  int below = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = cut | (1u << bit);
+    int s = 0;
+    for (int i = tid; i < n; i += ET) s += order_key(w[i]) < c;
+    s = block_sum(s, red);
+    if (s < e) {
+      cut = c;
+      below = s;
+    }
+  }
+  const int equal_go = e - below, keep = n - e;
+  int32_t* holes = list + 4;
+  int32_t* ends = holes + 2 * (size_t)cv.max_pages_per_req;
+  int equal = 0, nh = 0, nm = 0;
+  for (int i0 = 0; i0 < n; i0 += ET) {
+    const int i = i0 + tid;
+    const uint32_t key = i < n ? order_key(w[i]) : 0xffffffffu;
+    int all;
+    const bool eq = i < n && key == cut;
+    const int rank = equal + block_rank(eq, red, &all);
+    equal += all;
+    const bool go = i < n && (key < cut || (eq && rank < equal_go));
+    const bool hole = go && i < keep, end = i < n && !go && i >= keep;
+    const int hr = nh + block_rank(hole, red, &all);
+    nh += all;
+    if (hole) holes[hr] = i;
+    const int er = nm + block_rank(end, red, &all);
+    nm += all;
+    if (end) ends[er] = i;
+  }
+  if (tid == 0) list[0] = nh;
+}
+
+// Moves the listed blocks, a warp each, and takes the evicted tokens off the
+// lengths.  Sources lie at or beyond the history's new end, targets before it.
+__global__ void __launch_bounds__(256) evict_move_kernel(Kv8Evict a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const CacheView& cv = a.cv;
+  const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv;
+  const int32_t* list = a.list + (size_t)seg * kv8_evict_stride(cv.max_pages_per_req);
+  const int count = list[0];
+  const int32_t* holes = list + 4;
+  const int32_t* ends = holes + 2 * (size_t)cv.max_pages_per_req;
+  const int32_t* pt = cv.page_table + (size_t)b * cv.max_pages_per_req;
+  float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) + KV8_RING_BLOCKS;
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < count; i += gridDim.y * 8) {
+    const int to = holes[i], from = ends[i];
+    uint8_t* tb = kv8_head(cv, pt[to / KV8_PAGE_BLOCKS], h);
+    const uint8_t* fb = kv8_head(cv, pt[from / KV8_PAGE_BLOCKS], h);
+    const int ts = to % KV8_PAGE_BLOCKS, fs = from % KV8_PAGE_BLOCKS;
+    const uint4* src = (const uint4*)(fb + fs * KV8_BLOCK_BYTES) + lane;
+    uint4* dst = (uint4*)(tb + ts * KV8_BLOCK_BYTES) + lane;
+    uint4 x[KV8_BLOCK_BYTES / 512];
+#pragma unroll
+    for (int j = 0; j < KV8_BLOCK_BYTES / 512; ++j) x[j] = src[32 * j];
+#pragma unroll
+    for (int j = 0; j < KV8_BLOCK_BYTES / 512; ++j) dst[32 * j] = x[j];
+    if (lane == 0) {
+      ((float2*)(tb + KV8_OFF_SCALES))[ts] = ((const float2*)(fb + KV8_OFF_SCALES))[fs];
+      w[to] = w[from];
+    }
+  }
+  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0 && list[1]) {
+    cv.seq_lens[b] -= list[1];
+    cv.hist_lens[b] -= list[1];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, int num_sms, cudaStream_t st, Profiler* prof) {
+  const long long units = ((long long)a.T + KV8_BLK - 2) / KV8_BLK + 1 + 1;  // blocks a call can touch, and the sink
+  const long long ctas = (units * a.cv.Hkv * 2 + AW - 1) / AW;
+  cudaError_t e;
+  prof_begin(prof, OSCAR_KERNEL_KV8_APPEND, st);
+  if (ctas <= 2) {
+    e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, true>, dim3(1, B), dim3(AW * 32), 0, st, a)
+                               : launch_pdl(append_kernel<OSCAR_KV8_INT8, true>, dim3(1, B), dim3(AW * 32), 0, st, a);
+  } else {
+    long long x = (4LL * num_sms + B - 1) / B;
+    if (x > ctas) x = ctas;
+    const dim3 grid((unsigned)x, B);
+    e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, false>, grid, dim3(AW * 32), 0, st, a)
+                               : launch_pdl(append_kernel<OSCAR_KV8_INT8, false>, grid, dim3(AW * 32), 0, st, a);
+    if (e == cudaSuccess) e = launch_pdl(append_lengths_kernel, dim3(B), dim3(128), 0, st, a);
+  }
+  prof_end(prof, OSCAR_KERNEL_KV8_APPEND, st);
+  return e;
+}
+
+int kv8_evict_requests(int batch, int Hkv, int max_pages) {
+  size_t n = KV8_SCRATCH_AIM / (kv8_evict_stride(max_pages) * 4 * Hkv);
+  if (n < 1) n = 1;
+  if (n > KV8_MAX_REQUESTS) n = KV8_MAX_REQUESTS;
+  return (size_t)batch < n ? batch : (int)n;
+}
+
+size_t kv8_evict_scratch(int B, int Hkv, int max_pages) { return (size_t)B * Hkv * kv8_evict_stride(max_pages) * 4; }
+
+cudaError_t launch_kv8_evict(const Kv8Evict& a, int B, int num_sms, cudaStream_t st, Profiler* prof) {
+  const int segs = B * a.cv.Hkv;
+  const int per = (4 * num_sms + segs - 1) / segs;  // CTAs per (request, kv head)
+  prof_begin(prof, OSCAR_KERNEL_KV8_EVICT, st);
+  cudaError_t e = launch_pdl(evict_select_kernel, dim3(segs), dim3(ET), 0, st, a);
+  if (e == cudaSuccess) e = launch_pdl(evict_move_kernel, dim3(segs, per), dim3(256), 0, st, a);
+  prof_end(prof, OSCAR_KERNEL_KV8_EVICT, st);
+  return e;
+}
+
+}  // namespace oscar

@@ -1,0 +1,702 @@
+// Decode attention over a cache with 8-bit history (sm_103a).
+//
+//   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(q k_j / sqrt(128)),
+// over the sink, the history and the recent window, j one token each.  A
+// history token's key is s_K c_K and its value s_V c_V, with 8-bit codes c and
+// one scale per block of 16 tokens.
+//
+// kv8_decode_kernel splits the work evenly over its CTAs; each CTA writes one
+// partial record per (request, kv head) it has a part of, and
+// kv8_merge_kernel joins the records and adds up the blocks' weights.
+#include "oscar_kv8.cuh"
+
+namespace oscar {
+
+namespace {
+
+constexpr int KW = 8;   // warps per decode CTA
+constexpr int MT = 256; // threads per merge CTA
+// A partial record holds per query head: the largest logit m (base 2) and
+// l = sum 2^(s - m); the largest M of t = s + log2 s_V and o = sum 2^(t - M) c_V.
+// The two maxima differ because 2^(t - M) goes through fp16 on its way into
+// the product: the factor s_V must not push it out of range, however the
+// scales of the blocks differ.
+constexpr int REC_M = 0, REC_L = 1, REC_T = 2;
+
+// ------------------------------------------------------------- the work list
+// The work is a sequence of units, 16 KB each: for every (request, kv head) in
+// order, the 32-token pieces of the BF16 regions that hold a token (bit i of
+// the mask: 0, 1 the sink, 2 + r ring slots 32r .. 32r + 31), then the history
+// pages.  CTA i of n takes units [floor(i W / n), floor((i + 1) W / n)).
+__device__ __forceinline__ uint32_t window_units(int L, int H) {
+  uint32_t m = L > 32 ? 3u : L > 0 ? 1u : 0u;
+#pragma unroll
+  for (int r = 0; r < KV8_RING_UNITS; ++r)
+    if (kv8_ring_held(L, H, 2 * r) || kv8_ring_held(L, H, 2 * r + 1)) m |= 4u << r;
+  return m;
+}
+
+struct Segment {  // a request's share of the list, the same for each of its kv heads
+  int L, H, pages, units;
+  uint32_t win;
+};
+
+__device__ __forceinline__ Segment segment_of(const CacheView& cv, int b, bool* ok = nullptr) {
+  const Kv8Req r = kv8_req(cv, b);
+  Segment s;
+  s.L = r.L;
+  s.H = r.H;
+  s.win = window_units(r.L, r.H);
+  s.pages = (r.H + PAGE - 1) / PAGE;
+  s.units = s.pages + __popc(s.win);
+  if (ok) *ok = r.ok;
+  return s;
+}
+
+// ------------------------------------------------------------------ the math
+struct State {
+  float o[8][4];  // o^T: row tile j, channels 16gid + 2j (o[j][hc]) and + 1 (o[j][hc + 2]), head 2tq + hc
+  float m[2], l[2], M[2];
+};
+
+__device__ __forceinline__ void state_clear(State& S) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) S.o[j][0] = S.o[j][1] = S.o[j][2] = S.o[j][3] = 0.f;
+  S.m[0] = S.m[1] = S.M[0] = S.M[1] = -INFINITY;
+  S.l[0] = S.l[1] = 0.f;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// q's fragments: word [c][j] holds channels 32c + 8tq + 2j, + 1 of head gid.
+// As BF16 (the window's products), then as FP16 scaled by a power of two that
+// brings the head's largest magnitude to [2^14, 2^15): exact but for channels
+// more than 2^28 below the largest.
+struct Query {
+  uint32_t w[4][4];
+  float alpha[2];  // of heads 2tq, 2tq + 1: log2(e) / sqrt(128), over the power of two once FP16
+};
+
+__device__ __forceinline__ void query_load(Query& Q, const __nv_bfloat16* q, int G, int gid, int tq) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (gid < G) x = *(const uint4*)(q + (size_t)gid * D + 32 * c + 8 * tq);
+    Q.w[c][0] = x.x;
+    Q.w[c][1] = x.y;
+    Q.w[c][2] = x.z;
+    Q.w[c][3] = x.w;
+  }
+  Q.alpha[0] = Q.alpha[1] = LOG2E * INV_SQRT_D;
+}
+
+__device__ __forceinline__ void query_to_fp16(Query& Q, int tq) {
+  uint32_t mx = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, Q.w[c][j] & 0x7fff7fffu);
+  mx = max(mx >> 16, mx & 0xffffu);
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int e = max((int)(mx >> 7) - 127, -100);
+  const float f = pow2i(14 - e);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x = Q.w[c][j];
+      const __half2 y = __floats2half2_rn(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+      Q.w[c][j] = *(const uint32_t*)&y;
+    }
+  const float al = LOG2E * INV_SQRT_D * pow2i(e - 14);
+  Q.alpha[0] = __shfl_sync(0xffffffffu, al, 8 * tq);  // lane 4n holds head n
+  Q.alpha[1] = __shfl_sync(0xffffffffu, al, 8 * tq + 4);
+}
+
+// Codes 0, 1 and 2, 3 of a word as FP16 pairs, exactly.
+template <int TYPE>
+__device__ __forceinline__ void codes_fp16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (TYPE == OSCAR_KV8_E4M3) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // c + 128 under the exponent of 1024, less 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*(__half2*)&a, off), y = __hsub2(*(__half2*)&b, off);
+    lo = *(uint32_t*)&x;
+    hi = *(uint32_t*)&y;
+  }
+}
+
+// One online-softmax step over NT tiles of 16 tokens.  s: the logits in base 2,
+// -inf where there is no token (at least one token is there), rows gid and
+// gid + 8, heads 2tq and 2tq + 1; lv: log2 of each tile's value scale.  On
+// return p holds 2^(t - M) and sum[t][hc] this thread's part of the tile's
+// sum of 2^(s - m).
+template <int NT>
+__device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], const float (&lv)[NT], float (&p)[NT][4],
+                                             float (&sum)[NT][2]) {
+#pragma unroll
+  for (int hc = 0; hc < 2; ++hc) {
+    float ms = -INFINITY, mt = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float x = fmaxf(s[t][hc], s[t][hc + 2]);
+      ms = fmaxf(ms, x);
+      mt = fmaxf(mt, x + lv[t]);
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    }
+    if (ms > S.m[hc]) {
+      S.l[hc] *= ex2(S.m[hc] - ms);
+      S.m[hc] = ms;
+    }
+    if (mt > S.M[hc]) {
+      const float al = ex2(S.M[hc] - mt);
+      S.M[hc] = mt;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        S.o[j][hc] *= al;
+        S.o[j][hc + 2] *= al;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      sum[t][hc] = ex2(s[t][hc] - S.m[hc]) + ex2(s[t][hc + 2] - S.m[hc]);
+      S.l[hc] += sum[t][hc];
+      p[t][hc] = ex2(s[t][hc] + lv[t] - S.M[hc]);
+      p[t][hc + 2] = ex2(s[t][hc + 2] + lv[t] - S.M[hc]);
+    }
+  }
+}
+
+// The block sums of NT tiles for the merge: ws[n] the sums of head n's blocks,
+// wm[n] what they are relative to.
+template <int NT>
+__device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], float* ws, float* wm, int G, int gid,
+                                           int tq) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int hc = 0; hc < 2; ++hc)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum[t][hc] += __shfl_xor_sync(0xffffffffu, sum[t][hc], o);
+  const int n = 2 * tq + gid;  // lanes of gid 0 and 1 write a head each
+  if (gid < 2 && n < G) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float* x = (float*)&v;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) x[t] = gid ? sum[t][1] : sum[t][0];
+    *(float4*)(ws + 4 * n) = v;
+    wm[n] = gid ? S.m[1] : S.m[0];
+  }
+}
+
+// A page's blocks 0 .. nb - 1 (the others hold nothing and are not looked at).
+template <int TYPE, bool WEIGHTS>
+__device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_t* page, int nb, int lane, int G,
+                                          float* ws, float* wm) {
+  const int gid = lane >> 2, tq = lane & 3;
+  float s[4][4], lv[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
+    lv[t] = 0.f;
+    if (t < nb) {
+      float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 k = *(const uint4*)(page + t * KV8_BLOCK_BYTES + c * 512 + lane * 16);
+        uint32_t a0, a1, a2, a3;
+        codes_fp16<TYPE>(k.x, a0, a1);
+        codes_fp16<TYPE>(k.y, a2, a3);
+        mma_f16(a, a0, a1, a2, a3, Q.w[c][0], Q.w[c][1]);
+        codes_fp16<TYPE>(k.z, a0, a1);
+        codes_fp16<TYPE>(k.w, a2, a3);
+        mma_f16(a, a0, a1, a2, a3, Q.w[c][2], Q.w[c][3]);
+      }
+      const float2 sc = *(const float2*)(page + KV8_OFF_SCALES + 8 * t);
+      // the append makes no scale below 2^-109; a zero (a page that nothing wrote) must not become -inf
+      lv[t] = sc.y < 1.17549435e-38f ? -126.f : lg2(sc.y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][e] = a[e] * (Q.alpha[e & 1] * sc.x);
+    }
+  }
+  float p[4][4], sum[4][2];
+  softmax_step<4>(S, s, lv, p, sum);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (t < nb) {
+      const __half2 h0 = __floats2half2_rn(p[t][0], p[t][1]), h1 = __floats2half2_rn(p[t][2], p[t][3]);
+      const uint32_t b0 = movmatrix_t(*(const uint32_t*)&h0), b1 = movmatrix_t(*(const uint32_t*)&h1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = *(const uint4*)(page + t * KV8_BLOCK_BYTES + KV8_BLK * D + c * 512 + lane * 16);
+        uint32_t a0, a1, a2, a3;
+        codes_fp16<TYPE>(v.x, a0, a1);
+        codes_fp16<TYPE>(v.y, a2, a3);
+        mma_f16(S.o[2 * c], a0, a1, a2, a3, b0, b1);
+        codes_fp16<TYPE>(v.z, a0, a1);
+        codes_fp16<TYPE>(v.w, a2, a3);
+        mma_f16(S.o[2 * c + 1], a0, a1, a2, a3, b0, b1);
+      }
+    }
+  }
+  if (WEIGHTS) write_sums<4>(S, sum, ws, wm, G, gid, tq);
+}
+
+// 32 BF16 tokens at K and V (`stride` bytes from row to row), of which the
+// first n0 of the first 16 and the first n1 of the last 16 are there.  The
+// others may hold anything: their logits become -inf and their values 0.
+// The weights go into the product as two BF16 parts (16 bits together): the
+// newest tokens often carry most of the weight.
+template <bool WEIGHTS>
+__device__ __forceinline__ void window_step(State& S, const Query& Q, const uint8_t* K, const uint8_t* V, int stride,
+                                            int n0, int n1, int lane, int G, float* ws, float* wm) {
+  const int gid = lane >> 2, tq = lane & 3;
+  float s[2][4];
+  const float lv[2] = {0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = t ? n1 : n0;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 x = *(const uint4*)(K + (16 * t + gid) * stride + 64 * c + 16 * tq);
+      const uint4 y = *(const uint4*)(K + (16 * t + 8 + gid) * stride + 64 * c + 16 * tq);
+      mma_bf16(a, x.x, y.x, x.y, y.y, Q.w[c][0], Q.w[c][1]);
+      mma_bf16(a, x.z, y.z, x.w, y.w, Q.w[c][2], Q.w[c][3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[t][e] = (e < 2 ? gid : gid + 8) < n ? a[e] * Q.alpha[e & 1] : -INFINITY;
+  }
+  float p[2][4], sum[2][2];
+  softmax_step<2>(S, s, lv, p, sum);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int n = t ? n1 : n0;
+    if (n == 0) continue;
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(p[t][2 * r], p[t][2 * r + 1]);
+      const float2 f = __bfloat1622float2(hi);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(p[t][2 * r] - f.x, p[t][2 * r + 1] - f.y);
+      bh[r] = movmatrix_t(*(const uint32_t*)&hi);
+      bl[r] = movmatrix_t(*(const uint32_t*)&lo);
+    }
+    uint32_t v[4][8];  // rows 2tq, 2tq + 1, 8 + 2tq, 9 + 2tq, channels 16gid ..
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 8 * (u >> 1) + 2 * tq + (u & 1);
+      const uint4* src = (const uint4*)(V + (16 * t + row) * stride + 32 * gid);
+      const uint4 x = src[0], y = src[1];
+      const bool in = row < n;
+      v[u][0] = in ? x.x : 0u, v[u][1] = in ? x.y : 0u, v[u][2] = in ? x.z : 0u, v[u][3] = in ? x.w : 0u;
+      v[u][4] = in ? y.x : 0u, v[u][5] = in ? y.y : 0u, v[u][6] = in ? y.z : 0u, v[u][7] = in ? y.w : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t a0 = prmt(v[0][j], v[1][j], 0x5410), a1 = prmt(v[0][j], v[1][j], 0x7632);
+      const uint32_t a2 = prmt(v[2][j], v[3][j], 0x5410), a3 = prmt(v[2][j], v[3][j], 0x7632);
+      mma_bf16(S.o[j], a0, a1, a2, a3, bh[0], bh[1]);
+      mma_bf16(S.o[j], a0, a1, a2, a3, bl[0], bl[1]);
+    }
+  }
+  if (WEIGHTS) write_sums<2>(S, sum, ws, wm, G, gid, tq);
+}
+
+// ------------------------------------------------------------------- decode
+struct DecodeSmem {
+  int off_pre, off_comb, total;
+};
+__host__ __device__ inline DecodeSmem decode_smem(int B, int G) {
+  DecodeSmem s;
+  s.off_pre = 0;
+  s.off_comb = (int)(((size_t)(B + 1) * 8 + 127) & ~(size_t)127);
+  s.total = s.off_comb + KW * G * (D + 4) * 4;
+  return s;
+}
+
+// pre[b] = units of the requests before b, over all kv heads; pre[B] = all.
+__device__ inline void unit_prefix(const CacheView& cv, int B, long long* pre) {
+  for (int b = threadIdx.x; b < B; b += blockDim.x) {
+    bool ok;
+    pre[b + 1] = (long long)segment_of(cv, b, &ok).units * cv.Hkv;
+    if (!ok && blockIdx.x == 0) record_error(cv.err, OSCAR_ERR_STATE);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long carry = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      long long v = b0 + lane < B ? pre[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      v += carry;
+      if (b0 + lane < B) pre[b0 + lane + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) pre[0] = 0;
+  }
+  __syncthreads();
+}
+
+template <int TYPE, bool WEIGHTS>
+__global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const CacheView& cv = a.cv;
+  const DecodeSmem SL = decode_smem(a.B, cv.G);
+  long long* pre = (long long*)(smem + SL.off_pre);
+  float* comb = (float*)(smem + SL.off_comb);  // [warp][head][m, l, M, -, o]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tq = lane & 3;
+  const int G = cv.G, Hkv = cv.Hkv, B = a.B;
+  pdl_launch_dependents();
+  pdl_wait();
+  unit_prefix(cv, B, pre);
+  const long long W = pre[B];
+  const long long n = W < a.grid ? W : a.grid;
+  if (blockIdx.x >= n) return;
+  long long u = blockIdx.x * W / n;
+  const long long end = (blockIdx.x + 1) * W / n;
+  int b = balanced_request(pre, B, u);
+  Segment sg = segment_of(cv, b);
+  int h = (int)((u - pre[b]) / sg.units);
+  while (u < end) {  // u: the first unit of (b, h) in this CTA's range
+    const long long s0 = pre[b] + (long long)h * sg.units;
+    const int lo = (int)(u - s0), hi = (int)((end - s0) < sg.units ? end - s0 : sg.units);
+    const int nwin = __popc(sg.win);
+    const int seg = b * Hkv + h;
+    State S;
+    state_clear(S);
+    Query Q;
+    bool fp16 = false;
+    query_load(Q, a.q + ((size_t)b * cv.Hq + (size_t)h * G) * D, G, gid, tq);
+    for (int i = lo + warp; i < hi; i += KW) {
+      if (i < nwin) {
+        const int unit = __fns(sg.win, 0, i + 1);
+        const bool sink = unit < 2;
+        const int r = unit - 2;
+        const uint8_t *K, *V;
+        int n0, n1;
+        if (sink) {
+          K = (const uint8_t*)(cv.sink_k + ((size_t)seg * SINK + 32 * unit) * D);
+          V = (const uint8_t*)(cv.sink_v + ((size_t)seg * SINK + 32 * unit) * D);
+          n0 = min(max(sg.L - 32 * unit, 0), 16);
+          n1 = min(max(sg.L - 32 * unit - 16, 0), 16);
+        } else {
+          K = (const uint8_t*)(cv.ring_k + ((size_t)seg * RECENT + 32 * r) * D);
+          V = (const uint8_t*)(cv.ring_v + ((size_t)seg * RECENT + 32 * r) * D);
+          n0 = kv8_ring_held(sg.L, sg.H, 2 * r);
+          n1 = kv8_ring_held(sg.L, sg.H, 2 * r + 1);
+        }
+        float *ws = nullptr, *wm = nullptr;
+        if (WEIGHTS && !sink) {
+          const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + cv.max_pages_per_req + r;
+          ws = a.wsum + at * G * 4;
+          wm = a.wmax + at * G;
+        }
+        if (WEIGHTS && !sink) window_step<true>(S, Q, K, V, D * 2, n0, n1, lane, G, ws, wm);
+        else window_step<false>(S, Q, K, V, D * 2, n0, n1, lane, G, ws, wm);
+      } else {
+        if (!fp16) query_to_fp16(Q, tq);
+        fp16 = true;
+        const int pg = i - nwin;
+        const int pid = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
+        float *ws = nullptr, *wm = nullptr;
+        if (WEIGHTS) {
+          const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + pg;
+          ws = a.wsum + at * G * 4;
+          wm = a.wmax + at * G;
+        }
+        if (pid < 0 || pid >= cv.num_pages) {  // its tokens are left out
+          if (lane == 0) record_error(cv.err, pid < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+          if (WEIGHTS && lane < G) {
+            *(float4*)(ws + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
+            wm[lane] = -INFINITY;
+          }
+          continue;
+        }
+        const int nb = min(KV8_PAGE_BLOCKS, sg.H / KV8_BLK - pg * KV8_PAGE_BLOCKS);
+        page_step<TYPE, WEIGHTS>(S, Q, kv8_head(cv, pid, h), nb, lane, G, ws, wm);
+      }
+    }
+    // join the warps
+#pragma unroll
+    for (int hc = 0; hc < 2; ++hc) {
+      S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 4);
+      S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 8);
+      S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 16);
+      const int hd = 2 * tq + hc;
+      if (hd < G) {
+        float* c = comb + (warp * G + hd) * PART_STRIDE;
+        if (gid == 0) {
+          c[REC_M] = S.m[hc];
+          c[REC_L] = S.l[hc];
+          c[REC_T] = S.M[hc];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          *(float4*)(c + PART_O + 16 * gid + 2 * j) = make_float4(S.o[j][hc], S.o[j][hc + 2], S.o[j + 1][hc], S.o[j + 1][hc + 2]);
+      }
+    }
+    __syncthreads();
+    float* rec = a.part + ((size_t)blockIdx.x + seg) * G * PART_STRIDE;
+    for (int e = threadIdx.x; e < G * D; e += KW * 32) {
+      const int hd = e / D, c = e % D;
+      float m = -INFINITY, M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        m = fmaxf(m, comb[(w * G + hd) * PART_STRIDE + REC_M]);
+        M = fmaxf(M, comb[(w * G + hd) * PART_STRIDE + REC_T]);
+      }
+      float l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float* x = comb + (w * G + hd) * PART_STRIDE;
+        if (x[REC_M] == -INFINITY) continue;
+        l += x[REC_L] * ex2(x[REC_M] - m);
+        o += x[PART_O + c] * ex2(x[REC_T] - M);
+      }
+      float* y = rec + hd * PART_STRIDE;
+      y[PART_O + c] = o;
+      if (c == 0) {
+        y[REC_M] = m;
+        y[REC_L] = l;
+        y[REC_T] = M;
+      }
+    }
+    __syncthreads();
+    u = s0 + hi;
+    if (u < end && ++h == Hkv) {
+      h = 0;
+      do sg = segment_of(cv, ++b);
+      while (sg.units == 0);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- merge
+// grid (B Hkv, G + slices of the weights): CTA y < G writes the output of the
+// kv head's query head y, the others update a slice of the block weights.
+__global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
+  __shared__ long long sums[MT / 32][2];
+  __shared__ float wm[MT / 32], wl[MT / 32], wt[MT / 32];
+  __shared__ __align__(16) float wo[MT / 32][D];
+  __shared__ float tot_m[MAX_G], tot_r[MAX_G];
+  const CacheView& cv = a.cv;
+  const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv, G = cv.G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  pdl_wait();
+  long long before = 0, all = 0;
+  for (int i = threadIdx.x; i < a.B; i += MT) {
+    const long long x = (long long)segment_of(cv, i).units * cv.Hkv;
+    all += x;
+    if (i < b) before += x;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    sums[warp][0] = before;
+    sums[warp][1] = all;
+  }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < MT / 32; ++w) {
+    before += sums[w][0];
+    all += sums[w][1];
+  }
+  const Segment sg = segment_of(cv, b);
+  Balanced bl;
+  bl.W = all;
+  bl.n = (int)(all < a.grid ? all : a.grid);
+  bl.wch = 0;
+  const long long s0 = before + (long long)h * sg.units;
+  int i0 = 0, i1 = -1;
+  if (sg.units) {
+    i0 = balanced_owner(bl, s0);
+    i1 = balanced_owner(bl, s0 + sg.units - 1);
+  }
+  if (blockIdx.y < G) {
+    const int hd = blockIdx.y;
+    float m = -INFINITY, l = 0.f, M = -INFINITY;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = i0 + warp; i <= i1; i += MT / 32) {
+      const float* r = a.part + (((size_t)i + seg) * G + hd) * PART_STRIDE;
+      const float4 x = *(const float4*)r;
+      if (x.x == -INFINITY) continue;
+      const float4 y = *(const float4*)(r + PART_O + 4 * lane);
+      const float mn = fmaxf(m, x.x), Mn = fmaxf(M, x.z);
+      l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
+      const float fo = ex2(M - Mn), fn = ex2(x.z - Mn);
+      o.x = o.x * fo + y.x * fn;
+      o.y = o.y * fo + y.y * fn;
+      o.z = o.z * fo + y.z * fn;
+      o.w = o.w * fo + y.w * fn;
+      m = mn;
+      M = Mn;
+    }
+    if (lane == 0) {
+      wm[warp] = m;
+      wl[warp] = l;
+      wt[warp] = M;
+    }
+    *(float4*)&wo[warp][4 * lane] = o;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float gm = -INFINITY, gM = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < MT / 32; ++w) {
+        gm = fmaxf(gm, wm[w]);
+        gM = fmaxf(gM, wt[w]);
+      }
+      float gl = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < MT / 32; ++w) {
+        if (wm[w] == -INFINITY) continue;
+        gl += wl[w] * ex2(wm[w] - gm);
+        const float f = ex2(wt[w] - gM);
+        x += wo[w][2 * threadIdx.x] * f;
+        y += wo[w][2 * threadIdx.x + 1] * f;
+      }
+      const bool none = gm == -INFINITY;  // no token at all: zeros and -inf
+      const float f = none ? 0.f : ex2(gM - gm) / gl;
+      const size_t row = (size_t)b * cv.Hq + (size_t)h * G + hd;
+      ((__nv_bfloat162*)(a.out + row * D))[threadIdx.x] = none ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(x * f, y * f);
+      if (a.lse && threadIdx.x == 0) a.lse[row] = none ? -INFINITY : (gm + log2f(gl)) * LN2;
+    }
+    return;
+  }
+  // weights: every head's total first
+  for (int hd = warp; hd < G; hd += MT / 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = i0 + lane; i <= i1; i += 32) {
+      const float* r = a.part + (((size_t)i + seg) * G + hd) * PART_STRIDE;
+      const float rm = r[REC_M], rl = r[REC_L];
+      if (rm == -INFINITY) continue;
+      const float mn = fmaxf(m, rm);
+      l = l * ex2(m - mn) + rl * ex2(rm - mn);
+      m = mn;
+    }
+    float gm = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+    l = m == -INFINITY ? 0.f : l * ex2(m - gm);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      tot_m[hd] = gm;
+      tot_r[hd] = 1.f / l;
+    }
+  }
+  __syncthreads();
+  if (tot_m[0] == -INFINITY) return;  // nothing was attended to
+  const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS);
+  float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req);
+  const int slice = blockIdx.y - G, slices = gridDim.y - G;
+  auto gather = [&](size_t rec) {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int hd = 0; hd < G; ++hd) {
+      const float4 y = *(const float4*)(a.wsum + (rec * G + hd) * 4);
+      const float f = ex2(a.wmax[rec * G + hd] - tot_m[hd]) * tot_r[hd];
+      x.x += y.x * f;
+      x.y += y.y * f;
+      x.z += y.z * f;
+      x.w += y.w * f;
+    }
+    return x;
+  };
+  for (int p = slice * MT + threadIdx.x; p < sg.pages; p += slices * MT) {
+    const float4 x = gather(at + p);
+    float4* dst = (float4*)(w + KV8_RING_BLOCKS) + p;
+    float4 v = *dst;
+    const int nb = sg.H / KV8_BLK - p * KV8_PAGE_BLOCKS;
+    v.x = fmaf(v.x, a.decay, x.x);
+    if (nb > 1) v.y = fmaf(v.y, a.decay, x.y);
+    if (nb > 2) v.z = fmaf(v.z, a.decay, x.z);
+    if (nb > 3) v.w = fmaf(v.w, a.decay, x.w);
+    *dst = v;
+  }
+  if (slice == 0 && threadIdx.x < KV8_RING_UNITS) {
+    const int r = threadIdx.x;
+    const int n0 = kv8_ring_held(sg.L, sg.H, 2 * r), n1 = kv8_ring_held(sg.L, sg.H, 2 * r + 1);
+    if (n0 || n1) {
+      const float4 x = gather(at + cv.max_pages_per_req + r);
+      if (n0) w[2 * r] = fmaf(w[2 * r], a.decay, x.x);
+      if (n1) w[2 * r + 1] = fmaf(w[2 * r + 1], a.decay, x.y);
+    }
+  }
+}
+
+template <int TYPE, bool WEIGHTS>
+cudaError_t launch_main(const Kv8Decode& a, cudaStream_t st) {
+  const int smem = decode_smem(a.B, a.cv.G).total;
+  static int limit[MAX_DEVICES];
+  const cudaError_t e = raise_smem_limit(kv8_decode_kernel<TYPE, WEIGHTS>, limit, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv8_decode_kernel<TYPE, WEIGHTS>, dim3(a.grid), dim3(KW * 32), smem, st, a);
+}
+
+}  // namespace
+
+int kv8_decode_requests(int batch, int Hkv, int G, int max_pages, bool weights) {
+  size_t n = KV8_MAX_REQUESTS;
+  if (weights) n = KV8_SCRATCH_AIM / ((size_t)Hkv * (max_pages + KV8_RING_UNITS) * G * 20);
+  if (n < 1) n = 1;
+  if (n > KV8_MAX_REQUESTS) n = KV8_MAX_REQUESTS;
+  return (size_t)batch < n ? batch : (int)n;
+}
+
+Kv8Scratch kv8_decode_scratch(int B, int Hkv, int G, int max_pages, bool weights, int grid) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const size_t recs = weights ? (size_t)B * Hkv * (max_pages + KV8_RING_UNITS) * G : 0;
+  Kv8Scratch s;
+  s.off_wsum = up(((size_t)grid + (size_t)B * Hkv) * G * PART_STRIDE * 4);
+  s.off_wmax = s.off_wsum + up(recs * 16);
+  s.total = s.off_wmax + up(recs * 4);
+  return s;
+}
+
+cudaError_t launch_kv8_decode(const Kv8Decode& a, int type, cudaStream_t st, Profiler* prof) {
+  prof_begin(prof, OSCAR_KERNEL_KV8_DECODE, st);
+  cudaError_t e;
+  if (type == OSCAR_KV8_E4M3)
+    e = a.weights ? launch_main<OSCAR_KV8_E4M3, true>(a, st) : launch_main<OSCAR_KV8_E4M3, false>(a, st);
+  else
+    e = a.weights ? launch_main<OSCAR_KV8_INT8, true>(a, st) : launch_main<OSCAR_KV8_INT8, false>(a, st);
+  prof_end(prof, OSCAR_KERNEL_KV8_DECODE, st);
+  if (e != cudaSuccess) return e;
+  const int segs = a.B * a.cv.Hkv;
+  int slices = 0;
+  if (a.weights) {
+    slices = (2 * a.grid + segs - 1) / segs;
+    const int most = (a.cv.max_pages_per_req + MT - 1) / MT;
+    if (slices > most) slices = most;
+  }
+  prof_begin(prof, OSCAR_KERNEL_KV8_MERGE, st);
+  e = launch_pdl(kv8_merge_kernel, dim3(segs, a.cv.G + slices), dim3(MT), 0, st, a);
+  prof_end(prof, OSCAR_KERNEL_KV8_MERGE, st);
+  return e;
+}
+
+}  // namespace oscar

@@ -52,6 +52,9 @@ OPT_WAIT_POLLS = 4  # poll budget of each history page's first wait in the decod
 OPT_DECODE_PARTITION = 5  # 0 automatic, 1 item list, 2 balanced
 PARTITION_AUTO, PARTITION_ITEMS, PARTITION_BALANCED = 0, 1, 2
 WAIT_POLLS_DEFAULT = 1 << 22
+KV8_BLOCK = 16  # tokens per scale block of a cache with 8-bit history
+KV8_E4M3 = 0
+KV8_INT8 = 1
 
 
 class OscarError(RuntimeError):
@@ -71,6 +74,11 @@ class oscar_layout_info(ctypes.Structure):
         "int2_head_bytes", "int2_page_bytes", "off_k_codes", "off_v_codes", "off_k_sz", "off_v_sz",
         "bf16_head_bytes", "bf16_page_bytes", "sink_bytes", "ring_bytes", "decode_scratch_bytes",
         "prefill_scratch_bytes")]
+
+
+class oscar_kv8_layout_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in (
+        "head_bytes", "page_bytes", "off_scales", "weights_floats", "scratch_bytes")]
 
 
 class oscar_cache(ctypes.Structure):
@@ -107,6 +115,14 @@ _SIGS = {
                                    ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
     "oscar_import_bf16_history": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_void_p,
                                    ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_layout_kv8": ([ctypes.POINTER(oscar_config), ctypes.POINTER(oscar_kv8_layout_info)], ctypes.c_int),
+    "oscar_append_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                          ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_decode_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
+                          ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_evict_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                         ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
     "oscar_quantize_rotated_f32": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "oscar_debug_rotate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
@@ -154,8 +170,13 @@ KERNEL_STEP = 5
 KERNEL_PREFILL_PREP = 6
 KERNEL_PREFILL_ATTN = 7
 KERNEL_PREFILL_MERGE = 8
+KERNEL_KV8_APPEND = 9
+KERNEL_KV8_DECODE = 10
+KERNEL_KV8_MERGE = 11
+KERNEL_KV8_EVICT = 12
 KERNEL_NAMES = {0: "append", 1: "import", 2: "decode_prep", 3: "decode_main", 4: "decode_merge", 5: "step_append_prep",
-                6: "prefill_prep", 7: "prefill_attn", 8: "prefill_merge"}
+                6: "prefill_prep", 7: "prefill_attn", 8: "prefill_merge", 9: "kv8_append", 10: "kv8_decode",
+                11: "kv8_merge", 12: "kv8_evict"}
 
 
 def exported_symbols():
@@ -490,6 +511,80 @@ def oscar_import_bf16_history(ctx, cache: dict, K, V, batch, n, stream=None):
            "oscar_import_bf16_history")
 
 
+def oscar_layout_kv8(cfg: oscar_config) -> oscar_kv8_layout_info:
+    info = oscar_kv8_layout_info()
+    _check(lib().oscar_layout_kv8(ctypes.byref(cfg), ctypes.byref(info)), "oscar_layout_kv8")
+    return info
+
+
+def oscar_append_kv8(ctx, cache: dict, kv_type, k_new, v_new, T, batch, weights=None, stream=None):
+    """T tokens per request (k_new, v_new [batch][T][Hkv][128]) into a cache with
+    8-bit history: a decode step, a chunk, or a prompt into an empty request."""
+    cs = _cache_struct(cache)
+    _check(lib().oscar_append_kv8(ctx, ctypes.byref(cs), kv_type, _ptr(k_new), _ptr(v_new), T, _ptr(weights), batch,
+                                  _stream(stream)), "oscar_append_kv8")
+
+
+def oscar_decode_kv8(ctx, cache: dict, kv_type, q, out, lse, scratch, batch, weights=None, decay=1.0, stream=None):
+    """Decode attention over a cache with 8-bit history; with `weights` also
+    weights = decay * weights + each block's attention weight."""
+    cs = _cache_struct(cache)
+    _check(lib().oscar_decode_kv8(ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(out), _ptr(lse), _ptr(weights), decay,
+                                  _ptr(scratch), scratch.numel() * scratch.element_size(), batch, _stream(stream)),
+           "oscar_decode_kv8")
+
+
+def oscar_evict_kv8(ctx, cache: dict, weights, budget, scratch, batch, stream=None):
+    """Drops the history blocks with the smallest weights, 256 tokens at a time,
+    until at most budget + 255 history tokens are left per request."""
+    cs = _cache_struct(cache)
+    _check(lib().oscar_evict_kv8(ctx, ctypes.byref(cs), _ptr(weights), budget, _ptr(scratch),
+                                 scratch.numel() * scratch.element_size(), batch, _stream(stream)), "oscar_evict_kv8")
+
+
+def bind_append_kv8(ctx, cache: dict, kv_type, T, batch, weights=None, stream=None):
+    """oscar_append_kv8 with everything but the new tokens marshalled once:
+    returns f(k_new_ptr, v_new_ptr) taking raw addresses (ints)."""
+    cs = _cache_struct(cache)
+    csr, w, st, fn = ctypes.byref(cs), _ptr(weights), _stream(stream), lib().oscar_append_kv8
+
+    def call(k_ptr: int, v_ptr: int):
+        _check(fn(ctx, csr, kv_type, k_ptr, v_ptr, T, w, batch, st), "oscar_append_kv8")
+
+    call._keep = cs
+    return call
+
+
+def bind_decode_kv8(ctx, cache: dict, kv_type, q, out, lse, scratch, batch, weights=None, decay=1.0, stream=None):
+    """oscar_decode_kv8 with every argument marshalled once: returns a
+    no-argument callable."""
+    cs = _cache_struct(cache)
+    args = (ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(out), _ptr(lse), _ptr(weights), decay, _ptr(scratch),
+            scratch.numel() * scratch.element_size(), batch, _stream(stream))
+    fn = lib().oscar_decode_kv8
+
+    def call():
+        _check(fn(*args), "oscar_decode_kv8")
+
+    call._keep = cs
+    return call
+
+
+def bind_evict_kv8(ctx, cache: dict, weights, budget, scratch, batch, stream=None):
+    """oscar_evict_kv8 with every argument marshalled once: returns a
+    no-argument callable."""
+    cs = _cache_struct(cache)
+    args = (ctx, ctypes.byref(cs), _ptr(weights), budget, _ptr(scratch), scratch.numel() * scratch.element_size(),
+            batch, _stream(stream))
+    fn = lib().oscar_evict_kv8
+
+    def call():
+        _check(fn(*args), "oscar_evict_kv8")
+
+    call._keep = cs
+    return call
+
+
 def oscar_quantize_rotated_f32(x, group_size, clip, which, codes, sz, stream=None):
     _check(lib().oscar_quantize_rotated_f32(_ptr(x), x.shape[0], group_size, float(clip), which, _ptr(codes),
                                             _ptr(sz), _stream(stream)), "oscar_quantize_rotated_f32")
@@ -540,12 +635,16 @@ def oscar_profile_read(ctx, kernel_id: int, reset: bool = False):
 
 
 # ---------------------------------------------------------------- plumbing
-def alloc_cache(cfg: oscar_config, device="cuda", bf16_history=False, zero=True):
-    """Device buffers of one layer's cache (torch allocations, caller-owned)."""
+def alloc_cache(cfg: oscar_config, device="cuda", bf16_history=False, zero=True, kv8=False):
+    """Device buffers of one layer's cache (torch allocations, caller-owned);
+    the history is INT2, BF16 or (kv8) 8-bit."""
     import torch
 
-    info = oscar_layout(cfg)
-    page_bytes = info.bf16_page_bytes if bf16_history else info.int2_page_bytes
+    if kv8:
+        page_bytes = oscar_layout_kv8(cfg).page_bytes
+    else:
+        info = oscar_layout(cfg)
+        page_bytes = info.bf16_page_bytes if bf16_history else info.int2_page_bytes
     mk = torch.zeros if zero else torch.empty
     B, Hkv = cfg.max_batch, cfg.num_kv_heads
     return {
@@ -566,3 +665,19 @@ def alloc_scratch(cfg: oscar_config, device="cuda", prefill=False):
     info = oscar_layout(cfg)
     n = info.prefill_scratch_bytes if prefill else info.decode_scratch_bytes
     return torch.empty((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
+
+
+def alloc_scratch_kv8(cfg: oscar_config, device="cuda"):
+    """Working memory of oscar_decode_kv8 and oscar_evict_kv8 (one at a time)."""
+    import torch
+
+    n = oscar_layout_kv8(cfg).scratch_bytes
+    return torch.empty((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
+
+
+def alloc_weights_kv8(cfg: oscar_config, device="cuda"):
+    """Block weights of one layer's cache, all 0."""
+    import torch
+
+    n = oscar_layout_kv8(cfg).weights_floats
+    return torch.zeros(cfg.max_batch, cfg.num_kv_heads, n, dtype=torch.float32, device=device)

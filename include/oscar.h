@@ -480,6 +480,111 @@ oscar_status oscar_import_bf16_history(oscar_ctx* ctx, const oscar_cache* cache,
 oscar_status oscar_append_bf16_history(oscar_ctx* ctx, const oscar_cache* cache, const void* k_new,
                                        const void* v_new, int batch, oscar_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Cache with 8-bit history.  The pages compare INT2 history with BF16 history
+ * only; this is the library's own point between the two: half the bytes of
+ * BF16 at the accuracy of 8 bits, without rotation or calibration, and with an
+ * eviction that keeps a request's history at a budget.  Three calls share one
+ * cache: oscar_append_kv8 writes it, oscar_decode_kv8 attends over it (and adds
+ * up how much weight each block got), oscar_evict_kv8 drops the blocks with
+ * the least.
+ *
+ * Regions and windows are those of the other caches, oscar_cache with a pool of
+ * 8-bit pages, but history moves in blocks of OSCAR_KV8_BLOCK = 16 tokens: when
+ * the recent window would exceed 256 tokens its oldest whole blocks, as many as
+ * needed, go to the history.  So hist_lens[b] is a multiple of 16, and a full
+ * window holds 241 to 256 tokens.  Position p >= 64 + hist_lens[b] of a request
+ * lives in ring slot (p - 64) % 256 as elsewhere.
+ *
+ * Each block has one fp32 scale per KV head for its keys and one for its
+ * values, s = max(max|x|, 2^-100) / qmax, and codes c = x / s rounded to the
+ * nearest value of the type, ties to even, exactly (of x·qmax / max|x|, not of
+ * a rounded quotient); x is read back as c·s.  A block that holds an infinity
+ * or NaN has the scale NaN: every output that sees it is NaN.
+ *   OSCAR_KV8_E4M3: qmax = 448, c an e4m3 floating-point number;
+ *   OSCAR_KV8_INT8: qmax = 127, c a signed integer, -127 .. 127.
+ *
+ * Page = num_kv_heads parts of 16416 B, one per KV head: 4 blocks of
+ *   [K codes 2048 B][V codes 2048 B], then 4 x (K scale, V scale) fp32.
+ *   Byte 512c + 16(4g + q) + 8s + 4h + 2r + l of a block's codes is
+ *     K: token 8r + g,      channel 32c + 8q + 4s + 2h + l
+ *     V: token 8h + 2q + l, channel 16g + 4c + 2s + r
+ *   (c, q < 4; g < 8; s, h, r, l < 2).
+ *
+ * Block weights (optional): float [max_batch][num_kv_heads]
+ *   [16 + 4 max_pages_per_req], 16-byte aligned.  Entry i < 16 belongs to the
+ *   16 tokens in ring slots 16i .. 16i + 15, entry 16 + j to history block j.
+ *   The sink has none (it is never evicted).  A new block starts at 0, and a
+ *   block that goes to the history takes its entry along.  Entries of blocks
+ *   that hold no token are not used.
+ *
+ * Pages of a request that is appended to or evicted from must not be shared
+ * with another request.  The context's device must be the current device
+ * (OSCAR_ERR_INVALID_ARG otherwise).  A request whose lengths no append can
+ * have left (OSCAR_ERR_STATE) is left unchanged by the append and the eviction
+ * and counts as empty in the decode.  Rows from `batch` on are not touched. */
+#define OSCAR_KV8_BLOCK 16
+
+typedef enum { OSCAR_KV8_E4M3 = 0, OSCAR_KV8_INT8 = 1 } oscar_kv8_type;
+
+typedef struct {
+  size_t head_bytes;     /* one KV head's part of a page (16416)             */
+  size_t page_bytes;     /* whole page                                       */
+  size_t off_scales;     /* offset of the scales inside a head's part        */
+  size_t weights_floats; /* block weights per (request, KV head)             */
+  size_t scratch_bytes;  /* scratch that oscar_decode_kv8 and oscar_evict_kv8
+                            need at most, any batch up to max_batch          */
+} oscar_kv8_layout_info;
+
+/* Sizes for a configuration (cfg->group_size is not used).  Host only. */
+oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* out);
+
+/* Append T tokens to every request b < batch: a decode step (T = 1), a chunk, or
+ * a whole prompt into an empty request, with the same result as T calls with
+ * one token each.
+ *   k_new, v_new : device bf16 [batch][T][num_kv_heads][128] (or pinned host
+ *                  memory, read in place); 0 <= T <= 2^24
+ *   type : an oscar_kv8_type, the same for the life of a cache
+ *   weights : block weights, or NULL
+ * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad page
+ * among those that take the blocks, or too many pages; the request is then
+ * left unchanged. */
+oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* k_new,
+                              const void* v_new, int T, float* weights, int batch, oscar_stream_t stream);
+
+/* Decode attention for one new query token per request over sink, 8-bit history
+ * and recent window.  q, out, lse, scratch and batch as in oscar_decode
+ * (scratch: oscar_layout_kv8's scratch_bytes; 256-byte aligned, no initial
+ * contents needed, not to be shared by calls that may overlap, also of two
+ * captured graphs).
+ *   weights : block weights, or NULL.  With w the softmax weights of a block's
+ *             16 tokens summed over them and over the KV head's query heads,
+ *             every block that holds a token gets  entry = decay·entry + w.
+ *   decay : finite, >= 0 (1: plain sums); not used without weights
+ * Requests with no token give zeros and lse = -inf, and their weights stay.
+ * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad page,
+ * whose tokens are left out (their blocks' weights only decay). */
+oscar_status oscar_decode_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, void* out,
+                              float* lse, float* weights, float decay, void* scratch, size_t scratch_bytes,
+                              int batch, oscar_stream_t stream);
+
+/* Evict history blocks by weight until a request b < batch has at most
+ * budget + 255 history tokens: e = floor((hist_lens[b] - budget) / 256)·16
+ * blocks of every KV head, those with the smallest weights of that head (the
+ * lower index first among equal ones; NaN counts as largest, a negative one as
+ * smallest).  e is a multiple of 16 so that the window keeps its ring slots.
+ * Then hist_lens[b] and seq_lens[b] are less by 16e, and the blocks that stay are
+ * the first hist_lens[b]/16 ones: blocks beyond move, codes, scales and weight,
+ * into the places that became free, in ascending order (attention does not
+ * depend on the order of the history; positions are in the keys).  Pages
+ * beyond ceil(hist_lens[b]/64) are the caller's again.
+ *   weights : block weights;  budget : tokens, >= 0
+ *   scratch : as for oscar_decode_kv8
+ * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a bad page in the
+ * history of a request to evict from; the request is then left unchanged. */
+oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* weights, int budget,
+                             void* scratch, size_t scratch_bytes, int batch, oscar_stream_t stream);
+
 /* Test hook: the demotion's quantiser and packer on given rotated fp32
  * vectors, so that codes and bytes can be compared bit for bit.
  *   x : device float [n][128] rotated channels
@@ -538,7 +643,11 @@ typedef enum {
   OSCAR_KERNEL_PREFILL_PREP = 6,  /* prefill: q rotation and scaling       */
   OSCAR_KERNEL_PREFILL_ATTN = 7,  /* prefill: split attention over regions */
   OSCAR_KERNEL_PREFILL_MERGE = 8, /* prefill: split merge + un-rotation    */
-  OSCAR_KERNEL_COUNT = 9
+  OSCAR_KERNEL_KV8_APPEND = 9,  /* 8-bit history: append                   */
+  OSCAR_KERNEL_KV8_DECODE = 10, /* 8-bit history: split attention          */
+  OSCAR_KERNEL_KV8_MERGE = 11,  /* 8-bit history: split merge, weights     */
+  OSCAR_KERNEL_KV8_EVICT = 12,  /* 8-bit history: selection and moves      */
+  OSCAR_KERNEL_COUNT = 13
 } oscar_kernel;
 
 oscar_status oscar_profile_enable(oscar_ctx* ctx, int enable);
