@@ -53,6 +53,15 @@ __device__ __forceinline__ Segment segment_of(const CacheView& cv, int b, bool* 
   return s;
 }
 
+// Shared memory: a ring of `stages` 16 KB stages that units are copied into
+// ahead of their use (a window row takes 272 bytes, so that the eight rows of a
+// fragment start in different banks), the barriers, the warps' results, pre.
+constexpr int WROW = D * 2 + 16;
+constexpr int STAGE_BYTES = 64 * WROW;  // 32 key rows and 32 value rows; a page needs 16416
+static_assert(STAGE_BYTES >= KV8_HEAD_BYTES && STAGE_BYTES % 128 == 0, "stage size");
+constexpr int MAX_STAGES = 13;
+constexpr int SMEM_LIMIT = 227 * 1024;
+
 // ------------------------------------------------------------------ the math
 struct State {
   float o[8][4];  // o^T: row tile j, channels 16gid + 2j (o[j][hc]) and + 1 (o[j][hc + 2]), head 2tq + hc
@@ -204,7 +213,8 @@ __device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], 
 }
 
 // A page's blocks 0 .. nb - 1 (the others hold nothing and are not looked at).
-template <int TYPE, bool WEIGHTS>
+// FULL: all four, with nothing between them that keeps their products in order.
+template <int TYPE, bool WEIGHTS, bool FULL>
 __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_t* page, int nb, int lane, int G,
                                           float* ws, float* wm) {
   const int gid = lane >> 2, tq = lane & 3;
@@ -213,7 +223,7 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
   for (int t = 0; t < 4; ++t) {
     s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
     lv[t] = 0.f;
-    if (t < nb) {
+    if (FULL || t < nb) {
       float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -237,7 +247,7 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
   softmax_step<4>(S, s, lv, p, sum);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    if (t < nb) {
+    if (FULL || t < nb) {
       const __half2 h0 = __floats2half2_rn(p[t][0], p[t][1]), h1 = __floats2half2_rn(p[t][2], p[t][3]);
       const uint32_t b0 = movmatrix_t(*(const uint32_t*)&h0), b1 = movmatrix_t(*(const uint32_t*)&h1);
 #pragma unroll
@@ -256,14 +266,14 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
   if (WEIGHTS) write_sums<4>(S, sum, ws, wm, G, gid, tq);
 }
 
-// 32 BF16 tokens at K and V (`stride` bytes from row to row), of which the
-// first n0 of the first 16 and the first n1 of the last 16 are there.  The
-// others may hold anything: their logits become -inf and their values 0.
+// 32 BF16 tokens at K and V (WROW bytes from row to row), of which the first n0
+// of the first 16 and the first n1 of the last 16 are there.  The others may
+// hold anything: their logits become -inf and their values 0.
 // The weights go into the product as two BF16 parts (16 bits together): the
 // newest tokens often carry most of the weight.
 template <bool WEIGHTS>
-__device__ __forceinline__ void window_step(State& S, const Query& Q, const uint8_t* K, const uint8_t* V, int stride,
-                                            int n0, int n1, int lane, int G, float* ws, float* wm) {
+__device__ __forceinline__ void window_step(State& S, const Query& Q, const uint8_t* K, const uint8_t* V, int n0, int n1,
+                                            int lane, int G, float* ws, float* wm) {
   const int gid = lane >> 2, tq = lane & 3;
   float s[2][4];
   const float lv[2] = {0.f, 0.f};
@@ -273,8 +283,8 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
     float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint4 x = *(const uint4*)(K + (16 * t + gid) * stride + 64 * c + 16 * tq);
-      const uint4 y = *(const uint4*)(K + (16 * t + 8 + gid) * stride + 64 * c + 16 * tq);
+      const uint4 x = *(const uint4*)(K + (16 * t + gid) * WROW + 64 * c + 16 * tq);
+      const uint4 y = *(const uint4*)(K + (16 * t + 8 + gid) * WROW + 64 * c + 16 * tq);
       mma_bf16(a, x.x, y.x, x.y, y.y, Q.w[c][0], Q.w[c][1]);
       mma_bf16(a, x.z, y.z, x.w, y.w, Q.w[c][2], Q.w[c][3]);
     }
@@ -300,7 +310,7 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int row = 8 * (u >> 1) + 2 * tq + (u & 1);
-      const uint4* src = (const uint4*)(V + (16 * t + row) * stride + 32 * gid);
+      const uint4* src = (const uint4*)(V + (16 * t + row) * WROW + 32 * gid);
       const uint4 x = src[0], y = src[1];
       const bool in = row < n;
       v[u][0] = in ? x.x : 0u, v[u][1] = in ? x.y : 0u, v[u][2] = in ? x.z : 0u, v[u][3] = in ? x.w : 0u;
@@ -314,20 +324,28 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
       mma_bf16(S.o[j], a0, a1, a2, a3, bl[0], bl[1]);
     }
   }
-  if (WEIGHTS) write_sums<2>(S, sum, ws, wm, G, gid, tq);
+  if (WEIGHTS && ws) write_sums<2>(S, sum, ws, wm, G, gid, tq);
 }
 
 // ------------------------------------------------------------------- decode
 struct DecodeSmem {
-  int off_pre, off_comb, total;
+  int stages, off_bar, off_issued, off_comb, off_pre, total;
 };
 __host__ __device__ inline DecodeSmem decode_smem(int B, int G) {
+  const int comb = KW * G * PART_STRIDE * 4, pre = (B + 1) * 8, fixed = 128 + 128 + comb + pre;
   DecodeSmem s;
-  s.off_pre = 0;
-  s.off_comb = (int)(((size_t)(B + 1) * 8 + 127) & ~(size_t)127);
-  s.total = s.off_comb + KW * G * (D + 4) * 4;
+  s.stages = (SMEM_LIMIT - fixed) / STAGE_BYTES;
+  if (s.stages > MAX_STAGES) s.stages = MAX_STAGES;
+  s.off_bar = s.stages * STAGE_BYTES;
+  s.off_issued = s.off_bar + 128;
+  s.off_comb = s.off_issued + 128;
+  s.off_pre = s.off_comb + comb;
+  s.total = s.off_pre + pre;
   return s;
 }
+// eight warps take the units in turn, so at least eight stages keep all of them busy
+static_assert((SMEM_LIMIT - 256 - KW * MAX_G * PART_STRIDE * 4 - (KV8_MAX_REQUESTS + 1) * 8) / STAGE_BYTES > KW,
+              "stages at the largest batch and group");
 
 // pre[b] = units of the requests before b, over all kv heads; pre[B] = all.
 __device__ inline void unit_prefix(const CacheView& cv, int B, long long* pre) {
@@ -356,84 +374,176 @@ __device__ inline void unit_prefix(const CacheView& cv, int B, long long* pre) {
   __syncthreads();
 }
 
+// A position in the work list.
+struct Cursor {
+  Segment sg;
+  int b, h, i;  // unit i of (b, h)
+};
+
+__device__ __forceinline__ void cursor_set(Cursor& c, const CacheView& cv, const long long* pre, int B, long long u) {
+  c.b = balanced_request(pre, B, u);
+  c.sg = segment_of(cv, c.b);
+  c.h = (int)((u - pre[c.b]) / c.sg.units);
+  c.i = (int)(u - pre[c.b] - (long long)c.h * c.sg.units);
+}
+
+// Forward by n units; the position must exist.
+__device__ __forceinline__ void cursor_forward(Cursor& c, const CacheView& cv, int n) {
+  c.i += n;
+  while (c.i >= c.sg.units) {
+    c.i -= c.sg.units;
+    if (++c.h == cv.Hkv) {
+      c.h = 0;
+      do c.sg = segment_of(cv, ++c.b);
+      while (c.sg.units == 0);
+    }
+  }
+}
+
+__device__ __forceinline__ int cursor_page(const Cursor& c, const CacheView& cv) {
+  const int pg = c.i - __popc(c.sg.win);
+  return pg < 0 ? 0 : cv.page_table[(size_t)c.b * cv.max_pages_per_req + pg];
+}
+
+// A warp starts the copy of the unit at c into a stage.
+__device__ __forceinline__ void issue_unit(const Cursor& c, const CacheView& cv, int pid, uint8_t* stage, uint64_t* bar,
+                                           int* issued, int lane) {
+  if (lane == 0) ++*issued;
+  if (c.i < __popc(c.sg.win)) {
+    const int unit = __fns(c.sg.win, 0, c.i + 1);
+    const size_t seg = (size_t)c.b * cv.Hkv + c.h;
+    const size_t row = unit < 2 ? seg * SINK + 32 * unit : seg * RECENT + 32 * (unit - 2);
+    if (lane == 0) mbar_expect_tx(bar, 64 * D * 2);
+    __syncwarp();
+    bulk_g2s(stage + lane * WROW, (unit < 2 ? cv.sink_k : cv.ring_k) + (row + lane) * D, D * 2, bar);
+    bulk_g2s(stage + (32 + lane) * WROW, (unit < 2 ? cv.sink_v : cv.ring_v) + (row + lane) * D, D * 2, bar);
+  } else if (lane == 0) {
+    if (pid >= 0 && pid < cv.num_pages) {
+      mbar_expect_tx(bar, KV8_HEAD_BYTES);
+      bulk_g2s_hint(stage, kv8_head(cv, pid, c.h), KV8_HEAD_BYTES, bar, l2_evict_first_policy());
+    } else {
+      record_error(cv.err, pid < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+      mbar_expect_tx(bar, 0);
+    }
+  }
+}
+
+// Waits until the copy number `use` (from 0) into a stage has arrived.  A
+// barrier tells apart only odd and even phases, and the warp that waits may be
+// one whole turn of the ring ahead of the copy before: it first waits until its
+// own copy has been started, which is after the one before was read.
+__device__ __forceinline__ bool wait_unit(uint64_t* bar, const int* issued, int use, int polls) {
+  for (int it = 0; *(const volatile int*)issued <= use; ++it)
+    if (it >= polls) return false;
+  return mbar_wait(bar, use & 1, polls);
+}
+
+// One persistent CTA per SM.  Unit i of its range goes to warp i % 8 and
+// through stage i % stages; the warp that has read a stage starts the copy
+// that comes into it next, whoever will read that, so a stage needs no barrier
+// that says it is free.  Each warp keeps a softmax state of its own over its
+// units of a (request, kv head); they are joined when the CTA is through with
+// it.
 template <int TYPE, bool WEIGHTS>
 __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheView& cv = a.cv;
   const DecodeSmem SL = decode_smem(a.B, cv.G);
+  const int NS = SL.stages;
+  uint64_t* bars = (uint64_t*)(smem + SL.off_bar);
+  int* issued = (int*)(smem + SL.off_issued);  // copies started into each stage; [MAX_STAGES]: a wait ran out
   long long* pre = (long long*)(smem + SL.off_pre);
-  float* comb = (float*)(smem + SL.off_comb);  // [warp][head][m, l, M, -, o]
+  float* comb = (float*)(smem + SL.off_comb);  // [warp][head] partial records
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tq = lane & 3;
   const int G = cv.G, Hkv = cv.Hkv, B = a.B;
+  if (threadIdx.x <= MAX_STAGES) {
+    issued[threadIdx.x] = 0;
+    if (threadIdx.x < NS) mbar_init(&bars[threadIdx.x], 1);
+  }
+  fence_proxy_async();
   pdl_launch_dependents();
   pdl_wait();
-  unit_prefix(cv, B, pre);
+  unit_prefix(cv, B, pre);  // (its barriers also order the ones above)
   const long long W = pre[B];
   const long long n = W < a.grid ? W : a.grid;
   if (blockIdx.x >= n) return;
-  long long u = blockIdx.x * W / n;
-  const long long end = (blockIdx.x + 1) * W / n;
-  int b = balanced_request(pre, B, u);
-  Segment sg = segment_of(cv, b);
-  int h = (int)((u - pre[b]) / sg.units);
-  while (u < end) {  // u: the first unit of (b, h) in this CTA's range
-    const long long s0 = pre[b] + (long long)h * sg.units;
-    const int lo = (int)(u - s0), hi = (int)((end - s0) < sg.units ? end - s0 : sg.units);
-    const int nwin = __popc(sg.win);
-    const int seg = b * Hkv + h;
+  const long long u0 = blockIdx.x * W / n;
+  const int count = (int)((blockIdx.x + 1) * W / n - u0);  // units of this CTA
+  // the warp's next unit to copy, and its page
+  Cursor ic;
+  int next = warp, pid = 0;
+  if (next < count) {
+    cursor_set(ic, cv, pre, B, u0 + next);
+    pid = cursor_page(ic, cv);
+  }
+  auto issue_next = [&](int stage, int step) {  // then moves on by `step` units
+    if (next < count) {
+      issue_unit(ic, cv, pid, smem + stage * STAGE_BYTES, &bars[stage], &issued[stage], lane);
+      next += step;
+      if (next < count) {
+        cursor_forward(ic, cv, step);
+        pid = cursor_page(ic, cv);
+      }
+    }
+  };
+  const bool two = warp + KW < NS;  // the warp fills two stages at the start
+  issue_next(warp, two ? KW : NS);
+  if (two) issue_next(warp + KW, NS - KW);
+
+  Cursor c;
+  cursor_set(c, cv, pre, B, u0);
+  int first = 0;           // this CTA's first unit of (c.b, c.h)
+  int mine = warp;         // this warp's next unit, its stage and the copies into that before it
+  int stage = warp, use = 0;
+  while (first < count) {
+    const int lo = c.i, len = min(count - first, c.sg.units - lo);
+    const int nwin = __popc(c.sg.win), seg = c.b * Hkv + c.h;
     State S;
     state_clear(S);
     Query Q;
     bool fp16 = false;
-    query_load(Q, a.q + ((size_t)b * cv.Hq + (size_t)h * G) * D, G, gid, tq);
-    for (int i = lo + warp; i < hi; i += KW) {
+    query_load(Q, a.q + ((size_t)c.b * cv.Hq + (size_t)c.h * G) * D, G, gid, tq);
+    for (; mine < first + len; mine += KW) {
+      const int i = lo + mine - first;
+      if (!__all_sync(0xffffffffu, wait_unit(&bars[stage], &issued[stage], use, a.wait_polls))) {
+        if (lane == 0) {
+          record_error(cv.err, OSCAR_ERR_TIMEOUT);
+          issued[MAX_STAGES] = 1;
+        }
+        break;
+      }
+      const uint8_t* st = smem + stage * STAGE_BYTES;
       if (i < nwin) {
-        const int unit = __fns(sg.win, 0, i + 1);
+        const int unit = __fns(c.sg.win, 0, i + 1), r = unit - 2;
         const bool sink = unit < 2;
-        const int r = unit - 2;
-        const uint8_t *K, *V;
-        int n0, n1;
-        if (sink) {
-          K = (const uint8_t*)(cv.sink_k + ((size_t)seg * SINK + 32 * unit) * D);
-          V = (const uint8_t*)(cv.sink_v + ((size_t)seg * SINK + 32 * unit) * D);
-          n0 = min(max(sg.L - 32 * unit, 0), 16);
-          n1 = min(max(sg.L - 32 * unit - 16, 0), 16);
-        } else {
-          K = (const uint8_t*)(cv.ring_k + ((size_t)seg * RECENT + 32 * r) * D);
-          V = (const uint8_t*)(cv.ring_v + ((size_t)seg * RECENT + 32 * r) * D);
-          n0 = kv8_ring_held(sg.L, sg.H, 2 * r);
-          n1 = kv8_ring_held(sg.L, sg.H, 2 * r + 1);
-        }
-        float *ws = nullptr, *wm = nullptr;
-        if (WEIGHTS && !sink) {
-          const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + cv.max_pages_per_req + r;
-          ws = a.wsum + at * G * 4;
-          wm = a.wmax + at * G;
-        }
-        if (WEIGHTS && !sink) window_step<true>(S, Q, K, V, D * 2, n0, n1, lane, G, ws, wm);
-        else window_step<false>(S, Q, K, V, D * 2, n0, n1, lane, G, ws, wm);
+        const int n0 = sink ? min(max(c.sg.L - 32 * unit, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r);
+        const int n1 = sink ? min(max(c.sg.L - 32 * unit - 16, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r + 1);
+        const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + cv.max_pages_per_req + r;
+        window_step<WEIGHTS>(S, Q, st, st + 32 * WROW, n0, n1, lane, G, sink ? nullptr : a.wsum + at * G * 4,
+                             a.wmax + at * G);
       } else {
         if (!fp16) query_to_fp16(Q, tq);
         fp16 = true;
         const int pg = i - nwin;
-        const int pid = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
-        float *ws = nullptr, *wm = nullptr;
-        if (WEIGHTS) {
-          const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + pg;
-          ws = a.wsum + at * G * 4;
-          wm = a.wmax + at * G;
+        const int id = cv.page_table[(size_t)c.b * cv.max_pages_per_req + pg];
+        const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + pg;
+        float *ws = a.wsum + at * G * 4, *wm = a.wmax + at * G;
+        if (id >= 0 && id < cv.num_pages) {
+          const int nb = c.sg.H / KV8_BLK - pg * KV8_PAGE_BLOCKS;
+          if (nb >= KV8_PAGE_BLOCKS) page_step<TYPE, WEIGHTS, true>(S, Q, st, KV8_PAGE_BLOCKS, lane, G, ws, wm);
+          else page_step<TYPE, WEIGHTS, false>(S, Q, st, nb, lane, G, ws, wm);
+        } else if (WEIGHTS && lane < G) {  // its tokens are left out
+          *(float4*)(ws + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
+          wm[lane] = -INFINITY;
         }
-        if (pid < 0 || pid >= cv.num_pages) {  // its tokens are left out
-          if (lane == 0) record_error(cv.err, pid < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
-          if (WEIGHTS && lane < G) {
-            *(float4*)(ws + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
-            wm[lane] = -INFINITY;
-          }
-          continue;
-        }
-        const int nb = min(KV8_PAGE_BLOCKS, sg.H / KV8_BLK - pg * KV8_PAGE_BLOCKS);
-        page_step<TYPE, WEIGHTS>(S, Q, kv8_head(cv, pid, h), nb, lane, G, ws, wm);
+      }
+      __syncwarp();  // the stage has been read: the next copy may come into it
+      issue_next(stage, KW);
+      stage += KW;
+      if (stage >= NS) {
+        stage -= NS;
+        ++use;
       }
     }
     // join the warps
@@ -444,21 +554,22 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
       S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 16);
       const int hd = 2 * tq + hc;
       if (hd < G) {
-        float* c = comb + (warp * G + hd) * PART_STRIDE;
+        float* x = comb + (warp * G + hd) * PART_STRIDE;
         if (gid == 0) {
-          c[REC_M] = S.m[hc];
-          c[REC_L] = S.l[hc];
-          c[REC_T] = S.M[hc];
+          x[REC_M] = S.m[hc];
+          x[REC_L] = S.l[hc];
+          x[REC_T] = S.M[hc];
         }
 #pragma unroll
         for (int j = 0; j < 8; j += 2)
-          *(float4*)(c + PART_O + 16 * gid + 2 * j) = make_float4(S.o[j][hc], S.o[j][hc + 2], S.o[j + 1][hc], S.o[j + 1][hc + 2]);
+          *(float4*)(x + PART_O + 16 * gid + 2 * j) = make_float4(S.o[j][hc], S.o[j][hc + 2], S.o[j + 1][hc], S.o[j + 1][hc + 2]);
       }
     }
     __syncthreads();
+    if (issued[MAX_STAGES]) break;
     float* rec = a.part + ((size_t)blockIdx.x + seg) * G * PART_STRIDE;
     for (int e = threadIdx.x; e < G * D; e += KW * 32) {
-      const int hd = e / D, c = e % D;
+      const int hd = e / D, ch = e % D;
       float m = -INFINITY, M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
@@ -471,24 +582,23 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
         const float* x = comb + (w * G + hd) * PART_STRIDE;
         if (x[REC_M] == -INFINITY) continue;
         l += x[REC_L] * ex2(x[REC_M] - m);
-        o += x[PART_O + c] * ex2(x[REC_T] - M);
+        o += x[PART_O + ch] * ex2(x[REC_T] - M);
       }
       float* y = rec + hd * PART_STRIDE;
-      y[PART_O + c] = o;
-      if (c == 0) {
+      y[PART_O + ch] = o;
+      if (ch == 0) {
         y[REC_M] = m;
         y[REC_L] = l;
         y[REC_T] = M;
       }
     }
     __syncthreads();
-    u = s0 + hi;
-    if (u < end && ++h == Hkv) {
-      h = 0;
-      do sg = segment_of(cv, ++b);
-      while (sg.units == 0);
-    }
+    first += len;
+    if (first < count) cursor_forward(c, cv, len);
   }
+  // a wait ran out: no CTA leaves with a copy into its memory under way
+  if (issued[MAX_STAGES] && threadIdx.x < NS && issued[threadIdx.x])
+    mbar_wait(&bars[threadIdx.x], (issued[threadIdx.x] - 1) & 1);
 }
 
 // -------------------------------------------------------------------- merge

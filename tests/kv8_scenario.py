@@ -137,3 +137,56 @@ def check_decode(pair, q, out, lse, decay=None):
         assert (np.abs(ln[b] - rl) <= tl + 2.0 ** -22 * np.abs(rl)).all(), (b, r.L)
         worst = max(worst, float(dp.max()))
     return worst
+
+
+def dense(pair, b, h):
+    """(K, V) [L][128] in float64 of a request's head from the device state itself (for long requests)."""
+    L, H = int(pair.cache["seq_lens"][b]), int(pair.cache["hist_lens"][b])
+    heads = pair.cache["pool"].view(-1, pair.Hkv, K8.HEAD_BYTES)[pair.cache["page_table"][b, :-(-H // 64)].long(), h]
+    raw = heads[:, :16384].reshape(-1, 2, 2048)[:H // 16]
+    scale = heads[:, 16384:].contiguous().view(torch.float32).view(-1, 2)[:H // 16].double()
+    values = torch.from_numpy(K8.decode(np.arange(256, dtype=np.uint8), pair.kind)).cuda()
+    out = []
+    for side, x in enumerate("kv"):
+        y = torch.empty(H // 16, 2048, dtype=torch.float64, device="cuda")
+        y[:, torch.from_numpy(K8.PLACE[side]).cuda()] = values[raw[:, side].long()] * scale[:, side, None]
+        win = pair.cache["ring_" + x][b, h].double().roll(-(H % 256), 0)[:max(0, L - 64 - H)]
+        out.append(torch.cat([pair.cache["sink_" + x][b, h, :L].double(), y.view(-1, 128), win]))
+    return out
+
+
+def check_decode_dense(pair, q, out, lse, weights_before=None, decay=1.0):
+    """As check_decode, from the device state: for requests too long for the oracle."""
+    G = pair.G
+    qd = q.cuda().double().view(pair.B, pair.Hkv, G, 128)
+    od, ld = out.double().view(pair.B, pair.Hkv, G, 128), lse.double().view(pair.B, pair.Hkv, G)
+    for b in range(pair.B):
+        L, H = int(pair.cache["seq_lens"][b]), int(pair.cache["hist_lens"][b])
+        if L == 0:
+            assert bool((od[b] == 0).all()) and bool(torch.isneginf(ld[b]).all())
+            continue
+        for h in range(pair.Hkv):
+            K, V = dense(pair, b, h)
+            z = qd[b, h] @ K.T / 128 ** 0.5
+            p = torch.softmax(z, 1)
+            ref, rl = p @ V, torch.logsumexp(z, 1)
+            ds = 2.0 ** -16 * (qd[b, h].abs() @ K.abs().T).amax(1, keepdim=True) / 128 ** 0.5 + 2.0 ** -19
+            dp = 2 * ds + 2.0 ** -19
+            lim = (2.0 ** -11 + dp) * (p @ V.abs()) + L * 2.0 ** -25 * p.amax(1, keepdim=True) * V.abs().max()
+            lim = lim + 2.0 ** -8 * (ref.abs() + lim)
+            assert bool(((od[b, h] - ref).abs() <= lim).all()), (b, h, float(((od[b, h] - ref).abs() / lim).max()))
+            assert bool(((ld[b, h] - rl).abs() <= ds[:, 0] + 2.0 ** -19 + 2.0 ** -22 * rl.abs()).all()), (b, h)
+            if weights_before is not None:
+                t = p.sum(0)
+                want = weights_before[b, h].double().clone()
+                at = slice(16, 16 + H // 16)
+                want[at] = want[at] * decay + t[min(L, 64):min(L, 64) + H].view(-1, 16).sum(1)
+                n = -(-max(0, L - 64 - H) // 16)
+                rest = torch.zeros(n * 16, dtype=torch.float64, device="cuda")
+                rest[:max(0, L - 64 - H)] = t[min(L, 64) + H:]
+                slots = (torch.arange(n, device="cuda") + H // 16) % 16
+                want[slots] = want[slots] * decay + rest.view(n, 16).sum(1)
+                got = pair.weights[b, h].double()
+                held = torch.cat([slots, torch.arange(16, 16 + H // 16, device="cuda")])
+                lim = float(dp.max()) * want + 2.0 ** -22 * want + 1e-12
+                assert bool(((got - want).abs() <= lim)[held].all()), (b, h)

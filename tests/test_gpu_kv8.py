@@ -9,7 +9,7 @@ from bit_kv_cache_int2_gb300 import oscar
 
 pytestmark = pytest.mark.gpu
 
-from kv8_scenario import Pair, check_decode  # noqa: E402
+from kv8_scenario import Pair, check_decode, check_decode_dense  # noqa: E402
 
 KINDS = [oscar.KV8_E4M3, oscar.KV8_INT8]
 
@@ -171,6 +171,34 @@ def test_decode_long_and_uneven(kind):
         out, lse = p.decode(q, 1.0)
         worst = check_decode(p, q, out, lse, 1.0)
         p.check_state(weight_tol=2 * worst)
+        ok(p)
+    finally:
+        p.close()
+
+
+@pytest.mark.parametrize("kind,Hkv,G,lens", [
+    (0, 1, 8, [200000]),             # over a thousand pages per CTA's turns of the stage ring
+    (1, 2, 4, [150000, 131071]),
+    (0, 8, 2, [40000, 100, 0, 70001, 65]),
+    (1, 8, 1, [3000] * 40),          # several requests per CTA
+    (0, 4, 4, [33] * 150 + [700] * 150),
+])
+def test_decode_many_units_per_cta(kind, Hkv, G, lens):
+    p = Pair(kind, Hkv, G, len(lens), max(1, -(-max(lens) // 64)), seed=G)
+    try:
+        for b, n in enumerate(lens):
+            if n == 0:
+                continue
+            g = torch.Generator(device="cuda").manual_seed(b)
+            k = torch.randn(1, n, Hkv, 128, device="cuda", generator=g).bfloat16()
+            v = torch.randn(1, n, Hkv, 128, device="cuda", generator=g).bfloat16()
+            row = {x: p.cache[x][b:b + 1] if x != "pool" else p.cache[x] for x in p.cache}
+            oscar.oscar_append_kv8(p.ctx, row, kind, k, v, n, 1, weights=p.weights[b:b + 1])
+        for decay in (1.0, 0.75):
+            before = p.weights.clone()
+            q = p.query(1.5)
+            out, lse = p.decode(q, decay)
+            check_decode_dense(p, q, out, lse, before, decay)
         ok(p)
     finally:
         p.close()
