@@ -165,7 +165,7 @@ __device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, in
 // With one CTA per request (SOLE) the CTA writes the lengths when all its
 // warps are done; else append_lengths_kernel does afterwards.
 template <int TYPE, bool SOLE>
-__global__ void __launch_bounds__(AW * 32) append_kernel(Kv8Append a) {
+__global__ void __launch_bounds__(AW * 32, SOLE ? 1 : 2) append_kernel(Kv8Append a) {
   pdl_launch_dependents();
   pdl_wait();
   const CacheView& cv = a.cv;
@@ -261,24 +261,21 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ int block_sum(int v, int* red) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return __reduce_add_sync(0xffffffffu, red[threadIdx.x & 31]);
-}
-
-// Number of set flags in lower threads of the block, and of all (ET threads).
-__device__ __forceinline__ int block_rank(bool flag, int* red, int* all) {
-  const uint32_t m = __ballot_sync(0xffffffffu, flag);
+// Sums of v over lower threads of the block (returned) and over all ET (*all).
+// `red` alternates between two arrays, so one barrier a call is enough.
+__device__ __forceinline__ int block_scan(int v, int* red, int* all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();
-  if (lane == 0) red[warp] = __popc(m);
+  int upto = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) red[warp] = upto;
   __syncthreads();
   const int n = red[lane];
   *all = __reduce_add_sync(0xffffffffu, n);
-  return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + __popc(m & ((1u << lane) - 1u));
+  return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + upto - v;
 }
 
 // The blocks of one (request, kv head) that go: the e smallest weights, the
@@ -286,7 +283,7 @@ __device__ __forceinline__ int block_rank(bool flag, int* red, int* all) {
 // place n - e move into the places below it that become free; both lists are
 // in ascending order and equally long.
 __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
-  __shared__ int red[32];
+  __shared__ int red[2][32], hist[2][256];
   pdl_launch_dependents();
   pdl_wait();
   const CacheView& cv = a.cv;
@@ -316,38 +313,70 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
   if (!e) return;
   const float* w = a.weights + (size_t)blockIdx.x * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) +
                    KV8_RING_BLOCKS;
-  // the e-th smallest key, bit by bit: the largest value with fewer than e keys below it
+  // the e-th smallest key, eight bits at a time: how many of the keys that agree
+  // with it so far have each next digit.  Lanes of a warp with the same digit
+  // count as one (weights often share their exponent).
+  const int lane = tid & 31;
   uint32_t cut = 0;
-  int below = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = cut | (1u << bit);
-    int s = 0;
-    for (int i = tid; i < n; i += ET) s += order_key(w[i]) < c;
-    s = block_sum(s, red);
-    if (s < e) {
-      cut = c;
-      below = s;
+  int want = e;  // the key's rank among those that agree, from 1
+  if (tid < 512) hist[tid >> 8][tid & 255] = 0;
+  __syncthreads();
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* hs = hist[pass & 1];
+    for (int i0 = 0; i0 < n; i0 += ET) {
+      const int i = i0 + tid;
+      const uint32_t key = i < n ? order_key(w[i]) : 0;
+      const bool in = i < n && (pass == 0 || (key >> (shift + 8)) == (cut >> (shift + 8)));
+      const uint32_t digit = in ? (key >> shift) & 255u : 256u;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&hs[digit], __popc(same));
+    }
+    __syncthreads();
+    // every warp finds the digit by itself: a lane adds up eight bins
+    int v[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[j] = hs[8 * lane + j];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
+    int below = upto - sum, digit = 8 * lane;
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      if (below + v[j] >= want) break;
+      below += v[j];
+      ++digit;
+    }
+    cut |= (uint32_t)__shfl_sync(0xffffffffu, digit, l) << shift;
+    want -= __shfl_sync(0xffffffffu, below, l);
+    // the next pass counts in the other array; this one is cleared for the pass after it
+    if (pass < 2) {
+      __syncthreads();
+      if (tid < 256) hs[tid] = 0;
     }
   }
-  const int equal_go = e - below, keep = n - e;
+  const int equal_go = want, keep = n - e;  // of the keys equal to it, so many go
   int32_t* holes = list + 4;
   int32_t* ends = holes + 2 * (size_t)cv.max_pages_per_req;
   int equal = 0, nh = 0, nm = 0;
   for (int i0 = 0; i0 < n; i0 += ET) {
     const int i = i0 + tid;
     const uint32_t key = i < n ? order_key(w[i]) : 0xffffffffu;
-    int all;
     const bool eq = i < n && key == cut;
-    const int rank = equal + block_rank(eq, red, &all);
+    int all;
+    const int rank = equal + block_scan(eq, red[0], &all);
     equal += all;
     const bool go = i < n && (key < cut || (eq && rank < equal_go));
     const bool hole = go && i < keep, end = i < n && !go && i >= keep;
-    const int hr = nh + block_rank(hole, red, &all);
-    nh += all;
-    if (hole) holes[hr] = i;
-    const int er = nm + block_rank(end, red, &all);
-    nm += all;
-    if (end) ends[er] = i;
+    const int r = block_scan((int)hole | (int)end << 16, red[1], &all);  // both counts at once
+    if (hole) holes[nh + (r & 0xffff)] = i;
+    if (end) ends[nm + (r >> 16)] = i;
+    nh += all & 0xffff;
+    nm += all >> 16;
   }
   if (tid == 0) list[0] = nh;
 }
@@ -365,22 +394,39 @@ __global__ void __launch_bounds__(256) evict_move_kernel(Kv8Evict a) {
   const int32_t* ends = holes + 2 * (size_t)cv.max_pages_per_req;
   const int32_t* pt = cv.page_table + (size_t)b * cv.max_pages_per_req;
   float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) + KV8_RING_BLOCKS;
-  const int lane = threadIdx.x & 31;
-  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < count; i += gridDim.y * 8) {
-    const int to = holes[i], from = ends[i];
-    uint8_t* tb = kv8_head(cv, pt[to / KV8_PAGE_BLOCKS], h);
-    const uint8_t* fb = kv8_head(cv, pt[from / KV8_PAGE_BLOCKS], h);
-    const int ts = to % KV8_PAGE_BLOCKS, fs = from % KV8_PAGE_BLOCKS;
+  const int lane = threadIdx.x & 31, step = gridDim.y * 8;
+  int i = blockIdx.y * 8 + (threadIdx.x >> 5);
+  int to = 0, from = 0, tp = 0, fp = 0;  // the move's blocks and pages, fetched one move ahead
+  auto fetch = [&](int k) {
+    if (k < count) {
+      to = holes[k];
+      from = ends[k];
+      tp = pt[to / KV8_PAGE_BLOCKS];
+      fp = pt[from / KV8_PAGE_BLOCKS];
+    }
+  };
+  fetch(i);
+  for (; i < count; i += step) {
+    const int t = to, f = from, ts = t % KV8_PAGE_BLOCKS, fs = f % KV8_PAGE_BLOCKS;
+    uint8_t* tb = kv8_head(cv, tp, h);
+    const uint8_t* fb = kv8_head(cv, fp, h);
     const uint4* src = (const uint4*)(fb + fs * KV8_BLOCK_BYTES) + lane;
     uint4* dst = (uint4*)(tb + ts * KV8_BLOCK_BYTES) + lane;
     uint4 x[KV8_BLOCK_BYTES / 512];
 #pragma unroll
     for (int j = 0; j < KV8_BLOCK_BYTES / 512; ++j) x[j] = src[32 * j];
+    fetch(i + step);
+    float2 scales;
+    float weight;
+    if (lane == 0) {
+      scales = ((const float2*)(fb + KV8_OFF_SCALES))[fs];
+      weight = w[f];
+    }
 #pragma unroll
     for (int j = 0; j < KV8_BLOCK_BYTES / 512; ++j) dst[32 * j] = x[j];
     if (lane == 0) {
-      ((float2*)(tb + KV8_OFF_SCALES))[ts] = ((const float2*)(fb + KV8_OFF_SCALES))[fs];
-      w[to] = w[from];
+      ((float2*)(tb + KV8_OFF_SCALES))[ts] = scales;
+      w[t] = weight;
     }
   }
   if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0 && list[1]) {
@@ -400,7 +446,7 @@ cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, int num_sms, 
     e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, true>, dim3(1, B), dim3(AW * 32), 0, st, a)
                                : launch_pdl(append_kernel<OSCAR_KV8_INT8, true>, dim3(1, B), dim3(AW * 32), 0, st, a);
   } else {
-    long long x = (4LL * num_sms + B - 1) / B;
+    long long x = (2LL * num_sms + B - 1) / B;  // CTAs that run at once
     if (x > ctas) x = ctas;
     const dim3 grid((unsigned)x, B);
     e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, false>, grid, dim3(AW * 32), 0, st, a)

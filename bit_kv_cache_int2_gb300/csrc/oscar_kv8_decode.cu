@@ -41,7 +41,7 @@ struct Segment {  // a request's share of the list, the same for each of its kv 
   uint32_t win;
 };
 
-__device__ __forceinline__ Segment segment_of(const CacheView& cv, int b, bool* ok = nullptr) {
+__device__ __forceinline__ Segment segment_of(const CacheView& cv, int b) {
   const Kv8Req r = kv8_req(cv, b);
   Segment s;
   s.L = r.L;
@@ -49,13 +49,12 @@ __device__ __forceinline__ Segment segment_of(const CacheView& cv, int b, bool* 
   s.win = window_units(r.L, r.H);
   s.pages = (r.H + PAGE - 1) / PAGE;
   s.units = s.pages + __popc(s.win);
-  if (ok) *ok = r.ok;
   return s;
 }
 
 // Shared memory: a ring of `stages` 16 KB stages that units are copied into
 // ahead of their use (a window row takes 272 bytes, so that the eight rows of a
-// fragment start in different banks), the barriers, the warps' results, pre.
+// fragment start in different banks), the barriers and the warps' results.
 constexpr int WROW = D * 2 + 16;
 constexpr int STAGE_BYTES = 64 * WROW;  // 32 key rows and 32 value rows; a page needs 16416
 static_assert(STAGE_BYTES >= KV8_HEAD_BYTES && STAGE_BYTES % 128 == 0, "stage size");
@@ -329,49 +328,39 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
 
 // ------------------------------------------------------------------- decode
 struct DecodeSmem {
-  int stages, off_bar, off_issued, off_comb, off_pre, total;
+  int stages, off_bar, off_issued, off_comb, total;
 };
-__host__ __device__ inline DecodeSmem decode_smem(int B, int G) {
-  const int comb = KW * G * PART_STRIDE * 4, pre = (B + 1) * 8, fixed = 128 + 128 + comb + pre;
-  DecodeSmem s;
-  s.stages = (SMEM_LIMIT - fixed) / STAGE_BYTES;
+__host__ __device__ constexpr DecodeSmem decode_smem(int G) {
+  const int comb = KW * G * PART_STRIDE * 4;
+  DecodeSmem s = {};
+  s.stages = (SMEM_LIMIT - 256 - comb) / STAGE_BYTES;
   if (s.stages > MAX_STAGES) s.stages = MAX_STAGES;
   s.off_bar = s.stages * STAGE_BYTES;
   s.off_issued = s.off_bar + 128;
   s.off_comb = s.off_issued + 128;
-  s.off_pre = s.off_comb + comb;
-  s.total = s.off_pre + pre;
+  s.total = s.off_comb + comb;
   return s;
 }
-// eight warps take the units in turn, so at least eight stages keep all of them busy
-static_assert((SMEM_LIMIT - 256 - KW * MAX_G * PART_STRIDE * 4 - (KV8_MAX_REQUESTS + 1) * 8) / STAGE_BYTES > KW,
-              "stages at the largest batch and group");
+// eight warps take the units in turn, so more than eight stages keep all of them busy
+static_assert(decode_smem(MAX_G).stages > KW, "stages at the largest group");
 
-// pre[b] = units of the requests before b, over all kv heads; pre[B] = all.
-__device__ inline void unit_prefix(const CacheView& cv, int B, long long* pre) {
-  for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    bool ok;
-    pre[b + 1] = (long long)segment_of(cv, b, &ok).units * cv.Hkv;
-    if (!ok && blockIdx.x == 0) record_error(cv.err, OSCAR_ERR_STATE);
+// Units of all requests and, in *before, of those before request b; over all
+// kv heads.  Every warp finds them by itself.
+__device__ __forceinline__ long long count_units(const CacheView& cv, int B, int b, long long* before) {
+  const int lane = threadIdx.x & 31;
+  long long all = 0, part = 0;
+  for (int i = lane; i < B; i += 32) {
+    const int x = segment_of(cv, i).units;
+    all += x;
+    if (i < b) part += x;
   }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    long long carry = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-      long long v = b0 + lane < B ? pre[b0 + lane + 1] : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      v += carry;
-      if (b0 + lane < B) pre[b0 + lane + 1] = v;
-      carry = __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) pre[0] = 0;
+  for (int o = 16; o; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    part += __shfl_xor_sync(0xffffffffu, part, o);
   }
-  __syncthreads();
+  *before = part * cv.Hkv;
+  return all * cv.Hkv;
 }
 
 // A position in the work list.
@@ -380,11 +369,30 @@ struct Cursor {
   int b, h, i;  // unit i of (b, h)
 };
 
-__device__ __forceinline__ void cursor_set(Cursor& c, const CacheView& cv, const long long* pre, int B, long long u) {
-  c.b = balanced_request(pre, B, u);
+// The cursor at unit u of the list (which has it); a whole warp calls it.
+__device__ __forceinline__ void cursor_set(Cursor& c, const CacheView& cv, int B, long long u) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const long long own = b0 + lane < B ? (long long)segment_of(cv, b0 + lane).units * cv.Hkv : 0;
+    long long upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t beyond = __ballot_sync(0xffffffffu, before + upto > u);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      c.b = b0 + l;
+      before += __shfl_sync(0xffffffffu, upto - own, l);
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
   c.sg = segment_of(cv, c.b);
-  c.h = (int)((u - pre[c.b]) / c.sg.units);
-  c.i = (int)(u - pre[c.b] - (long long)c.h * c.sg.units);
+  c.h = (int)((u - before) / c.sg.units);
+  c.i = (int)(u - before - (long long)c.h * c.sg.units);
 }
 
 // Forward by n units; the position must exist.
@@ -448,11 +456,10 @@ template <int TYPE, bool WEIGHTS>
 __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
   extern __shared__ __align__(128) uint8_t smem[];
   const CacheView& cv = a.cv;
-  const DecodeSmem SL = decode_smem(a.B, cv.G);
+  const DecodeSmem SL = decode_smem(cv.G);
   const int NS = SL.stages;
   uint64_t* bars = (uint64_t*)(smem + SL.off_bar);
   int* issued = (int*)(smem + SL.off_issued);  // copies started into each stage; [MAX_STAGES]: a wait ran out
-  long long* pre = (long long*)(smem + SL.off_pre);
   float* comb = (float*)(smem + SL.off_comb);  // [warp][head] partial records
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tq = lane & 3;
@@ -462,19 +469,22 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
     if (threadIdx.x < NS) mbar_init(&bars[threadIdx.x], 1);
   }
   fence_proxy_async();
-  pdl_launch_dependents();
+  __syncthreads();
   pdl_wait();
-  unit_prefix(cv, B, pre);  // (its barriers also order the ones above)
-  const long long W = pre[B];
+  pdl_launch_dependents();  // after the wait: what the merge reads before its own wait is there
+  long long none;
+  const long long W = count_units(cv, B, 0, &none);
   const long long n = W < a.grid ? W : a.grid;
   if (blockIdx.x >= n) return;
   const long long u0 = blockIdx.x * W / n;
   const int count = (int)((blockIdx.x + 1) * W / n - u0);  // units of this CTA
+  Cursor c;
+  cursor_set(c, cv, B, u0);
   // the warp's next unit to copy, and its page
-  Cursor ic;
+  Cursor ic = c;
   int next = warp, pid = 0;
   if (next < count) {
-    cursor_set(ic, cv, pre, B, u0 + next);
+    cursor_forward(ic, cv, warp);
     pid = cursor_page(ic, cv);
   }
   auto issue_next = [&](int stage, int step) {  // then moves on by `step` units
@@ -491,8 +501,6 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
   issue_next(warp, two ? KW : NS);
   if (two) issue_next(warp + KW, NS - KW);
 
-  Cursor c;
-  cursor_set(c, cv, pre, B, u0);
   int first = 0;           // this CTA's first unit of (c.b, c.h)
   int mine = warp;         // this warp's next unit, its stage and the copies into that before it
   int stage = warp, use = 0;
@@ -604,108 +612,88 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
 // -------------------------------------------------------------------- merge
 // grid (B Hkv, G + slices of the weights): CTA y < G writes the output of the
 // kv head's query head y, the others update a slice of the block weights.
+// What is in the records of a (request, kv head) follows from the lengths, so
+// it is worked out while the decode kernel still runs.
 __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
-  __shared__ long long sums[MT / 32][2];
-  __shared__ float wm[MT / 32], wl[MT / 32], wt[MT / 32];
   __shared__ __align__(16) float wo[MT / 32][D];
   __shared__ float tot_m[MAX_G], tot_r[MAX_G];
   const CacheView& cv = a.cv;
   const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv, G = cv.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  pdl_wait();
-  long long before = 0, all = 0;
-  for (int i = threadIdx.x; i < a.B; i += MT) {
-    const long long x = (long long)segment_of(cv, i).units * cv.Hkv;
-    all += x;
-    if (i < b) before += x;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if (lane == 0) {
-    sums[warp][0] = before;
-    sums[warp][1] = all;
-  }
-  __syncthreads();
-  before = all = 0;
-#pragma unroll
-  for (int w = 0; w < MT / 32; ++w) {
-    before += sums[w][0];
-    all += sums[w][1];
-  }
   const Segment sg = segment_of(cv, b);
+  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0 && !kv8_req(cv, b).ok) record_error(cv.err, OSCAR_ERR_STATE);
   Balanced bl;
-  bl.W = all;
-  bl.n = (int)(all < a.grid ? all : a.grid);
+  long long before;
+  bl.W = count_units(cv, a.B, b, &before);
+  bl.n = (int)(bl.W < a.grid ? bl.W : a.grid);
   bl.wch = 0;
   const long long s0 = before + (long long)h * sg.units;
-  int i0 = 0, i1 = -1;
+  int i0 = 0, n = 0;  // records i0 .. i0 + n - 1, one of each CTA that had a part
   if (sg.units) {
     i0 = balanced_owner(bl, s0);
-    i1 = balanced_owner(bl, s0 + sg.units - 1);
+    n = balanced_owner(bl, s0 + sg.units - 1) - i0 + 1;
   }
+  pdl_wait();
+  const float* recs = a.part + ((size_t)i0 + seg) * G * PART_STRIDE;
   if (blockIdx.y < G) {
-    const int hd = blockIdx.y;
-    float m = -INFINITY, l = 0.f, M = -INFINITY;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = i0 + warp; i <= i1; i += MT / 32) {
-      const float* r = a.part + (((size_t)i + seg) * G + hd) * PART_STRIDE;
-      const float4 x = *(const float4*)r;
-      if (x.x == -INFINITY) continue;
-      const float4 y = *(const float4*)(r + PART_O + 4 * lane);
-      const float mn = fmaxf(m, x.x), Mn = fmaxf(M, x.z);
-      l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
-      const float fo = ex2(M - Mn), fn = ex2(x.z - Mn);
-      o.x = o.x * fo + y.x * fn;
-      o.y = o.y * fo + y.y * fn;
-      o.z = o.z * fo + y.z * fn;
-      o.w = o.w * fo + y.w * fn;
+    const float* rec = recs + blockIdx.y * PART_STRIDE;
+    const size_t stride = (size_t)G * PART_STRIDE;
+    float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);  // the warp's first record, while the maxima are found
+    if (warp < n) y0 = *(const float4*)(rec + warp * stride + PART_O + 4 * lane);
+    float m = -INFINITY, M = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float4 x = *(const float4*)(rec + i * stride);
+      const float mn = fmaxf(m, x.x);
+      if (x.x != -INFINITY) l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
       m = mn;
-      M = Mn;
+      M = fmaxf(M, x.z);
     }
-    if (lane == 0) {
-      wm[warp] = m;
-      wl[warp] = l;
-      wt[warp] = M;
+    const float own = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    }
+    if (own != -INFINITY) l *= ex2(own - m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const bool none = m == -INFINITY;  // no token at all: zeros and -inf
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!none) {
+#pragma unroll 4
+      for (int i = warp; i < n; i += MT / 32) {
+        const float4 y = i == warp ? y0 : *(const float4*)(rec + i * stride + PART_O + 4 * lane);
+        const float f = ex2(rec[i * stride + REC_T] - M);
+        o.x = fmaf(y.x, f, o.x);
+        o.y = fmaf(y.y, f, o.y);
+        o.z = fmaf(y.z, f, o.z);
+        o.w = fmaf(y.w, f, o.w);
+      }
     }
     *(float4*)&wo[warp][4 * lane] = o;
     __syncthreads();
     if (threadIdx.x < D / 2) {
-      float gm = -INFINITY, gM = -INFINITY;
+      float x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < MT / 32; ++w) {
-        gm = fmaxf(gm, wm[w]);
-        gM = fmaxf(gM, wt[w]);
+        x += wo[w][2 * threadIdx.x];
+        y += wo[w][2 * threadIdx.x + 1];
       }
-      float gl = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-      for (int w = 0; w < MT / 32; ++w) {
-        if (wm[w] == -INFINITY) continue;
-        gl += wl[w] * ex2(wm[w] - gm);
-        const float f = ex2(wt[w] - gM);
-        x += wo[w][2 * threadIdx.x] * f;
-        y += wo[w][2 * threadIdx.x + 1] * f;
-      }
-      const bool none = gm == -INFINITY;  // no token at all: zeros and -inf
-      const float f = none ? 0.f : ex2(gM - gm) / gl;
-      const size_t row = (size_t)b * cv.Hq + (size_t)h * G + hd;
-      ((__nv_bfloat162*)(a.out + row * D))[threadIdx.x] = none ? __floats2bfloat162_rn(0.f, 0.f) : __floats2bfloat162_rn(x * f, y * f);
-      if (a.lse && threadIdx.x == 0) a.lse[row] = none ? -INFINITY : (gm + log2f(gl)) * LN2;
+      const float f = none ? 0.f : ex2(M - m) / l;
+      const size_t row = (size_t)b * cv.Hq + (size_t)h * G + blockIdx.y;
+      ((__nv_bfloat162*)(a.out + row * D))[threadIdx.x] = __floats2bfloat162_rn(x * f, y * f);
+      if (a.lse && threadIdx.x == 0) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
     }
     return;
   }
   // weights: every head's total first
   for (int hd = warp; hd < G; hd += MT / 32) {
     float m = -INFINITY, l = 0.f;
-    for (int i = i0 + lane; i <= i1; i += 32) {
-      const float* r = a.part + (((size_t)i + seg) * G + hd) * PART_STRIDE;
-      const float rm = r[REC_M], rl = r[REC_L];
-      if (rm == -INFINITY) continue;
-      const float mn = fmaxf(m, rm);
-      l = l * ex2(m - mn) + rl * ex2(rm - mn);
+    for (int i = lane; i < n; i += 32) {
+      const float2 x = *(const float2*)(recs + ((size_t)i * G + hd) * PART_STRIDE);
+      const float mn = fmaxf(m, x.x);
+      if (x.x != -INFINITY) l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
       m = mn;
     }
     float gm = m;
@@ -760,7 +748,7 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
 
 template <int TYPE, bool WEIGHTS>
 cudaError_t launch_main(const Kv8Decode& a, cudaStream_t st) {
-  const int smem = decode_smem(a.B, a.cv.G).total;
+  const int smem = decode_smem(a.cv.G).total;
   static int limit[MAX_DEVICES];
   const cudaError_t e = raise_smem_limit(kv8_decode_kernel<TYPE, WEIGHTS>, limit, smem);
   if (e != cudaSuccess) return e;
@@ -797,11 +785,10 @@ cudaError_t launch_kv8_decode(const Kv8Decode& a, int type, cudaStream_t st, Pro
   prof_end(prof, OSCAR_KERNEL_KV8_DECODE, st);
   if (e != cudaSuccess) return e;
   const int segs = a.B * a.cv.Hkv;
-  int slices = 0;
+  int slices = 0;  // a thread per page, up to 16 CTAs a (request, kv head)
   if (a.weights) {
-    slices = (2 * a.grid + segs - 1) / segs;
-    const int most = (a.cv.max_pages_per_req + MT - 1) / MT;
-    if (slices > most) slices = most;
+    slices = (a.cv.max_pages_per_req + MT - 1) / MT;
+    if (slices > 16) slices = 16;
   }
   prof_begin(prof, OSCAR_KERNEL_KV8_MERGE, st);
   e = launch_pdl(kv8_merge_kernel, dim3(segs, a.cv.G + slices), dim3(MT), 0, st, a);
