@@ -873,10 +873,15 @@ oscar_status oscar_decode_bf16_history(oscar_ctx* ctx, const oscar_cache* cache,
   return decode_common(ctx, 0, cache, q, out, lse, scratch, scratch_bytes, batch, stream, true);
 }
 
+static bool kv8_supported(const oscar_config& c) {
+  return (long long)c.num_kv_heads * (c.max_pages_per_req + KV8_WIN_UNITS) <= KV8_MAX_UNITS;
+}
+
 oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* out) {
   const oscar_status s = check_cfg(cfg);
   if (s != OSCAR_OK) return s;
   if (!out) return OSCAR_ERR_INVALID_ARG;
+  if (!kv8_supported(*cfg)) return OSCAR_ERR_UNSUPPORTED;
   const int Hkv = cfg->num_kv_heads, G = cfg->num_q_heads / Hkv, P = cfg->max_pages_per_req;
   out->head_bytes = KV8_HEAD_BYTES;
   out->page_bytes = (size_t)KV8_HEAD_BYTES * Hkv;
@@ -912,6 +917,7 @@ static CacheView kv8_rows(const oscar_ctx* ctx, const oscar_cache* c, int b0) {
 static oscar_status kv8_check(const oscar_ctx* ctx, const oscar_cache* cache, const float* weights, int batch) {
   if (!ctx || !cache_ok(cache, true)) return OSCAR_ERR_INVALID_ARG;
   if (batch < 0 || batch > ctx->cfg.max_batch || !aligned(weights, 16)) return OSCAR_ERR_INVALID_ARG;
+  if (!kv8_supported(ctx->cfg)) return OSCAR_ERR_UNSUPPORTED;
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_status(e);

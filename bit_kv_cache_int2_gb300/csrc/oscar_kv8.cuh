@@ -35,10 +35,12 @@ struct Kv8Req {
   bool ok;
 };
 
-__device__ __forceinline__ Kv8Req kv8_req(const CacheView& cv, int b) {
+// early: read past the L1, by a kernel that looks before its wait at values that
+// may still change.
+__device__ __forceinline__ Kv8Req kv8_req(const CacheView& cv, int b, bool early = false) {
   Kv8Req r;
-  r.L = cv.seq_lens[b];
-  r.H = cv.hist_lens[b];
+  r.L = early ? __ldcg(cv.seq_lens + b) : cv.seq_lens[b];
+  r.H = early ? __ldcg(cv.hist_lens + b) : cv.hist_lens[b];
   const int past = r.L > SINK ? r.L - SINK : 0;
   r.ok = r.L >= 0 && r.H >= 0 && r.H % KV8_BLK == 0 && r.H <= past && past - r.H <= RECENT &&
          (r.H + PAGE - 1) / PAGE <= cv.max_pages_per_req;
@@ -90,6 +92,10 @@ struct Kv8Evict {
 };
 __host__ __device__ __forceinline__ size_t kv8_evict_stride(int max_pages) { return 4 + 4 * (size_t)max_pages; }
 cudaError_t launch_kv8_evict(const Kv8Evict& a, int B, int num_sms, cudaStream_t st, Profiler* prof);
+
+// The largest number of 16 KB units a request may have: the work list counts
+// 32 requests in 32 bits.
+constexpr long long KV8_MAX_UNITS = 1 << 26;
 
 // Requests that one launch takes (a longer batch is several launches on the
 // stream, sharing the scratch), and the scratch of such a launch.

@@ -29,11 +29,20 @@ constexpr int REC_M = 0, REC_L = 1, REC_T = 2;
 // the mask: 0, 1 the sink, 2 + r ring slots 32r .. 32r + 31), then the history
 // pages.  CTA i of n takes units [floor(i W / n), floor((i + 1) W / n)).
 __device__ __forceinline__ uint32_t window_units(int L, int H) {
-  uint32_t m = L > 32 ? 3u : L > 0 ? 1u : 0u;
-#pragma unroll
-  for (int r = 0; r < KV8_RING_UNITS; ++r)
-    if (kv8_ring_held(L, H, 2 * r) || kv8_ring_held(L, H, 2 * r + 1)) m |= 4u << r;
-  return m;
+  const int held = max(L - SINK - H, 0);
+  uint32_t m = ((1u << ((held + KV8_BLK - 1) / KV8_BLK)) - 1u) << (H / KV8_BLK % KV8_RING_BLOCKS);
+  m |= m >> KV8_RING_BLOCKS;         // ring blocks that hold a token, in the low 16 bits
+  m = (m | m >> 1) & 0x5555u;        // ring units, every other bit
+  m = (m | m >> 1) & 0x3333u;
+  m = (m | m >> 2) & 0x0f0fu;
+  m = (m | m >> 4) & 0x00ffu;
+  return m << 2 | (L > 32 ? 3u : L > 0 ? 1u : 0u);
+}
+
+// The place of set bit number i of a unit mask.
+__device__ __forceinline__ int nth_unit(uint32_t m, int i) {
+  for (; i > 0; --i) m &= m - 1;
+  return __ffs(m) - 1;
 }
 
 struct Segment {  // a request's share of the list, the same for each of its kv heads
@@ -41,23 +50,29 @@ struct Segment {  // a request's share of the list, the same for each of its kv 
   uint32_t win;
 };
 
-__device__ __forceinline__ Segment segment_of(const CacheView& cv, int b) {
-  const Kv8Req r = kv8_req(cv, b);
+__device__ __forceinline__ Segment make_segment(int L, int H) {
   Segment s;
-  s.L = r.L;
-  s.H = r.H;
-  s.win = window_units(r.L, r.H);
-  s.pages = (r.H + PAGE - 1) / PAGE;
+  s.L = L;
+  s.H = H;
+  s.win = window_units(L, H);
+  s.pages = (H + PAGE - 1) / PAGE;
   s.units = s.pages + __popc(s.win);
   return s;
 }
 
-// Shared memory: a ring of `stages` 16 KB stages that units are copied into
-// ahead of their use (a window row takes 272 bytes, so that the eight rows of a
-// fragment start in different banks), the barriers and the warps' results.
-constexpr int WROW = D * 2 + 16;
-constexpr int STAGE_BYTES = 64 * WROW;  // 32 key rows and 32 value rows; a page needs 16416
-static_assert(STAGE_BYTES >= KV8_HEAD_BYTES && STAGE_BYTES % 128 == 0, "stage size");
+__device__ __forceinline__ Segment segment_of(const CacheView& cv, int b, bool early = false) {
+  const Kv8Req r = kv8_req(cv, b, early);
+  return make_segment(r.L, r.H);
+}
+
+// Shared memory: a ring of `stages` stages of a unit each, which units are copied
+// into ahead of their use, the barriers and the warps' results.  A window unit
+// is 32 key rows and then 32 value rows of 256 bytes, as they stand in memory:
+// the fragments' loads conflict two and four times, but a unit is two copies
+// (rows padded to 272 bytes took 64 copies, and 1.4 us to start them).
+constexpr int WROW = D * 2;
+constexpr int STAGE_BYTES = (KV8_HEAD_BYTES + 127) / 128 * 128;
+static_assert(STAGE_BYTES >= 64 * WROW, "a window unit fits a stage");
 constexpr int MAX_STAGES = 13;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
@@ -344,23 +359,22 @@ __host__ __device__ constexpr DecodeSmem decode_smem(int G) {
 // eight warps take the units in turn, so more than eight stages keep all of them busy
 static_assert(decode_smem(MAX_G).stages > KW, "stages at the largest group");
 
-// Units of all requests and, in *before, of those before request b; over all
-// kv heads.  Every warp finds them by itself.
-__device__ __forceinline__ long long count_units(const CacheView& cv, int B, int b, long long* before) {
+// Sum over the warp's lanes, and over the lanes below.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, uint32_t* all) {
   const int lane = threadIdx.x & 31;
-  long long all = 0, part = 0;
-  for (int i = lane; i < B; i += 32) {
-    const int x = segment_of(cv, i).units;
-    all += x;
-    if (i < b) part += x;
-  }
+  uint32_t upto = v;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    part += __shfl_xor_sync(0xffffffffu, part, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
-  *before = part * cv.Hkv;
-  return all * cv.Hkv;
+  *all = __shfl_sync(0xffffffffu, upto, 31);
+  return upto - v;
+}
+
+// Request b; empty beyond the batch.
+__device__ __forceinline__ Segment segment_or_none(const CacheView& cv, int B, int b, bool early = false) {
+  return b < B ? segment_of(cv, b, early) : make_segment(0, 0);
 }
 
 // A position in the work list.
@@ -369,48 +383,90 @@ struct Cursor {
   int b, h, i;  // unit i of (b, h)
 };
 
-// The cursor at unit u of the list (which has it); a whole warp calls it.
-__device__ __forceinline__ void cursor_set(Cursor& c, const CacheView& cv, int B, long long u) {
+// CTA i of `grid`: its first unit in c, and how many it has (0: none, c is not
+// set).  A whole warp calls it; every warp finds its CTA's share by itself.  Early,
+// before the wait, the lengths may change under it: then the answer is of no
+// use, but every read stays in range.
+__device__ __forceinline__ int cta_share(Cursor& c, const CacheView& cv, int B, uint32_t i, uint32_t grid,
+                                         bool early) {
   const int lane = threadIdx.x & 31;
-  long long before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    const long long own = b0 + lane < B ? (long long)segment_of(cv, b0 + lane).units * cv.Hkv : 0;
-    long long upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t beyond = __ballot_sync(0xffffffffu, before + upto > u);
-    if (beyond) {
-      const int l = __ffs(beyond) - 1;
-      c.b = b0 + l;
-      before += __shfl_sync(0xffffffffu, upto - own, l);
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+  Segment own = segment_or_none(cv, B, lane, early);
+  uint32_t units = (uint32_t)(own.units * cv.Hkv), sum;
+  uint32_t below = warp_scan(units, &sum);
+  unsigned long long W = sum;
+  for (int b0 = 32; b0 < B; b0 += 32)
+    W += __reduce_add_sync(0xffffffffu, (uint32_t)(segment_or_none(cv, B, b0 + lane, early).units * cv.Hkv));
+  const uint32_t n = W < grid ? (uint32_t)W : grid;
+  if (i >= n) return 0;
+  // floor(i W / n) with one division by n
+  unsigned long long q;
+  uint32_t r;
+  if (W >> 32 == 0) {
+    q = (uint32_t)W / n;
+    r = (uint32_t)W - (uint32_t)q * n;
+  } else {
+    q = W / n;
+    r = (uint32_t)(W - q * n);
   }
-  c.sg = segment_of(cv, c.b);
-  c.h = (int)((u - before) / c.sg.units);
-  c.i = (int)(u - before - (long long)c.h * c.sg.units);
+  const unsigned long long u0 = q * i + i * r / n;
+  const int count = (int)(q * (i + 1) + (i + 1) * r / n - u0);
+  unsigned long long before = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    if (b0) {
+      own = segment_or_none(cv, B, b0 + lane, early);
+      units = (uint32_t)(own.units * cv.Hkv);
+      below = warp_scan(units, &sum);
+    }
+    if (u0 < before + sum) {
+      const uint32_t u = (uint32_t)(u0 - before);
+      const int l = __ffs(__ballot_sync(0xffffffffu, below + units > u)) - 1;
+      c.b = b0 + l;
+      c.sg = make_segment(__shfl_sync(0xffffffffu, own.L, l), __shfl_sync(0xffffffffu, own.H, l));
+      const uint32_t v = u - __shfl_sync(0xffffffffu, below, l);
+      c.h = (int)(v / (uint32_t)c.sg.units);
+      c.i = (int)(v - (uint32_t)c.h * c.sg.units);
+      return count;
+    }
+    before += sum;
+  }
+  return 0;
 }
 
-// Forward by n units; the position must exist.
-__device__ __forceinline__ void cursor_forward(Cursor& c, const CacheView& cv, int n) {
+// Forward by n units; false at the end of the list.
+__device__ __forceinline__ bool cursor_forward(Cursor& c, const CacheView& cv, int B, int n, bool early = false) {
   c.i += n;
   while (c.i >= c.sg.units) {
     c.i -= c.sg.units;
     if (++c.h == cv.Hkv) {
       c.h = 0;
-      do c.sg = segment_of(cv, ++c.b);
-      while (c.sg.units == 0);
+      do {
+        if (++c.b >= B) return false;
+        c.sg = segment_of(cv, c.b, early);
+      } while (c.sg.units == 0);
     }
   }
+  return true;
 }
 
-__device__ __forceinline__ int cursor_page(const Cursor& c, const CacheView& cv) {
+// The page of the unit at c (any number for a window unit).
+__device__ __forceinline__ int cursor_page(const Cursor& c, const CacheView& cv, bool early = false) {
   const int pg = c.i - __popc(c.sg.win);
-  return pg < 0 ? 0 : cv.page_table[(size_t)c.b * cv.max_pages_per_req + pg];
+  if (pg < 0) return 0;
+  const int32_t* p = cv.page_table + (size_t)c.b * cv.max_pages_per_req + pg;
+  return early ? __ldcg(p) : *p;
+}
+
+// A hint to bring the unit at c into the L2 (lane 0).
+__device__ __forceinline__ void prefetch_unit(const Cursor& c, const CacheView& cv, int pid) {
+  if (c.i < __popc(c.sg.win)) {
+    const int unit = nth_unit(c.sg.win, c.i);
+    const size_t seg = (size_t)c.b * cv.Hkv + c.h;
+    const size_t row = unit < 2 ? seg * SINK + 32 * unit : seg * RECENT + 32 * (unit - 2);
+    bulk_prefetch_l2((unit < 2 ? cv.sink_k : cv.ring_k) + row * D, 32 * WROW);
+    bulk_prefetch_l2((unit < 2 ? cv.sink_v : cv.ring_v) + row * D, 32 * WROW);
+  } else if (pid >= 0 && pid < cv.num_pages) {
+    bulk_prefetch_l2(kv8_head(cv, pid, c.h), KV8_HEAD_BYTES);
+  }
 }
 
 // A warp starts the copy of the unit at c into a stage.
@@ -418,13 +474,14 @@ __device__ __forceinline__ void issue_unit(const Cursor& c, const CacheView& cv,
                                            int* issued, int lane) {
   if (lane == 0) ++*issued;
   if (c.i < __popc(c.sg.win)) {
-    const int unit = __fns(c.sg.win, 0, c.i + 1);
+    const int unit = nth_unit(c.sg.win, c.i);
     const size_t seg = (size_t)c.b * cv.Hkv + c.h;
     const size_t row = unit < 2 ? seg * SINK + 32 * unit : seg * RECENT + 32 * (unit - 2);
-    if (lane == 0) mbar_expect_tx(bar, 64 * D * 2);
-    __syncwarp();
-    bulk_g2s(stage + lane * WROW, (unit < 2 ? cv.sink_k : cv.ring_k) + (row + lane) * D, D * 2, bar);
-    bulk_g2s(stage + (32 + lane) * WROW, (unit < 2 ? cv.sink_v : cv.ring_v) + (row + lane) * D, D * 2, bar);
+    if (lane == 0) {
+      mbar_expect_tx(bar, 64 * WROW);
+      bulk_g2s(stage, (unit < 2 ? cv.sink_k : cv.ring_k) + row * D, 32 * WROW, bar);
+      bulk_g2s(stage + 32 * WROW, (unit < 2 ? cv.sink_v : cv.ring_v) + row * D, 32 * WROW, bar);
+    }
   } else if (lane == 0) {
     if (pid >= 0 && pid < cv.num_pages) {
       mbar_expect_tx(bar, KV8_HEAD_BYTES);
@@ -470,34 +527,43 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
   }
   fence_proxy_async();
   __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();  // after the wait: what the merge reads before its own wait is there
-  long long none;
-  const long long W = count_units(cv, B, 0, &none);
-  const long long n = W < a.grid ? W : a.grid;
-  if (blockIdx.x >= n) return;
-  const long long u0 = blockIdx.x * W / n;
-  const int count = (int)((blockIdx.x + 1) * W / n - u0);  // units of this CTA
-  Cursor c;
-  cursor_set(c, cv, B, u0);
-  // the warp's next unit to copy, and its page
-  Cursor ic = c;
-  int next = warp, pid = 0;
-  if (next < count) {
-    cursor_forward(ic, cv, warp);
-    pid = cursor_page(ic, cv);
+  // The CTA's share and the warp's first two units, twice: before the wait, from
+  // lengths and pages that the kernel before may still change, only to have the
+  // code and the data at hand (the L2 prefetch is a hint); then for good.
+  const bool two = warp + KW < NS;  // the warp fills two stages at the start
+  Cursor c, ic;                     // the CTA's first unit; the warp's next unit to copy, and its page
+  int count, next, pid = 0;
+#pragma unroll 1
+  for (bool early = true;; early = false) {
+    count = cta_share(c, cv, B, blockIdx.x, a.grid, early);
+    next = warp;
+    bool more = next < count;
+    if (more) {
+      ic = c;
+      more = cursor_forward(ic, cv, B, next, early);
+      if (more) pid = cursor_page(ic, cv, early);
+    }
+    if (!early) break;
+    if (lane == 0 && more) {
+      prefetch_unit(ic, cv, pid);
+      if (two && next + KW < count && cursor_forward(ic, cv, B, KW, true))
+        prefetch_unit(ic, cv, cursor_page(ic, cv, true));
+    }
+    __syncwarp();
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait: what the merge reads before its own wait is there
   }
+  if (count == 0) return;
   auto issue_next = [&](int stage, int step) {  // then moves on by `step` units
     if (next < count) {
       issue_unit(ic, cv, pid, smem + stage * STAGE_BYTES, &bars[stage], &issued[stage], lane);
       next += step;
       if (next < count) {
-        cursor_forward(ic, cv, step);
+        cursor_forward(ic, cv, B, step);
         pid = cursor_page(ic, cv);
       }
     }
   };
-  const bool two = warp + KW < NS;  // the warp fills two stages at the start
   issue_next(warp, two ? KW : NS);
   if (two) issue_next(warp + KW, NS - KW);
 
@@ -523,7 +589,7 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
       }
       const uint8_t* st = smem + stage * STAGE_BYTES;
       if (i < nwin) {
-        const int unit = __fns(c.sg.win, 0, i + 1), r = unit - 2;
+        const int unit = nth_unit(c.sg.win, i), r = unit - 2;
         const bool sink = unit < 2;
         const int n0 = sink ? min(max(c.sg.L - 32 * unit, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r);
         const int n1 = sink ? min(max(c.sg.L - 32 * unit - 16, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r + 1);
@@ -602,7 +668,7 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
     }
     __syncthreads();
     first += len;
-    if (first < count) cursor_forward(c, cv, len);
+    if (first < count) cursor_forward(c, cv, B, len);
   }
   // a wait ran out: no CTA leaves with a copy into its memory under way
   if (issued[MAX_STAGES] && threadIdx.x < NS && issued[threadIdx.x])
@@ -624,10 +690,15 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   const Segment sg = segment_of(cv, b);
   if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0 && !kv8_req(cv, b).ok) record_error(cv.err, OSCAR_ERR_STATE);
   Balanced bl;
-  long long before;
-  bl.W = count_units(cv, a.B, b, &before);
-  bl.n = (int)(bl.W < a.grid ? bl.W : a.grid);
+  bl.W = 0;
   bl.wch = 0;
+  long long before = 0;
+  for (int r0 = 0; r0 < a.B; r0 += 32) {
+    const uint32_t x = (uint32_t)(segment_or_none(cv, a.B, r0 + lane).units * cv.Hkv);
+    bl.W += __reduce_add_sync(0xffffffffu, x);
+    before += __reduce_add_sync(0xffffffffu, r0 + lane < b ? x : 0u);
+  }
+  bl.n = (int)(bl.W < a.grid ? bl.W : a.grid);
   const long long s0 = before + (long long)h * sg.units;
   int i0 = 0, n = 0;  // records i0 .. i0 + n - 1, one of each CTA that had a part
   if (sg.units) {
@@ -639,8 +710,12 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   if (blockIdx.y < G) {
     const float* rec = recs + blockIdx.y * PART_STRIDE;
     const size_t stride = (size_t)G * PART_STRIDE;
-    float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);  // the warp's first record, while the maxima are found
-    if (warp < n) y0 = *(const float4*)(rec + warp * stride + PART_O + 4 * lane);
+    float4 y[4];  // the warp's first records, while the maxima are found
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = warp + j * (MT / 32);
+      y[j] = i < n ? *(const float4*)(rec + i * stride + PART_O + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float m = -INFINITY, M = -INFINITY, l = 0.f;
     for (int i = lane; i < n; i += 32) {
       const float4 x = *(const float4*)(rec + i * stride);
@@ -660,16 +735,19 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const bool none = m == -INFINITY;  // no token at all: zeros and -inf
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& x, int i) {
+      const float f = ex2(rec[i * stride + REC_T] - M);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    };
     if (!none) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (warp + j * (MT / 32) < n) add(y[j], warp + j * (MT / 32));
 #pragma unroll 4
-      for (int i = warp; i < n; i += MT / 32) {
-        const float4 y = i == warp ? y0 : *(const float4*)(rec + i * stride + PART_O + 4 * lane);
-        const float f = ex2(rec[i * stride + REC_T] - M);
-        o.x = fmaf(y.x, f, o.x);
-        o.y = fmaf(y.y, f, o.y);
-        o.z = fmaf(y.z, f, o.z);
-        o.w = fmaf(y.w, f, o.w);
-      }
+      for (int i = warp + MT / 8; i < n; i += MT / 32) add(*(const float4*)(rec + i * stride + PART_O + 4 * lane), i);
     }
     *(float4*)&wo[warp][4 * lane] = o;
     __syncthreads();
@@ -713,15 +791,23 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req);
   const int slice = blockIdx.y - G, slices = gridDim.y - G;
   auto gather = [&](size_t rec) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int hd = 0; hd < G; ++hd) {
-      const float4 y = *(const float4*)(a.wsum + (rec * G + hd) * 4);
-      const float f = ex2(a.wmax[rec * G + hd] - tot_m[hd]) * tot_r[hd];
-      x.x += y.x * f;
-      x.y += y.y * f;
-      x.z += y.z * f;
-      x.w += y.w * f;
-    }
+    float4 y[MAX_G], x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float r[MAX_G];
+#pragma unroll
+    for (int hd = 0; hd < MAX_G; ++hd)
+      if (hd < G) {
+        y[hd] = *(const float4*)(a.wsum + (rec * G + hd) * 4);
+        r[hd] = a.wmax[rec * G + hd];
+      }
+#pragma unroll
+    for (int hd = 0; hd < MAX_G; ++hd)
+      if (hd < G) {
+        const float f = ex2(r[hd] - tot_m[hd]) * tot_r[hd];
+        x.x = fmaf(y[hd].x, f, x.x);
+        x.y = fmaf(y[hd].y, f, x.y);
+        x.z = fmaf(y[hd].z, f, x.z);
+        x.w = fmaf(y[hd].w, f, x.w);
+      }
     return x;
   };
   for (int p = slice * MT + threadIdx.x; p < sg.pages; p += slices * MT) {

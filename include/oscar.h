@@ -536,7 +536,9 @@ typedef struct {
                             need at most, any batch up to max_batch          */
 } oscar_kv8_layout_info;
 
-/* Sizes for a configuration (cfg->group_size is not used).  Host only. */
+/* Sizes for a configuration (cfg->group_size is not used).  Host only.  Above
+ * num_kv_heads (max_pages_per_req + 10) = 2^26 this and the calls below return
+ * OSCAR_ERR_UNSUPPORTED. */
 oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* out);
 
 /* Append T tokens to every request b < batch: a decode step (T = 1), a chunk, or
