@@ -76,8 +76,8 @@ struct Kv8Decode {
   float* weights;          // as above or null
   float decay;
   float* part;             // scratch [grid + B Hkv][G][PART_STRIDE]: m, l, M, o (oscar_kv8_decode.cu)
-  float* wsum;             // scratch [B Hkv][max_pages + 8][G][4]: sums of a page's blocks ...
-  float* wmax;             // scratch [B Hkv][max_pages + 8][G]: ... relative to 2^this
+  float* wsum;             // scratch [B Hkv][G][max_pages + 8][4]: sums of a page's blocks ...
+  float* wmax;             // scratch [B Hkv][G][max_pages + 8]: ... relative to 2^this
   int B, grid, wait_polls;
 };
 constexpr int KV8_WIN_UNITS = 10;                                  // 32-token pieces of the BF16 regions

@@ -39,14 +39,28 @@ __device__ __forceinline__ void load_side(SideRows& S, int side, int lane, Row r
   }
 }
 
-// x qmax / am rounded to the nearest 8-bit value, ties to even, exactly.
-// f = qmax / am has one rounding and x f another, so y is within 2^-23 of the
-// quotient.  x and am have 8 significant bits and the midpoints between codes
-// at most 8, so a quotient that is not a midpoint is at least 2^-16 away from
-// it: rounding y to 20 bits first puts every midpoint back in its place and
-// moves nothing across one.
-__device__ __forceinline__ float snap20(float y) {
-  return __uint_as_float((__float_as_uint(y) + 8u) & ~15u);
+// x qmax / am rounded to the nearest 8-bit value, ties to even, exactly, without
+// a division per value.  f = qmax / am has one rounding, so the product x f is
+// within 2^-24 of the quotient.  x and am have 8 significant bits and a
+// midpoint between codes at most 8: a quotient that is not a midpoint is at
+// least 2^-16 away from one (2^-13 for e4m3), relative.  So the exact product is
+// first rounded to a grid that holds the midpoints and is finer than that, which
+// puts the midpoints back in their places and moves nothing across one.
+struct Factor {
+  float f, g;
+};
+
+// e4m3: 20 bits.  g = 17 f (about): c = x g is a multiple of 16 ulp(x f), d is
+// x f - c rounded to such multiples, and c + d, exact, the multiple next to x f.
+__device__ __forceinline__ float snap20(float x, Factor k) {
+  const float c = __fmul_rn(x, k.g);
+  return __fadd_rn(c, __fmaf_rn(x, k.f, -c));
+}
+
+// int8: multiples of 2^-16 (2^-15 from 64 on, 2^-17 below -64) by adding 192; then
+// the rest of 1.5 2^23, which rounds to an integer that is the low byte's code.
+__device__ __forceinline__ uint32_t round8(float x, Factor k) {
+  return __float_as_uint(__fadd_rn(__fmaf_rn(x, k.f, 192.f), 12582912.f - 192.f));
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -54,23 +68,22 @@ __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 
 
 // Bytes 0..3 = the codes of a, b, c, d.
 template <int TYPE>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float f) {
-  a = snap20(a * f);
-  b = snap20(b * f);
-  c = snap20(c * f);
-  d = snap20(d * f);
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, Factor k) {
   if (TYPE == OSCAR_KV8_E4M3) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(d), "f"(c));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(snap20(b, k)), "f"(snap20(a, k)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(snap20(d, k)), "f"(snap20(c, k)));
     return (uint32_t)lo | ((uint32_t)hi << 16);
   } else {
-    // y + 1.5 2^23 rounds y to an integer, whose low byte is the code
-    const float M = 12582912.f;
-    const uint32_t ab = prmt(__float_as_uint(a + M), __float_as_uint(b + M), 0x0040);
-    const uint32_t cd = prmt(__float_as_uint(c + M), __float_as_uint(d + M), 0x0040);
-    return prmt(ab, cd, 0x5410);
+    return prmt(prmt(round8(a, k), round8(b, k), 0x0040), prmt(round8(c, k), round8(d, k), 0x0040), 0x5410);
   }
+}
+
+// Larger magnitudes of two BF16 pairs; NaN if one is.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b32 t;\n abs.bf16x2 t, %2;\n max.NaN.bf16x2 %0, %1, t;\n}\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // A warp quantises one side of a block and writes codes and scale.
@@ -83,7 +96,7 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = __vmaxu2(mx, word(S.w[i][r], j) & 0x7fff7fffu);
+      for (int j = 0; j < 4; ++j) mx = max_abs2(mx, word(S.w[i][r], j));
   mx = max(mx >> 16, mx & 0xffffu);
   mx = __reduce_max_sync(0xffffffffu, mx);
   // an infinity or NaN in the block: NaN as its scale, so that whatever reads the block shows it
@@ -91,7 +104,9 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
   const float am = fmaxf(__uint_as_float(mx << 16), KV8_TINY);
   const int e = (int)((__float_as_uint(am) >> 23) & 0xffu) - 127;  // am = 2^e x [1, 2)
   const float unit = __uint_as_float((__float_as_uint(am) & 0x007fffffu) | 0x3f800000u);
-  const float f = bad ? 0.f : ldexpf(__fdiv_rn(qmax, unit), -e);
+  Factor k;
+  k.f = ldexpf(__fdiv_rn(qmax, unit), -e);
+  k.g = 17.f * k.f;
   uint4* dst = (uint4*)(block + side * (KV8_BLK * D)) + lane;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -113,7 +128,7 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
           y = word(S.w[2 * h + 1][j >> 2], j & 3);
           a = bf_lo(x), b = bf_lo(y), p = bf_hi(x), q = bf_hi(y);
         }
-        ow[2 * s + h] = bad ? 0u : codes4<TYPE>(a, b, p, q, f);
+        ow[2 * s + h] = bad ? 0u : codes4<TYPE>(a, b, p, q, k);
       }
     dst[32 * c] = o;
   }
@@ -149,8 +164,7 @@ __device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, in
       if (id < 0) bad |= 1;
       if (id >= cv.num_pages) bad |= 2;
     }
-  const int none = __syncthreads_or(bad & 1), range = __syncthreads_or(bad & 2);
-  if (!p.err && (none || range)) p.err = none ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
+  if (__syncthreads_or(bad)) p.err = __syncthreads_or(bad & 1) ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
   return p;
 }
 
@@ -166,8 +180,8 @@ __device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, in
 // warps are done; else append_lengths_kernel does afterwards.
 template <int TYPE, bool SOLE>
 __global__ void __launch_bounds__(AW * 32, SOLE ? 1 : 2) append_kernel(Kv8Append a) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: append_lengths_kernel looks before its own
   const CacheView& cv = a.cv;
   const int b = blockIdx.y, Hkv = cv.Hkv, T = a.T;
   const AppendPlan p = append_plan(cv, b, T);
@@ -180,10 +194,17 @@ __global__ void __launch_bounds__(AW * 32, SOLE ? 1 : 2) append_kernel(Kv8Append
   const int first = ((p.L > SINK ? p.L : SINK) - SINK) / KV8_BLK;       // first block with a new one
   const int last = p.L1 > SINK ? (p.L1 - SINK - 1) / KV8_BLK : -1;
   const int h0 = p.H / KV8_BLK, h1 = p.H1 / KV8_BLK;
-  const long long tasks = (long long)(1 + (last >= first ? last - first + 1 : 0)) * Hkv * 2;
+  const int units = 1 + (last >= first ? last - first + 1 : 0), width = 2 * Hkv;  // tasks: units x (kv head, side)
   const size_t wrow = (size_t)KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req;
-  for (long long w = (long long)blockIdx.x * AW + warp; w < tasks; w += (long long)gridDim.x * AW) {
-    const int side = (int)(w & 1), h = (int)((w >> 1) % Hkv), u = (int)((w >> 1) / Hkv) - 1;
+  const uint32_t w0 = blockIdx.x * AW + warp, step = gridDim.x * AW;
+  const int step_u = (int)(step / width), step_s = (int)(step % width);
+  int unit = (int)(w0 / width), s = (int)(w0 % width);
+  for (; unit < units; unit += step_u, s += step_s) {
+    if (s >= width) {
+      s -= width;
+      if (++unit >= units) break;
+    }
+    const int side = s & 1, h = s >> 1, u = unit - 1;
     const size_t head = (size_t)b * Hkv + h;
     const __nv_bfloat16* in = (side ? a.v : a.k) + ((size_t)b * T * Hkv + h) * D;  // token t at in + t Hkv D
     const size_t in_row = (size_t)Hkv * D;
@@ -238,10 +259,12 @@ __global__ void __launch_bounds__(AW * 32, SOLE ? 1 : 2) append_kernel(Kv8Append
   }
 }
 
+// After append_kernel<.., false>, which leaves the lengths as they are: the plan is
+// made again while that still runs.
 __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
   pdl_launch_dependents();
-  pdl_wait();
   const AppendPlan p = append_plan(a.cv, blockIdx.x, a.T);
+  pdl_wait();
   if (threadIdx.x != 0) return;
   if (p.err) {
     record_error(a.cv.err, p.err);
@@ -253,6 +276,7 @@ __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
 
 // ------------------------------------------------------------------ eviction
 constexpr int ET = 1024;  // threads that select the blocks of one (request, kv head)
+constexpr int EVICT_HELD = 50 * 1024;  // keys kept in shared memory (200 KB)
 
 // Unsigned keys in the order of the floats, NaN last.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -282,7 +306,10 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* all) {
 // lower index first among equal ones.  Of the n - e that stay, those beyond
 // place n - e move into the places below it that become free; both lists are
 // in ascending order and equally long.
-__global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
+// The keys are read once into shared memory (the first `held`; a history beyond
+// 800K tokens reads the others again).
+__global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a, int held) {
+  extern __shared__ uint32_t keys[];
   __shared__ int red[2][32], hist[2][256];
   pdl_launch_dependents();
   pdl_wait();
@@ -301,8 +328,7 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
       if (id < 0) bad |= 1;
       if (id >= cv.num_pages) bad |= 2;
     }
-    const int none = __syncthreads_or(bad & 1), range = __syncthreads_or(bad & 2);
-    if (none || range) err = none ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
+    if (__syncthreads_or(bad)) err = __syncthreads_or(bad & 1) ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
   }
   if (err) e = 0;
   if (tid == 0) {
@@ -317,6 +343,16 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
   // with it so far have each next digit.  Lanes of a warp with the same digit
   // count as one (weights often share their exponent).
   const int lane = tid & 31;
+  for (int i0 = tid; i0 < n && i0 < held; i0 += 8 * ET) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j * ET < n && i0 + j * ET < held) x[j] = w[i0 + j * ET];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j * ET < n && i0 + j * ET < held) keys[i0 + j * ET] = order_key(x[j]);
+  }
+  auto key_of = [&](int i) { return i < held ? keys[i] : order_key(w[i]); };  // (a thread reads what it wrote)
   uint32_t cut = 0;
   int want = e;  // the key's rank among those that agree, from 1
   if (tid < 512) hist[tid >> 8][tid & 255] = 0;
@@ -326,7 +362,7 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
     int* hs = hist[pass & 1];
     for (int i0 = 0; i0 < n; i0 += ET) {
       const int i = i0 + tid;
-      const uint32_t key = i < n ? order_key(w[i]) : 0;
+      const uint32_t key = i < n ? key_of(i) : 0;
       const bool in = i < n && (pass == 0 || (key >> (shift + 8)) == (cut >> (shift + 8)));
       const uint32_t digit = in ? (key >> shift) & 255u : 256u;
       const uint32_t same = __match_any_sync(0xffffffffu, digit);
@@ -365,7 +401,7 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a) {
   int equal = 0, nh = 0, nm = 0;
   for (int i0 = 0; i0 < n; i0 += ET) {
     const int i = i0 + tid;
-    const uint32_t key = i < n ? order_key(w[i]) : 0xffffffffu;
+    const uint32_t key = i < n ? key_of(i) : 0xffffffffu;
     const bool eq = i < n && key == cut;
     int all;
     const int rank = equal + block_scan(eq, red[0], &all);
@@ -470,7 +506,11 @@ cudaError_t launch_kv8_evict(const Kv8Evict& a, int B, int num_sms, cudaStream_t
   const int segs = B * a.cv.Hkv;
   const int per = (4 * num_sms + segs - 1) / segs;  // CTAs per (request, kv head)
   prof_begin(prof, OSCAR_KERNEL_KV8_EVICT, st);
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(segs), dim3(ET), 0, st, a);
+  int held = KV8_PAGE_BLOCKS * a.cv.max_pages_per_req;
+  if (held > EVICT_HELD) held = EVICT_HELD;
+  static int limit[MAX_DEVICES];
+  cudaError_t e = raise_smem_limit(evict_select_kernel, limit, held * 4);
+  if (e == cudaSuccess) e = launch_pdl(evict_select_kernel, dim3(segs), dim3(ET), held * 4, st, a, held);
   if (e == cudaSuccess) e = launch_pdl(evict_move_kernel, dim3(segs, per), dim3(256), 0, st, a);
   prof_end(prof, OSCAR_KERNEL_KV8_EVICT, st);
   return e;

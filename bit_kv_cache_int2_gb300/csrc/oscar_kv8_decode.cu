@@ -204,11 +204,23 @@ __device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], 
   }
 }
 
-// The block sums of NT tiles for the merge: ws[n] the sums of head n's blocks,
-// wm[n] what they are relative to.
+// Block sums for the merge, [B Hkv][G][max_pages + 8]: of a page's four blocks
+// (of a ring unit's two, after the pages), and the maximum they are relative to.
+// The merge reads them a page per thread, so the pages are innermost.
+struct Sums {
+  float4* sum;
+  float* max;
+  size_t stride;  // from head to head
+};
+
+__device__ __forceinline__ Sums sums_at(const Kv8Decode& a, int seg, int rec) {
+  const size_t stride = a.cv.max_pages_per_req + KV8_RING_UNITS;
+  const size_t at = (size_t)seg * a.cv.G * stride + rec;
+  return {(float4*)a.wsum + at, a.wmax + at, stride};
+}
+
 template <int NT>
-__device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], float* ws, float* wm, int G, int gid,
-                                           int tq) {
+__device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], const Sums& w, int G, int gid, int tq) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -221,8 +233,8 @@ __device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], 
     float* x = (float*)&v;
 #pragma unroll
     for (int t = 0; t < NT; ++t) x[t] = gid ? sum[t][1] : sum[t][0];
-    *(float4*)(ws + 4 * n) = v;
-    wm[n] = gid ? S.m[1] : S.m[0];
+    w.sum[n * w.stride] = v;
+    w.max[n * w.stride] = gid ? S.m[1] : S.m[0];
   }
 }
 
@@ -230,7 +242,7 @@ __device__ __forceinline__ void write_sums(const State& S, float (&sum)[NT][2], 
 // FULL: all four, with nothing between them that keeps their products in order.
 template <int TYPE, bool WEIGHTS, bool FULL>
 __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_t* page, int nb, int lane, int G,
-                                          float* ws, float* wm) {
+                                          const Sums& w) {
   const int gid = lane >> 2, tq = lane & 3;
   float s[4][4], lv[4];
 #pragma unroll
@@ -277,7 +289,7 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
       }
     }
   }
-  if (WEIGHTS) write_sums<4>(S, sum, ws, wm, G, gid, tq);
+  if (WEIGHTS) write_sums<4>(S, sum, w, G, gid, tq);
 }
 
 // 32 BF16 tokens at K and V (WROW bytes from row to row), of which the first n0
@@ -287,7 +299,7 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
 // newest tokens often carry most of the weight.
 template <bool WEIGHTS>
 __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint8_t* K, const uint8_t* V, int n0, int n1,
-                                            int lane, int G, float* ws, float* wm) {
+                                            int lane, int G, bool sums, const Sums& w) {
   const int gid = lane >> 2, tq = lane & 3;
   float s[2][4];
   const float lv[2] = {0.f, 0.f};
@@ -338,7 +350,7 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
       mma_bf16(S.o[j], a0, a1, a2, a3, bl[0], bl[1]);
     }
   }
-  if (WEIGHTS && ws) write_sums<2>(S, sum, ws, wm, G, gid, tq);
+  if (WEIGHTS && sums) write_sums<2>(S, sum, w, G, gid, tq);
 }
 
 // ------------------------------------------------------------------- decode
@@ -593,23 +605,21 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
         const bool sink = unit < 2;
         const int n0 = sink ? min(max(c.sg.L - 32 * unit, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r);
         const int n1 = sink ? min(max(c.sg.L - 32 * unit - 16, 0), 16) : kv8_ring_held(c.sg.L, c.sg.H, 2 * r + 1);
-        const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + cv.max_pages_per_req + r;
-        window_step<WEIGHTS>(S, Q, st, st + 32 * WROW, n0, n1, lane, G, sink ? nullptr : a.wsum + at * G * 4,
-                             a.wmax + at * G);
+        window_step<WEIGHTS>(S, Q, st, st + 32 * WROW, n0, n1, lane, G, !sink,
+                             sums_at(a, seg, cv.max_pages_per_req + max(r, 0)));
       } else {
         if (!fp16) query_to_fp16(Q, tq);
         fp16 = true;
         const int pg = i - nwin;
         const int id = cv.page_table[(size_t)c.b * cv.max_pages_per_req + pg];
-        const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS) + pg;
-        float *ws = a.wsum + at * G * 4, *wm = a.wmax + at * G;
+        const Sums w = sums_at(a, seg, pg);
         if (id >= 0 && id < cv.num_pages) {
           const int nb = c.sg.H / KV8_BLK - pg * KV8_PAGE_BLOCKS;
-          if (nb >= KV8_PAGE_BLOCKS) page_step<TYPE, WEIGHTS, true>(S, Q, st, KV8_PAGE_BLOCKS, lane, G, ws, wm);
-          else page_step<TYPE, WEIGHTS, false>(S, Q, st, nb, lane, G, ws, wm);
+          if (nb >= KV8_PAGE_BLOCKS) page_step<TYPE, WEIGHTS, true>(S, Q, st, KV8_PAGE_BLOCKS, lane, G, w);
+          else page_step<TYPE, WEIGHTS, false>(S, Q, st, nb, lane, G, w);
         } else if (WEIGHTS && lane < G) {  // its tokens are left out
-          *(float4*)(ws + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
-          wm[lane] = -INFINITY;
+          w.sum[lane * w.stride] = make_float4(0.f, 0.f, 0.f, 0.f);
+          w.max[lane * w.stride] = -INFINITY;
         }
       }
       __syncwarp();  // the stage has been read: the next copy may come into it
@@ -787,17 +797,17 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   }
   __syncthreads();
   if (tot_m[0] == -INFINITY) return;  // nothing was attended to
-  const size_t at = (size_t)seg * (cv.max_pages_per_req + KV8_RING_UNITS);
   float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req);
   const int slice = blockIdx.y - G, slices = gridDim.y - G;
-  auto gather = [&](size_t rec) {
+  auto gather = [&](int rec) {
+    const Sums sums = sums_at(a, seg, rec);
     float4 y[MAX_G], x = make_float4(0.f, 0.f, 0.f, 0.f);
     float r[MAX_G];
 #pragma unroll
     for (int hd = 0; hd < MAX_G; ++hd)
       if (hd < G) {
-        y[hd] = *(const float4*)(a.wsum + (rec * G + hd) * 4);
-        r[hd] = a.wmax[rec * G + hd];
+        y[hd] = sums.sum[hd * sums.stride];
+        r[hd] = sums.max[hd * sums.stride];
       }
 #pragma unroll
     for (int hd = 0; hd < MAX_G; ++hd)
@@ -811,7 +821,7 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
     return x;
   };
   for (int p = slice * MT + threadIdx.x; p < sg.pages; p += slices * MT) {
-    const float4 x = gather(at + p);
+    const float4 x = gather(p);
     float4* dst = (float4*)(w + KV8_RING_BLOCKS) + p;
     float4 v = *dst;
     const int nb = sg.H / KV8_BLK - p * KV8_PAGE_BLOCKS;
@@ -825,7 +835,7 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
     const int r = threadIdx.x;
     const int n0 = kv8_ring_held(sg.L, sg.H, 2 * r), n1 = kv8_ring_held(sg.L, sg.H, 2 * r + 1);
     if (n0 || n1) {
-      const float4 x = gather(at + cv.max_pages_per_req + r);
+      const float4 x = gather(cv.max_pages_per_req + r);
       if (n0) w[2 * r] = fmaf(w[2 * r], a.decay, x.x);
       if (n1) w[2 * r + 1] = fmaf(w[2 * r + 1], a.decay, x.y);
     }
