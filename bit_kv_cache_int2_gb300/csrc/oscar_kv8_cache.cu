@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
 }
 
 // ------------------------------------------------------------------ eviction
-constexpr int ET = 1024;  // threads that select the blocks of one (request, kv head)
+constexpr int ET = 512;  // threads that select the blocks of one (request, kv head)
 constexpr int EVICT_HELD = 50 * 1024;  // keys kept in shared memory (200 KB)
 
 // Unsigned keys in the order of the floats, NaN last.
@@ -285,21 +285,16 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Sums of v over lower threads of the block (returned) and over all ET (*all).
-// `red` alternates between two arrays, so one barrier a call is enough.
-__device__ __forceinline__ int block_scan(int v, int* red, int* all) {
+// Sum over the lower warps of the block (returned) and over all (*all) of v,
+// which is the same in all lanes of a warp.  Calls alternate between two
+// arrays `red`, so one barrier each is enough.
+__device__ __forceinline__ int warps_scan(int v, int* red, int* all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int upto = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) red[warp] = upto;
+  if (lane == 0) red[warp] = v;
   __syncthreads();
-  const int n = red[lane];
+  const int n = lane < ET / 32 ? red[lane] : 0;
   *all = __reduce_add_sync(0xffffffffu, n);
-  return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + upto - v;
+  return __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
 }
 
 // The blocks of one (request, kv head) that go: the e smallest weights, the
@@ -307,27 +302,37 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* all) {
 // place n - e move into the places below it that become free; both lists are
 // in ascending order and equally long.
 // The keys are read once into shared memory (the first `held`; a history beyond
-// 800K tokens reads the others again).
+// 800K tokens reads the others again).  The time is latency and the barriers of
+// some ten short phases, each run once (fetching its code is part of it, so
+// loops are not unrolled): the block is 16 warps (32 took longer), a digit is 11 bits: the weights fall apart into about a hundred first digits, and the
+// second digit nearly always decides.
 __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a, int held) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int red[2][32], hist[2][256];
-  pdl_launch_dependents();
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(16) int hist[2048];
+  __shared__ int red[2][ET / 32], found[3];
   pdl_wait();
+  pdl_launch_dependents();
   const CacheView& cv = a.cv;
-  const int b = blockIdx.x / cv.Hkv, tid = threadIdx.x;
+  const int b = blockIdx.x / cv.Hkv, tid = threadIdx.x, lane = tid & 31;
   int32_t* list = a.list + (size_t)blockIdx.x * kv8_evict_stride(cv.max_pages_per_req);
+  const float* w = a.weights + (size_t)blockIdx.x * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) +
+                   KV8_RING_BLOCKS;
   const Kv8Req r = kv8_req(cv, b);
   const int n = r.H / KV8_BLK;
   // whole turns of the ring, so that the window's tokens keep their slots
   int e = r.H > a.budget ? (r.H - a.budget) / RECENT * KV8_RING_BLOCKS : 0;
   int err = r.ok ? 0 : OSCAR_ERR_STATE;
   if (e) {
+    *(int4*)&hist[4 * tid] = make_int4(0, 0, 0, 0);
     int bad = 0;
     for (int pg = tid; pg < (r.H + PAGE - 1) / PAGE; pg += ET) {
       const int id = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
       if (id < 0) bad |= 1;
       if (id >= cv.num_pages) bad |= 2;
     }
+    const int end = n < held ? n : held;
+#pragma unroll 4
+    for (int i = tid; i < end; i += ET) keys[i] = order_key(w[i]);
     if (__syncthreads_or(bad)) err = __syncthreads_or(bad & 1) ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE;
   }
   if (err) e = 0;
@@ -337,84 +342,98 @@ __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a, int held) 
     if (!e) list[0] = 0;
   }
   if (!e) return;
-  const float* w = a.weights + (size_t)blockIdx.x * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req) +
-                   KV8_RING_BLOCKS;
-  // the e-th smallest key, eight bits at a time: how many of the keys that agree
-  // with it so far have each next digit.  Lanes of a warp with the same digit
-  // count as one (weights often share their exponent).
-  const int lane = tid & 31;
-  for (int i0 = tid; i0 < n && i0 < held; i0 += 8 * ET) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i0 + j * ET < n && i0 + j * ET < held) x[j] = w[i0 + j * ET];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i0 + j * ET < n && i0 + j * ET < held) keys[i0 + j * ET] = order_key(x[j]);
-  }
-  auto key_of = [&](int i) { return i < held ? keys[i] : order_key(w[i]); };  // (a thread reads what it wrote)
-  uint32_t cut = 0;
-  int want = e;  // the key's rank among those that agree, from 1
-  if (tid < 512) hist[tid >> 8][tid & 255] = 0;
-  __syncthreads();
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    int* hs = hist[pass & 1];
-    for (int i0 = 0; i0 < n; i0 += ET) {
-      const int i = i0 + tid;
+  auto key_of = [&](int i) { return i < held ? keys[i] : order_key(w[i]); };
+  // the e-th smallest key, a digit at a time, until all keys that agree with it go:
+  // how many of the keys that agree so far have each next digit.  A warp's keys
+  // that share lane 0's digit count as one (equal weights, zeros above all, are common).
+  uint32_t cut = 0;  // its bits from `shift` on
+  int want = e;      // its rank among those that agree, from 1
+  int agree = n, shift = 32;
+  while (shift > 0 && want < agree) {
+    const int bits = shift > 11 ? 11 : shift, to = shift - bits;
+    const uint32_t mask = (1u << bits) - 1u;
+#pragma unroll 4
+    for (int i0 = tid - lane; i0 < n; i0 += ET) {
+      const int i = i0 + lane;
       const uint32_t key = i < n ? key_of(i) : 0;
-      const bool in = i < n && (pass == 0 || (key >> (shift + 8)) == (cut >> (shift + 8)));
-      const uint32_t digit = in ? (key >> shift) & 255u : 256u;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hs[digit], __popc(same));
+      const bool in = i < n && (shift == 32 || key >> shift == cut);
+      const uint32_t digit = in ? key >> to & mask : ~0u;
+      const uint32_t common = __shfl_sync(0xffffffffu, digit, 0);
+      const uint32_t same = __ballot_sync(0xffffffffu, digit == common);
+      if (in && (lane == 0 || digit != common)) atomicAdd(&hist[digit], lane == 0 ? __popc(same) : 1);
     }
     __syncthreads();
-    // every warp finds the digit by itself: a lane adds up eight bins
-    int v[8], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += v[j] = hs[8 * lane + j];
-    int upto = sum;
+    // four bins a thread: how many keys stand in lower ones
+    const int4 c = *(const int4*)&hist[4 * tid];
+    const int own = c.x + c.y + c.z + c.w;
+    int below = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+      const int x = __shfl_up_sync(0xffffffffu, below, o);
+      if (lane >= o) below += x;
     }
-    const int l = __ffs(__ballot_sync(0xffffffffu, upto >= want)) - 1;
-    int below = upto - sum, digit = 8 * lane;
-#pragma unroll
-    for (int j = 0; j < 7; ++j) {
-      if (below + v[j] >= want) break;
-      below += v[j];
-      ++digit;
+    if (lane == 31) red[0][tid >> 5] = below;
+    *(int4*)&hist[4 * tid] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    below += __reduce_add_sync(0xffffffffu, lane < (tid >> 5) ? red[0][lane] : 0) - own;
+    if (below < want && want <= below + own) {
+      const int v[4] = {c.x, c.y, c.z, c.w};
+      int j = 0;
+      while (below + v[j] < want) below += v[j++];
+      found[0] = 4 * tid + j;
+      found[1] = below;
+      found[2] = v[j];
     }
-    cut |= (uint32_t)__shfl_sync(0xffffffffu, digit, l) << shift;
-    want -= __shfl_sync(0xffffffffu, below, l);
-    // the next pass counts in the other array; this one is cleared for the pass after it
-    if (pass < 2) {
-      __syncthreads();
-      if (tid < 256) hs[tid] = 0;
-    }
+    __syncthreads();
+    cut = (shift == 32 ? 0u : cut << bits) | (uint32_t)found[0];
+    want -= found[1];
+    agree = found[2];
+    shift = to;
   }
-  const int equal_go = want, keep = n - e;  // of the keys equal to it, so many go
+  // now a block goes if its key is below the cut (in the bits from `shift` on), or
+  // agrees with it and is among the first `want` that do
+  const int keep = n - e, warp = tid >> 5;
+  const uint32_t lower = (1u << lane) - 1u;
+  const int chunks = (n + 31) / 32, share = (chunks + ET / 32 - 1) / (ET / 32);  // 32 keys each; a warp's are in a row
+  const int c0 = warp * share, c1 = min(c0 + share, chunks);
+  int first = 0, all;  // agreeing keys before this warp's
+  if (want < agree) {  // (when all that agree go, their order does not matter)
+    int v = 0;
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) {
+      const int i = 32 * c + lane;
+      v += __popc(__ballot_sync(0xffffffffu, i < n && key_of(i) >> shift == cut));  // (shift < 32 here)
+    }
+    first = warps_scan(v, red[0], &all);
+  }
   int32_t* holes = list + 4;
   int32_t* ends = holes + 2 * (size_t)cv.max_pages_per_req;
-  int equal = 0, nh = 0, nm = 0;
-  for (int i0 = 0; i0 < n; i0 += ET) {
-    const int i = i0 + tid;
-    const uint32_t key = i < n ? key_of(i) : 0xffffffffu;
-    const bool eq = i < n && key == cut;
-    int all;
-    const int rank = equal + block_scan(eq, red[0], &all);
-    equal += all;
-    const bool go = i < n && (key < cut || (eq && rank < equal_go));
-    const bool hole = go && i < keep, end = i < n && !go && i >= keep;
-    const int r = block_scan((int)hole | (int)end << 16, red[1], &all);  // both counts at once
-    if (hole) holes[nh + (r & 0xffff)] = i;
-    if (end) ends[nm + (r >> 16)] = i;
-    nh += all & 0xffff;
-    nm += all >> 16;
+  int nh = 0, ne = 0;  // counts; then, in the second turn, the places to write to
+#pragma unroll 1
+  for (int turn = 0; turn < 2; ++turn) {
+    int rank = first;
+#pragma unroll 4
+    for (int c = c0; c < c1; ++c) {
+      const int i = 32 * c + lane;
+      const uint32_t key = i < n && shift < 32 ? key_of(i) >> shift : 0u;
+      const uint32_t eq = __ballot_sync(0xffffffffu, i < n && key == cut);
+      const bool go = i < n && (key < cut || (key == cut && (want >= agree || rank + __popc(eq & lower) < want)));
+      rank += __popc(eq);
+      const bool hole = go && i < keep, end = !go && i >= keep && i < n;
+      const uint32_t mh = __ballot_sync(0xffffffffu, hole), me = __ballot_sync(0xffffffffu, end);
+      if (turn) {
+        if (hole) holes[nh + __popc(mh & lower)] = i;
+        if (end) ends[ne + __popc(me & lower)] = i;
+      }
+      nh += __popc(mh);
+      ne += __popc(me);
+    }
+    if (turn == 0) {
+      nh = warps_scan(nh, red[1], &all);
+      if (tid == 0) list[0] = all;
+      ne = warps_scan(ne, red[0], &all);
+    }
   }
-  if (tid == 0) list[0] = nh;
 }
 
 // Moves the listed blocks, a warp each, and takes the evicted tokens off the
