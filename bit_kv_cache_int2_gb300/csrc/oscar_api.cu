@@ -946,7 +946,7 @@ oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
     a.v = (const __nv_bfloat16*)v_new + off;
     a.weights = weights ? weights + b0 * kv8_weights_row(ctx) : nullptr;
     a.T = T;
-    const cudaError_t e = launch_kv8_append(a, type, n, ctx->num_sms, (cudaStream_t)stream, &ctx->prof);
+    const cudaError_t e = launch_kv8_append(a, type, n, (cudaStream_t)stream, &ctx->prof);
     if (e != cudaSuccess) return cuda_status(e);
   }
   return OSCAR_OK;

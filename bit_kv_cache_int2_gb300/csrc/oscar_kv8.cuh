@@ -66,7 +66,7 @@ struct Kv8Append {
   float* weights;              // [B][Hkv][16 + 4 max_pages] or null
   int T;
 };
-cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, int num_sms, cudaStream_t st, Profiler* prof);
+cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, cudaStream_t st, Profiler* prof);
 
 struct Kv8Decode {
   CacheView cv;

@@ -50,34 +50,55 @@ struct Factor {
   float f, g;
 };
 
-// e4m3: 20 bits.  g = 17 f (about): c = x g is a multiple of 16 ulp(x f), d is
-// x f - c rounded to such multiples, and c + d, exact, the multiple next to x f.
-__device__ __forceinline__ float snap20(float x, Factor k) {
-  const float c = __fmul_rn(x, k.g);
-  return __fadd_rn(c, __fmaf_rn(x, k.f, -c));
+// Two fp32 values in one register pair: one instruction works on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-// int8: multiples of 2^-16 (2^-15 from 64 on, 2^-17 below -64) by adding 192; then
-// the rest of 1.5 2^23, which rounds to an integer that is the low byte's code.
-__device__ __forceinline__ uint32_t round8(float x, Factor k) {
-  return __float_as_uint(__fadd_rn(__fmaf_rn(x, k.f, 192.f), 12582912.f - 192.f));
+// Codes of two values, in the low two bytes.
+//  e4m3: with g = -17 f (about), c = x g is a multiple of 16 ulp(x f), d is
+//    x f + c rounded to such multiples, and d - c, exact, the multiple next to x f:
+//    20 bits of it.
+//  int8: adding 192 rounds x f to multiples of 2^-16 (2^-15 from 64 on, 2^-17 below
+//    -64); adding the rest of 1.5 2^23 rounds that to an integer, whose low byte
+//    is the code.
+template <int TYPE>
+__device__ __forceinline__ uint32_t codes2(uint64_t x, Factor k) {
+  uint32_t r;
+  if (TYPE == OSCAR_KV8_E4M3) {
+    const uint64_t c = mul2(x, pair(k.g, k.g));
+    const uint64_t y = fma2(c, pair(-1.f, -1.f), fma2(x, pair(k.f, k.f), c));
+    asm("{\n .reg .f32 a, b;\n .reg .b16 t;\n mov.b64 {a, b}, %1;\n cvt.rn.satfinite.e4m3x2.f32 t, b, a;\n"
+        " cvt.u32.u16 %0, t;\n}\n"
+        : "=r"(r)
+        : "l"(y));
+  } else {
+    const float rest = 12582912.f - 192.f;
+    const uint64_t y = add2(fma2(x, pair(k.f, k.f), pair(192.f, 192.f)), pair(rest, rest));
+    asm("{\n .reg .b32 a, b;\n mov.b64 {a, b}, %1;\n prmt.b32 %0, a, b, 0x0040;\n}\n" : "=r"(r) : "l"(y));
+  }
+  return r;
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Bytes 0..3 = the codes of a, b, c, d.
-template <int TYPE>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, Factor k) {
-  if (TYPE == OSCAR_KV8_E4M3) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(snap20(b, k)), "f"(snap20(a, k)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(snap20(d, k)), "f"(snap20(c, k)));
-    return (uint32_t)lo | ((uint32_t)hi << 16);
-  } else {
-    return prmt(prmt(round8(a, k), round8(b, k), 0x0040), prmt(round8(c, k), round8(d, k), 0x0040), 0x5410);
-  }
-}
 
 // Larger magnitudes of two BF16 pairs; NaN if one is.
 __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
@@ -106,7 +127,7 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
   const float unit = __uint_as_float((__float_as_uint(am) & 0x007fffffu) | 0x3f800000u);
   Factor k;
   k.f = ldexpf(__fdiv_rn(qmax, unit), -e);
-  k.g = 17.f * k.f;
+  k.g = -17.f * k.f;
   uint4* dst = (uint4*)(block + side * (KV8_BLK * D)) + lane;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -128,7 +149,7 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
           y = word(S.w[2 * h + 1][j >> 2], j & 3);
           a = bf_lo(x), b = bf_lo(y), p = bf_hi(x), q = bf_hi(y);
         }
-        ow[2 * s + h] = bad ? 0u : codes4<TYPE>(a, b, p, q, k);
+        ow[2 * s + h] = bad ? 0u : prmt(codes2<TYPE>(pair(a, b), k), codes2<TYPE>(pair(p, q), k), 0x5410);
       }
     dst[32 * c] = o;
   }
@@ -136,13 +157,13 @@ __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8
 }
 
 // The lengths an append leaves, and whether it can be done at all: `err` is
-// the reason if not.  Every thread of the block calls it.
+// the reason if not.
 struct AppendPlan {
   int L, H, L1, H1;
   int err;
 };
 
-__device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, int T) {
+__device__ __forceinline__ AppendPlan append_lengths(const CacheView& cv, int b, int T) {
   AppendPlan p;
   const Kv8Req r = kv8_req(cv, b);
   p.L = r.L;
@@ -156,10 +177,15 @@ __device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, in
   if (!p.err && (H1 + PAGE - 1) / PAGE > cv.max_pages_per_req) p.err = OSCAR_ERR_RANGE;
   p.L1 = (int)L1;
   p.H1 = (int)H1;
+  return p;
+}
+
+// And the pages that take the blocks.  Every thread of the block calls it.
+__device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, int T) {
+  AppendPlan p = append_lengths(cv, b, T);
   int bad = 0;
-  if (!p.err)
-    for (int pg = r.H / PAGE + (int)threadIdx.x; pg < (int)((H1 + PAGE - 1) / PAGE); pg += blockDim.x) {
-      if (H1 == r.H) break;  // no block leaves the window: no page is looked at
+  if (!p.err && p.H1 > p.H)
+    for (int pg = p.H / PAGE + (int)threadIdx.x; pg < (p.H1 + PAGE - 1) / PAGE; pg += blockDim.x) {
       const int id = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
       if (id < 0) bad |= 1;
       if (id >= cv.num_pages) bad |= 2;
@@ -168,99 +194,200 @@ __device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, in
   return p;
 }
 
-// T new tokens of request blockIdx.y.  Work is in units of one block of 16
-// positions, kv head and side, a warp each; unit 0 is the sink.
-//  - A block of new tokens only that falls out of the window at once is
-//    quantised straight from the input.
-//  - A block that stays is written to its ring slots.  The block that had the
-//    slots, if it leaves the window in this call, is quantised first by the
-//    same warp (its tokens from the ring, and from the input those it still
-//    lacked), so no other warp reads what this one overwrites.
-// With one CTA per request (SOLE) the CTA writes the lengths when all its
-// warps are done; else append_lengths_kernel does afterwards.
-template <int TYPE, bool SOLE>
-__global__ void __launch_bounds__(AW * 32, SOLE ? 1 : 2) append_kernel(Kv8Append a) {
-  pdl_wait();
-  pdl_launch_dependents();  // after the wait: append_lengths_kernel looks before its own
+// The plan in blocks of 16 positions.
+struct AppendBlocks {
+  int first, last;  // blocks with a new token
+  int old_last;     // last block with a token before the call
+  int h0, h1;       // history before and after
+};
+
+__device__ __forceinline__ AppendBlocks append_blocks(const AppendPlan& p) {
+  AppendBlocks k;
+  k.old_last = p.L > SINK ? (p.L - SINK - 1) / KV8_BLK : -1;
+  k.first = ((p.L > SINK ? p.L : SINK) - SINK) / KV8_BLK;
+  k.last = p.L1 > SINK ? (p.L1 - SINK - 1) / KV8_BLK : -1;
+  k.h0 = p.H / KV8_BLK;
+  k.h1 = p.H1 / KV8_BLK;
+  return k;
+}
+
+__device__ __forceinline__ float* block_weights(const Kv8Append& a, size_t head) {
+  return a.weights ? a.weights + head * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * a.cv.max_pages_per_req) : nullptr;
+}
+
+// A warp quantises one side of block `go` of (b, h) from rows Row(t).
+template <int TYPE, typename Row>
+__device__ __forceinline__ void quantise_block(const Kv8Append& a, int b, int h, int side, int go, int lane, Row row) {
+  SideRows S;
+  load_side(S, side, lane, row);
+  const int pid = a.cv.page_table[(size_t)b * a.cv.max_pages_per_req + go / KV8_PAGE_BLOCKS];
+  uint8_t* base = kv8_head(a.cv, pid, h);
+  const int sub = go % KV8_PAGE_BLOCKS;
+  quantise_side<TYPE>(S, side, base + sub * KV8_BLOCK_BYTES, (float*)(base + KV8_OFF_SCALES) + 2 * sub + side, lane);
+}
+
+// What stays in BF16: unit 0 is the sink, unit 1 + i block max(first, h1) + i of
+// the window; a warp each per kv head and side.  The block that had the ring
+// slots, if it leaves the window in this call, is quantised first by the same
+// warp (its tokens from the ring, and from the input those it still lacked), so
+// no other warp reads what this one overwrites.
+template <int TYPE>
+__device__ __forceinline__ void append_window(const Kv8Append& a, const AppendPlan& p, const AppendBlocks& kb, int b, int h,
+                                              int side, int unit, int lane) {
   const CacheView& cv = a.cv;
-  const int b = blockIdx.y, Hkv = cv.Hkv, T = a.T;
-  const AppendPlan p = append_plan(cv, b, T);
-  if (p.err) {
-    if (SOLE && threadIdx.x == 0) record_error(cv.err, p.err);
+  const int Hkv = cv.Hkv;
+  const size_t head = (size_t)b * Hkv + h, in_row = (size_t)Hkv * D;
+  const __nv_bfloat16* in = (side ? a.v : a.k) + ((size_t)b * a.T * Hkv + h) * D;  // token t at in + t Hkv D
+  if (unit == 0) {
+    __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
+    const int end = p.L1 < SINK ? p.L1 : SINK;
+    for (int t = p.L + (lane >> 4); t < end; t += 2)
+      ((uint4*)(sink + (size_t)t * D))[lane & 15] = ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int old_last = p.L > SINK ? (p.L - SINK - 1) / KV8_BLK : -1;    // last block with a token before the call
-  const int first = ((p.L > SINK ? p.L : SINK) - SINK) / KV8_BLK;       // first block with a new one
-  const int last = p.L1 > SINK ? (p.L1 - SINK - 1) / KV8_BLK : -1;
-  const int h0 = p.H / KV8_BLK, h1 = p.H1 / KV8_BLK;
-  const int units = 1 + (last >= first ? last - first + 1 : 0), width = 2 * Hkv;  // tasks: units x (kv head, side)
-  const size_t wrow = (size_t)KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req;
-  const uint32_t w0 = blockIdx.x * AW + warp, step = gridDim.x * AW;
-  const int step_u = (int)(step / width), step_s = (int)(step % width);
-  int unit = (int)(w0 / width), s = (int)(w0 % width);
-  for (; unit < units; unit += step_u, s += step_s) {
-    if (s >= width) {
-      s -= width;
-      if (++unit >= units) break;
-    }
-    const int side = s & 1, h = s >> 1, u = unit - 1;
-    const size_t head = (size_t)b * Hkv + h;
-    const __nv_bfloat16* in = (side ? a.v : a.k) + ((size_t)b * T * Hkv + h) * D;  // token t at in + t Hkv D
-    const size_t in_row = (size_t)Hkv * D;
-    __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
-    float* wts = a.weights ? a.weights + head * wrow : nullptr;
-    if (u < 0) {  // the sink
-      __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
-      const int end = p.L1 < SINK ? p.L1 : SINK;
-      for (int t = p.L + (lane >> 4); t < end; t += 2)
-        ((uint4*)(sink + (size_t)t * D))[lane & 15] = ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
-      continue;
-    }
-    const int k = first + u;
-    int go = -1;  // the block to quantise
-    if (k < h1) {
-      if (k > old_last) go = k;
-    } else {
-      const int o = k - ((k - h0) & ~(KV8_RING_BLOCKS - 1));  // the block of [h0, h0 + 16) with k's ring slots
-      if (o < k && o <= old_last) go = o;
-    }
-    if (go >= 0) {
-      SideRows S;
-      const int pos = SINK + go * KV8_BLK;
-      load_side(S, side, lane, [&](int t) {
-        const int q = pos + t;
-        return q < p.L ? (const __nv_bfloat16*)(ring + (size_t)((q - SINK) & (RECENT - 1)) * D)
-                       : in + (size_t)(q - p.L) * in_row;
-      });
-      const int pid = cv.page_table[(size_t)b * cv.max_pages_per_req + go / KV8_PAGE_BLOCKS];
-      uint8_t* base = kv8_head(cv, pid, h);
-      const int sub = go % KV8_PAGE_BLOCKS;
-      quantise_side<TYPE>(S, side, base + sub * KV8_BLOCK_BYTES, (float*)(base + KV8_OFF_SCALES) + 2 * sub + side, lane);
-      if (wts && side == 0 && lane == 0)
-        wts[KV8_RING_BLOCKS + go] = go <= old_last ? wts[go & (KV8_RING_BLOCKS - 1)] : 0.f;
-    }
-    if (k >= h1) {
-      __syncwarp();  // every lane has read its rows of the block that leaves
-      const int p0 = SINK + k * KV8_BLK;
-      const int from = p0 > p.L ? p0 : p.L, to = p0 + KV8_BLK < p.L1 ? p0 + KV8_BLK : p.L1;
-      for (int t = from + (lane >> 4); t < to; t += 2)
-        ((uint4*)(ring + (size_t)((t - SINK) & (RECENT - 1)) * D))[lane & 15] =
-            ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
-      if (wts && side == 0 && lane == 0 && k > old_last) wts[k & (KV8_RING_BLOCKS - 1)] = 0.f;
-    }
+  __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
+  float* wts = block_weights(a, head);
+  const int k = (kb.first > kb.h1 ? kb.first : kb.h1) + unit - 1;
+  const int o = k - ((k - kb.h0) & ~(KV8_RING_BLOCKS - 1));  // the block of [h0, h0 + 16) with k's ring slots
+  if (o < k && o <= kb.old_last) {
+    const int pos = SINK + o * KV8_BLK;
+    quantise_block<TYPE>(a, b, h, side, o, lane, [&](int t) {
+      const int q = pos + t;
+      return q < p.L ? (const __nv_bfloat16*)(ring + (size_t)((q - SINK) & (RECENT - 1)) * D)
+                     : in + (size_t)(q - p.L) * in_row;
+    });
+    if (wts && side == 0 && lane == 0) wts[KV8_RING_BLOCKS + o] = wts[o & (KV8_RING_BLOCKS - 1)];
+    __syncwarp();  // every lane has read its rows of the block that leaves
   }
-  if (SOLE) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      cv.seq_lens[b] = p.L1;
-      cv.hist_lens[b] = p.H1;
-    }
+  const int p0 = SINK + k * KV8_BLK;
+  const int from = p0 > p.L ? p0 : p.L, to = p0 + KV8_BLK < p.L1 ? p0 + KV8_BLK : p.L1;
+  for (int t = from + (lane >> 4); t < to; t += 2)
+    ((uint4*)(ring + (size_t)((t - SINK) & (RECENT - 1)) * D))[lane & 15] =
+        ((const uint4*)(in + (size_t)(t - p.L) * in_row))[lane & 15];
+  if (wts && side == 0 && lane == 0 && k > kb.old_last) wts[k & (KV8_RING_BLOCKS - 1)] = 0.f;
+}
+
+__device__ __forceinline__ int window_units_of(const AppendBlocks& k) {
+  const int from = k.first > k.h1 ? k.first : k.h1;
+  return 1 + (k.last >= from ? k.last - from + 1 : 0);
+}
+
+// Fewer than 256 tokens (so that none of them can leave the window in the call
+// that brings it) and few tasks: one CTA per request, which writes the lengths
+// when all its warps are done.  blockIdx.x: the request.
+template <int TYPE>
+__global__ void __launch_bounds__(AW * 32) append_small_kernel(Kv8Append a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x;
+  const AppendPlan p = append_plan(a.cv, b, a.T);
+  if (p.err) {
+    if (threadIdx.x == 0) record_error(a.cv.err, p.err);
+    return;
+  }
+  const AppendBlocks kb = append_blocks(p);
+  const int tasks = window_units_of(kb) * a.cv.Hkv * 2;
+  for (int w = threadIdx.x >> 5; w < tasks; w += AW)
+    append_window<TYPE>(a, p, kb, b, (w >> 1) % a.cv.Hkv, w & 1, (w >> 1) / a.cv.Hkv, threadIdx.x & 31);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    a.cv.seq_lens[b] = p.L1;
+    a.cv.hist_lens[b] = p.H1;
   }
 }
 
-// After append_kernel<.., false>, which leaves the lengths as they are: the plan is
-// made again while that still runs.
+// Any number of tokens (blockIdx.y: the request).  The first gridDim.x - spans CTAs
+// do the window; the others AP_SHARE tasks per warp of the blocks that fall out
+// of the window at once: they have new tokens only and are quantised straight
+// from the input, a warp per block, kv head and side.  Each warp copies its next
+// rows to shared memory (cp.async, AP_DEPTH tasks ahead) while it works on the
+// present ones.  CTAs are small and many, two to an SM: SMs differ in how fast
+// the memory serves them, and one even share for each SM left a fifth of the
+// time idle.  append_lengths_kernel writes the lengths.
+// A request that is refused keeps its window and lengths; places behind the end
+// of its history may have been written.
+constexpr int PW = 8;        // warps per CTA
+constexpr int AP_SHARE = 8;  // tasks per warp
+constexpr int AP_DEPTH = 3;
+constexpr int AP_ROW = D * 2 + 16;             // a row's place: rows start in different banks
+constexpr int AP_STAGE = KV8_BLK * AP_ROW;
+
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(PW * 32, 2) append_kernel(Kv8Append a, int spans) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_wait();
+  pdl_launch_dependents();  // after the wait: append_lengths_kernel looks before its own
+  const CacheView& cv = a.cv;
+  const int b = blockIdx.y, Hkv = cv.Hkv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int windows = gridDim.x - spans;
+  if ((int)blockIdx.x < windows) {
+    const AppendPlan p = append_plan(cv, b, a.T);
+    if (p.err) return;
+    const AppendBlocks kb = append_blocks(p);
+    const int tasks = window_units_of(kb) * Hkv * 2;
+    for (int w = blockIdx.x * PW + warp; w < tasks; w += windows * PW)
+      append_window<TYPE>(a, p, kb, b, (w >> 1) % Hkv, w & 1, (w >> 1) / Hkv, lane);
+    return;
+  }
+  const AppendPlan p = append_lengths(cv, b, a.T);
+  if (p.err) return;
+  const AppendBlocks kb = append_blocks(p);
+  const int d0 = kb.h0 > kb.old_last + 1 ? kb.h0 : kb.old_last + 1;  // blocks d0 .. h1 - 1 come from the input alone
+  const size_t in_row = (size_t)Hkv * D;
+  // task i of the span and warp: block d0 + (its number) / (2 Hkv), 2 head + side the rest
+  const int width = 2 * Hkv;
+  const long long t0 = (long long)(blockIdx.x - windows) * (PW * AP_SHARE) + warp;
+  struct Task {
+    int k, s;
+  };
+  auto forward = [&](Task& t) {
+    t.k += PW / width;
+    t.s += PW % width;
+    if (t.s >= width) {
+      t.s -= width;
+      ++t.k;
+    }
+  };
+  uint8_t* ring = smem + warp * AP_DEPTH * AP_STAGE;
+  auto fetch = [&](const Task& t, int i) {
+    if (i < AP_SHARE && t.k < kb.h1) {
+      const __nv_bfloat16* src = (t.s & 1 ? a.v : a.k) +
+                                 ((size_t)b * a.T + (SINK + t.k * KV8_BLK - p.L)) * in_row + (size_t)(t.s >> 1) * D;
+      uint8_t* dst = ring + i % AP_DEPTH * AP_STAGE;
+#pragma unroll
+      for (int r = 0; r < KV8_BLK; r += 2) {
+        const int row = r + (lane >> 4);
+        copy16_async(dst + row * AP_ROW + 16 * (lane & 15), (const uint8_t*)(src + row * in_row) + 16 * (lane & 15));
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");  // (an empty one past the end, so that the count holds)
+  };
+  Task now = {d0 + (int)(t0 / width), (int)(t0 % width)}, next = now;
+#pragma unroll 1
+  for (int i = 0; i < AP_DEPTH - 1; ++i, forward(next)) fetch(next, i);
+#pragma unroll 1
+  for (int i = 0; i < AP_SHARE && now.k < kb.h1; ++i, forward(now), forward(next)) {
+    fetch(next, i + AP_DEPTH - 1);
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(AP_DEPTH - 1) : "memory");
+    __syncwarp();
+    const uint8_t* st = ring + i % AP_DEPTH * AP_STAGE;
+    const int h = now.s >> 1, side = now.s & 1;
+    const int pid = cv.page_table[(size_t)b * cv.max_pages_per_req + now.k / KV8_PAGE_BLOCKS];
+    if (pid >= 0 && pid < cv.num_pages) {
+      quantise_block<TYPE>(a, b, h, side, now.k, lane, [&](int t) { return (const __nv_bfloat16*)(st + t * AP_ROW); });
+      if (side == 0 && lane == 0)
+        if (float* wts = block_weights(a, (size_t)b * Hkv + h)) wts[KV8_RING_BLOCKS + now.k] = 0.f;
+    }
+    __syncwarp();  // every lane has read the stage
+  }
+}
+
+// After append_kernel, which leaves the lengths as they are: the plan is made
+// again while that still runs.
 __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
   pdl_launch_dependents();
   const AppendPlan p = append_plan(a.cv, blockIdx.x, a.T);
@@ -492,22 +619,28 @@ __global__ void __launch_bounds__(256) evict_move_kernel(Kv8Evict a) {
 
 }  // namespace
 
-cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, int num_sms, cudaStream_t st, Profiler* prof) {
-  const long long units = ((long long)a.T + KV8_BLK - 2) / KV8_BLK + 1 + 1;  // blocks a call can touch, and the sink
-  const long long ctas = (units * a.cv.Hkv * 2 + AW - 1) / AW;
-  cudaError_t e;
+template <int TYPE>
+static cudaError_t launch_append_type(const Kv8Append& a, int B, cudaStream_t st) {
+  const long long tasks = (((long long)a.T + KV8_BLK - 2) / KV8_BLK + 2) * a.cv.Hkv * 2;  // blocks a call can touch, and the sink
+  // one launch while a CTA's warps have two tasks at most (a step with 8 kv heads:
+  // 3.7 us against 6.1; a chunk of 64 has twelve each, and takes the other)
+  if (a.T < RECENT && tasks <= 2 * AW) return launch_pdl(append_small_kernel<TYPE>, dim3(B), dim3(AW * 32), 0, st, a);
+  // at most 17 blocks and the sink of the window; 256 tokens or fewer cannot leave it at once
+  const int windows = (18 * a.cv.Hkv * 2 + PW - 1) / PW;
+  const long long direct = a.T <= RECENT ? 0 : (long long)(a.T / KV8_BLK) * a.cv.Hkv * 2;
+  const int spans = (int)((direct + PW * AP_SHARE - 1) / (PW * AP_SHARE));
+  static int limit[MAX_DEVICES];
+  cudaError_t e = raise_smem_limit(append_kernel<TYPE>, limit, PW * AP_DEPTH * AP_STAGE);
+  if (e == cudaSuccess)
+    e = launch_pdl(append_kernel<TYPE>, dim3(windows + spans, B), dim3(PW * 32), PW * AP_DEPTH * AP_STAGE, st, a, spans);
+  if (e == cudaSuccess) e = launch_pdl(append_lengths_kernel, dim3(B), dim3(128), 0, st, a);
+  return e;
+}
+
+cudaError_t launch_kv8_append(const Kv8Append& a, int type, int B, cudaStream_t st, Profiler* prof) {
   prof_begin(prof, OSCAR_KERNEL_KV8_APPEND, st);
-  if (ctas <= 2) {
-    e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, true>, dim3(1, B), dim3(AW * 32), 0, st, a)
-                               : launch_pdl(append_kernel<OSCAR_KV8_INT8, true>, dim3(1, B), dim3(AW * 32), 0, st, a);
-  } else {
-    long long x = (2LL * num_sms + B - 1) / B;  // CTAs that run at once
-    if (x > ctas) x = ctas;
-    const dim3 grid((unsigned)x, B);
-    e = type == OSCAR_KV8_E4M3 ? launch_pdl(append_kernel<OSCAR_KV8_E4M3, false>, grid, dim3(AW * 32), 0, st, a)
-                               : launch_pdl(append_kernel<OSCAR_KV8_INT8, false>, grid, dim3(AW * 32), 0, st, a);
-    if (e == cudaSuccess) e = launch_pdl(append_lengths_kernel, dim3(B), dim3(128), 0, st, a);
-  }
+  const cudaError_t e = type == OSCAR_KV8_E4M3 ? launch_append_type<OSCAR_KV8_E4M3>(a, B, st)
+                                               : launch_append_type<OSCAR_KV8_INT8>(a, B, st);
   prof_end(prof, OSCAR_KERNEL_KV8_APPEND, st);
   return e;
 }
