@@ -570,6 +570,23 @@ def bind_decode_kv8(ctx, cache: dict, kv_type, q, out, lse, scratch, batch, weig
     return call
 
 
+def bind_step_kv8(ctx, cache: dict, kv_type, out, lse, scratch, weights=None, decay=1.0, stream=None):
+    """One decode step over 8-bit history (oscar_append_kv8 of one token, then
+    oscar_decode_kv8) with the cache and outputs marshalled once: returns
+    f(k_ptr, v_ptr, q_ptr, batch) taking raw addresses."""
+    cs = _cache_struct(cache)
+    csr, w, st = ctypes.byref(cs), _ptr(weights), _stream(stream)
+    o, ls, sc, nb = _ptr(out), _ptr(lse), _ptr(scratch), scratch.numel() * scratch.element_size()
+    fa, fd = lib().oscar_append_kv8, lib().oscar_decode_kv8
+
+    def call(k_ptr: int, v_ptr: int, q_ptr: int, batch: int):
+        _check(fa(ctx, csr, kv_type, k_ptr, v_ptr, 1, w, batch, st), "oscar_append_kv8")
+        _check(fd(ctx, csr, kv_type, q_ptr, o, ls, w, decay, sc, nb, batch, st), "oscar_decode_kv8")
+
+    call._keep = cs
+    return call
+
+
 def bind_evict_kv8(ctx, cache: dict, weights, budget, scratch, batch, stream=None):
     """oscar_evict_kv8 with every argument marshalled once: returns a
     no-argument callable."""

@@ -550,7 +550,8 @@ oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* ou
  *   weights : block weights, or NULL
  * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad page
  * among those that take the blocks, or too many pages; the request is then
- * left unchanged. */
+ * left unchanged (places behind the end of its history, in good pages, may have
+ * been written). */
 oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* k_new,
                               const void* v_new, int T, float* weights, int batch, oscar_stream_t stream);
 

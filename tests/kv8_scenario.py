@@ -18,8 +18,9 @@ class Pair:
         self.ctx = oscar.oscar_create(self.cfg)
         self.g = torch.Generator().manual_seed(seed)
         self.cache = oscar.alloc_cache(self.cfg, kv8=True)
-        ids = torch.randperm(npg, generator=self.g).int()[:mb * pages]
-        self.cache["page_table"].copy_(ids.view(mb, pages))
+        if npg >= mb * pages:  # else the test hands out the pages
+            ids = torch.randperm(npg, generator=self.g).int()[:mb * pages]
+            self.cache["page_table"].copy_(ids.view(mb, pages))
         if dirty:  # NaN patterns wherever no token is: bf16 NaN, e4m3 NaN, fp32 NaN
             for x in ("pool", "sink_k", "sink_v", "ring_k", "ring_v"):
                 self.cache[x].view(torch.uint8).fill_(0xFF)

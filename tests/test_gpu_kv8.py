@@ -341,3 +341,358 @@ def test_evict_refuses_bad_pages(kind=oscar.KV8_E4M3):
         assert bool(same)
     finally:
         p.close()
+
+
+# -------------------------------------------------------- as they would be used
+def advance(p, T, q, decay, budget, call=None):
+    """One turn on both sides: append, attend, evict when due; the eviction goes by the device's weights."""
+    p.append(T, call=call)
+    out, lse = p.decode(q, decay)
+    worst = check_decode(p, q, out, lse, decay)
+    if any(r.H - budget >= 256 for r in p.req):
+        w = p.weights.cpu().numpy()
+        oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, budget, p.scratch, p.B)
+        for b, r in enumerate(p.req):
+            r.evict(budget, w[b, :, 16:])
+    return worst
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_decode_evict_together(kind):
+    """A few hundred tokens in steps and chunks, attended to and evicted, stay
+    with the oracle: state bit for bit, weights within the roundings added up."""
+    p = Pair(kind, 2, 4, 3, 14, seed=21)
+    try:
+        worst = 0.0
+        for T in (500, 1, 1, 1, 60, 1, 30, 1, 200, 1, 1, 17, 1, 250, 1, 1, 90, 1):
+            worst += advance(p, T, p.query(1.2), 0.95, 300)
+            p.check_state(weight_tol=2 * worst)
+        assert all(r.H < 300 + 256 for r in p.req) and all(r.L < 1000 for r in p.req)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_captured_steps_replay(kind=oscar.KV8_INT8):
+    """A decode step and an eviction captured once and replayed many times
+    follow the lengths on the device, on a stream of their own."""
+    p = Pair(kind, 2, 2, 2, 14, seed=22)
+    try:
+        p.append(590)
+        k, v = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16).cuda(), torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16).cuda()
+        q = p.query().cuda()
+        out = torch.empty_like(q)
+        lse = torch.empty(2, 4, dtype=torch.float32, device="cuda")
+        st = torch.cuda.Stream()
+        g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        before = {x: p.cache[x].clone() for x in p.cache}
+        with torch.cuda.stream(st):
+            with torch.cuda.graph(g1, stream=st):
+                oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, 1, 2, weights=p.weights)
+                oscar.oscar_decode_kv8(p.ctx, p.cache, kind, q, out, lse, p.scratch, 2, weights=p.weights, decay=0.9)
+            with torch.cuda.graph(g2, stream=st):
+                oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, 256, p.scratch, 2)
+        torch.cuda.synchronize()
+        assert torch.equal(p.cache["seq_lens"], before["seq_lens"])  # capturing ran nothing
+        worst = 0.0
+        for i in range(300):
+            kn, vn = p.draw(1)
+            qn = p.query()
+            with torch.cuda.stream(st):
+                k.copy_(kn)
+                v.copy_(vn)
+                q.copy_(qn)
+                g1.replay()
+            for b, r in enumerate(p.req):
+                r.append(kn[b, 0].double().numpy(), vn[b, 0].double().numpy())
+            st.synchronize()
+            worst += check_decode(p, qn, out, lse, 0.9)
+            if p.req[0].H >= 512:
+                w = p.weights.cpu().numpy()
+                with torch.cuda.stream(st):
+                    g2.replay()
+                for b, r in enumerate(p.req):
+                    r.evict(256, w[b, :, 16:])
+        st.synchronize()
+        p.check_state(weight_tol=2 * worst)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_two_calls_at_once_on_two_streams(kind=oscar.KV8_E4M3):
+    """Different caches of one context on two streams, each with its own scratch."""
+    a = lengths_pair(kind, 2, 4, [4000, 900], seed=31)
+    b = Pair(kind, 2, 4, 2, a.pages, seed=32)
+    try:
+        b.append(2000)
+        sb = oscar.alloc_scratch_kv8(a.cfg)
+        qa, qb = a.query(), b.query()
+        oa, ob = qa.cuda(), qb.cuda()
+        la, lb = (torch.empty(2, 8, dtype=torch.float32, device="cuda") for _ in range(2))
+        da, db = oa.clone(), ob.clone()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            oscar.oscar_decode_kv8(a.ctx, a.cache, kind, da, oa, la, a.scratch, 2, stream=s1)
+            oscar.oscar_decode_kv8(a.ctx, b.cache, kind, db, ob, lb, sb, 2, stream=s2)
+        torch.cuda.synchronize()
+        check_decode(a, qa, oa, la)
+        check_decode(b, qb, ob, lb)
+        ok(a)
+    finally:
+        a.close()
+        b.close()
+
+
+def test_rows_behind_the_batch_stay(kind=oscar.KV8_INT8):
+    p = Pair(kind, 2, 2, 2, 12, seed=41, max_batch=4)
+    try:
+        p.cache["seq_lens"][2:] = 700
+        p.cache["hist_lens"][2:] = 384
+        p.weights[2:] = 3.0
+        keep = {x: p.cache[x][2:].clone() for x in p.cache if x not in ("pool", "page_table")}
+        mine = p.cache["page_table"][2:].reshape(-1).long()
+        pages = p.cache["pool"].view(p.cfg.num_pages, -1)[mine].clone()
+        for T in (600, 1, 300):
+            p.append(T)
+            q = p.query()
+            out = torch.full((4, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((4, 4), 7.0, device="cuda")
+            qd = torch.cat([q.cuda(), torch.zeros_like(q.cuda())])
+            oscar.oscar_decode_kv8(p.ctx, p.cache, kind, qd, out, lse, p.scratch, 2, weights=p.weights)
+            check_decode(p, q, out[:2], lse[:2], 1.0)
+            assert bool((out[2:] == 7).all()) and bool((lse[2:] == 7).all())
+        w = p.weights.cpu().numpy()
+        oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, 100, p.scratch, 2)
+        for b, r in enumerate(p.req):
+            r.evict(100, w[b, :, 16:])
+        p.check_state(weight_tol=1e-3)
+        for x in keep:
+            assert torch.equal(p.cache[x][2:].view(torch.uint8), keep[x].view(torch.uint8)), x
+        assert bool((p.weights[2:] == 3).all())
+        assert torch.equal(p.cache["pool"].view(p.cfg.num_pages, -1)[mine], pages)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_pinned_host_operands(kind=oscar.KV8_E4M3):
+    p = Pair(kind, 2, 2, 2, 12, seed=51)
+    try:
+        for T in (400, 1, 300):
+            k, v = p.draw(T)
+            p.append(T, (k, v), call=lambda k, v: oscar.oscar_append_kv8(
+                p.ctx, p.cache, kind, k.pin_memory(), v.pin_memory(), T, 2, weights=p.weights) or torch.cuda.synchronize())
+        p.check_state()
+        q = p.query()
+        out, lse = torch.empty_like(q).pin_memory(), torch.empty(2, 4).pin_memory()
+        oscar.oscar_decode_kv8(p.ctx, p.cache, kind, q.pin_memory(), out, lse, p.scratch, 2)
+        torch.cuda.synchronize()
+        check_decode(p, q, out, lse)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_batches_beyond_one_launch(kind=oscar.KV8_INT8):
+    """1100 requests: two launches of at most 1024, one after the other over one scratch."""
+    B = 1100
+    p = Pair(kind, 1, 1, B, 2, seed=61)
+    try:
+        g = torch.Generator(device="cuda").manual_seed(1)
+        for T in (340, 3):
+            k, v = (torch.randn(B, T, 1, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+            oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, T, B, weights=p.weights)
+        assert p.cache["seq_lens"].unique().tolist() == [343] and p.cache["hist_lens"].unique().tolist() == [32]
+        before = p.weights.clone()
+        q = p.query()
+        out, lse = p.decode(q, 0.5)
+        pick = [0, 1, 1022, 1023, 1024, 1025, B - 1]
+        few = Pair.__new__(Pair)
+        few.__dict__.update(p.__dict__)
+        few.B = len(pick)
+        few.cache = {x: p.cache[x][pick] if x != "pool" else p.cache[x] for x in p.cache}
+        few.weights = p.weights[pick]
+        check_decode_dense(few, q[pick], out[pick], lse[pick], before[pick], 0.5)
+        oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, 0, p.scratch, B)  # 32 tokens of history: nothing to do
+        assert p.cache["hist_lens"].unique().tolist() == [32]
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_weights_of_a_batch_in_several_launches(kind=oscar.KV8_E4M3):
+    """With weights the scratch is kept near 64 MB: long page tables split the batch."""
+    lens = [700, 40, 3000, 500, 321, 1200, 0, 900, 2000]
+    p = Pair(kind, 8, 8, len(lens), 6000, seed=71, num_pages=200)
+    try:
+        ids = torch.randperm(200, generator=p.g).int().cuda()
+        at = 0
+        for b, n in enumerate(lens):
+            m = -(-max(n - 320 + 15, 0) // 64)
+            p.cache["page_table"][b, :m] = ids[at:at + m]
+            at += m
+            if n:
+                k, v = p.draw(n, B=1)
+                row = {x: p.cache[x][b:b + 1] if x != "pool" else p.cache[x] for x in p.cache}
+                oscar.oscar_append_kv8(p.ctx, row, kind, k.cuda(), v.cuda(), n, 1, weights=p.weights[b:b + 1])
+        for decay in (1.0, 0.5):
+            before = p.weights.clone()
+            q = p.query()
+            out, lse = p.decode(q, decay)
+            check_decode_dense(p, q, out, lse, before, decay)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_pool_beyond_four_gigabytes(kind=oscar.KV8_INT8):
+    p = Pair(kind, 8, 4, 1, 40, seed=81, num_pages=36000, dirty=False)
+    try:
+        assert p.cache["pool"].numel() > 1 << 32
+        p.cache["page_table"][0] = torch.arange(36000 - 40, 36000).int().cuda()
+        p.append(1500)
+        q = p.query()
+        out, lse = p.decode(q)
+        check_decode(p, q, out, lse, 1.0)
+        w = p.weights.cpu().numpy()
+        oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, 500, p.scratch, 1)
+        p.req[0].evict(500, w[0, :, 16:])
+        p.check_state(weight_tol=1e-4)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_a_wait_that_runs_out_is_reported(kind=oscar.KV8_INT8):
+    p = lengths_pair(kind, 2, 2, [5000, 300], seed=91)
+    try:
+        q = p.query()
+        oscar.oscar_set_option(p.ctx, oscar.OPT_WAIT_POLLS, 0)
+        p.decode(q, weights=False)
+        assert oscar.oscar_get_error(p.ctx) == oscar.ERR_TIMEOUT
+        oscar.oscar_set_option(p.ctx, oscar.OPT_WAIT_POLLS, oscar.WAIT_POLLS_DEFAULT)
+        out, lse = p.decode(q, weights=False)
+        check_decode(p, q, out, lse)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_refusals():
+    p = Pair(oscar.KV8_INT8, 2, 2, 2, 4)
+    try:
+        k = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+        q = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+        out, lse, w, sc = torch.empty_like(q), torch.empty(2, 4, device="cuda"), p.weights, p.scratch
+        bad = oscar.ERR_INVALID_ARG
+
+        def refused(f, *a, status=bad, **kw):
+            with pytest.raises(oscar.OscarError) as e:
+                f(p.ctx, *a, **kw)
+            assert e.value.status == status
+
+        ap, de, ev = oscar.oscar_append_kv8, oscar.oscar_decode_kv8, oscar.oscar_evict_kv8
+        c = p.cache
+        odd = torch.zeros(2 * 2 * 128 + 8, dtype=torch.bfloat16, device="cuda")[1:]
+        refused(ap, c, 2, k, k, 1, 2)                      # type
+        refused(ap, c, -1, k, k, 1, 2)
+        refused(ap, c, 1, None, k, 1, 2)
+        refused(ap, c, 1, k, odd, 1, 2)                    # alignment
+        refused(ap, c, 1, k, k, -1, 2)
+        refused(ap, c, 1, k, k, (1 << 24) + 1, 2)
+        refused(ap, c, 1, k, k, 1, 3)                      # batch
+        refused(ap, c, 1, k, k, 1, -1)
+        refused(ap, c, 1, k, k, 1, 2, weights=w.view(-1)[1:])
+        refused(ap, {**c, "pool": None}, 1, k, k, 1, 2)
+        refused(ap, {**c, "hist_lens": None}, 1, k, k, 1, 2)
+        refused(de, c, 3, q, out, lse, sc, 2)
+        refused(de, c, 1, None, out, lse, sc, 2)
+        refused(de, c, 1, q, None, lse, sc, 2)
+        refused(de, c, 1, q, out, lse, sc[256:512], 2)     # too small
+        refused(de, c, 1, q, out, lse, sc[16:], 2)         # alignment
+        refused(de, c, 1, q, out, lse, sc, 3)
+        for decay in (-0.5, float("nan"), float("inf")):
+            refused(de, c, 1, q, out, lse, sc, 2, weights=w, decay=decay)
+        refused(ev, c, None, 0, sc, 2)
+        refused(ev, c, w, -1, sc, 2)
+        refused(ev, c, w, 0, sc[256:272], 2)
+        refused(ev, c, w, 0, sc, 3)
+        assert p.cache["seq_lens"].tolist() == [0, 0]
+        ap(p.ctx, c, 1, k, k, 0, 2)                        # nothing to do is fine
+        ap(p.ctx, c, 1, k, k, 1, 0)
+        de(p.ctx, c, 1, q, out, None, sc, 0)
+        ev(p.ctx, c, w, 0, sc, 0)
+        de(p.ctx, c, 1, q, out, None, sc, 2)               # empty requests, no lse
+        assert bool((out == 0).all())
+        ok(p)
+    finally:
+        p.close()
+
+
+@pytest.mark.parametrize("fmt,budget", [("e4m3", None), ("int8", 320), ("int8", 0)])
+def test_serving_loop(fmt, budget):
+    """Requests admitted, stepped together, moved between slots, evicted and
+    retired by the serving loop: every output within rounding of the oracle."""
+    from bit_kv_cache_int2_gb300 import serving
+    from oracle import kv8_oracle as K8
+
+    Hkv, G, max_batch, pool_pages = 2, 2, 4, 40
+    kind = serving.KV8_KINDS[fmt]
+    rng = np.random.default_rng(3)
+    reqs = [serving.Request(rid=i, prefix=int(rng.integers(0, 1300)), gen=int(rng.integers(20, 340))) for i in range(7)]
+    need = lambda prefix, gen: serving.pages_needed_kv8(prefix, gen, budget=budget)  # noqa: E731
+    mpr = max(need(r.prefix, r.gen) for r in reqs)
+    cfg = oscar.make_config(1, Hkv * G, Hkv, max_batch=max_batch, max_pages_per_req=mpr, num_pages=pool_pages)
+    ctx = oscar.oscar_create(cfg)
+    cache = oscar.alloc_cache(cfg, kv8=True)
+    streams, oracles, evictions = {}, {}, [0]
+
+    def draw(req):
+        g = torch.Generator().manual_seed(req.rid)
+        n = req.prefix + req.gen
+        K, V = (torch.randn(Hkv, n, 128, generator=g).bfloat16() for _ in range(2))
+        Q = torch.randn(req.gen, Hkv * G, 128, generator=g).bfloat16()
+        streams[req.rid] = (K.double().numpy(), V.double().numpy())
+        o = oracles[req.rid] = K8.Request(Hkv, kind)
+        for t in range(req.prefix):
+            o.append(streams[req.rid][0][:, t], streams[req.rid][1][:, t])
+        return K.cuda(), V.cuda(), Q.cuda()
+
+    class View:  # what check_decode needs
+        pass
+
+    def on_step(active, q, out):
+        v = View()
+        v.B, v.Hkv, v.G, v.req = len(active), Hkv, G, [oracles[r.rid] for r in active]
+        for r in active:
+            t = r.prefix + r.done
+            oracles[r.rid].append(streams[r.rid][0][:, t], streams[r.rid][1][:, t])
+        if sched.steps % 9 == 0:
+            lse = torch.zeros(len(active), Hkv * G)
+            for b, r in enumerate(v.req):
+                lse[b] = torch.from_numpy(r.attend(q[b].double().cpu().numpy().reshape(Hkv, G, 128))[1].reshape(-1)).float()
+            check_decode(v, q.cpu(), out, lse)
+
+    def on_evict(active):
+        evictions[0] += 1
+        w = backend.weights.cpu().numpy()
+        for b, r in enumerate(active):
+            oracles[r.rid].evict(budget, w[b, :, 16:])
+
+    try:
+        backend = serving.DeviceBackend(fmt, ctx, cfg, cache, draw, on_step=on_step, budget=budget, on_evict=on_evict)
+        sched = serving.Scheduler(serving.PagePool(pool_pages), max_batch, backend, mpr, need)
+        for r in reqs:
+            sched.submit(r)
+        done = sched.run()
+        assert oscar.oscar_get_error(ctx) == 0
+        assert sorted(r.rid for r in done) == list(range(len(reqs)))
+        assert sched.pool.available == pool_pages and len(set(sched.pool._free)) == pool_pages
+        assert (evictions[0] > 0) == (budget is not None)
+        with pytest.raises(ValueError):
+            serving.DeviceBackend("int2", ctx, cfg, cache, draw, budget=3)
+    finally:
+        oscar.oscar_destroy(ctx)

@@ -87,3 +87,58 @@ def test_oracle_window_holds_241_to_256_tokens_once_full():
         assert r.L == n and r.H % 16 == 0
         assert r.H == max(0, -(-(n - 320) // 16) * 16)
         assert len(r.window) <= 256
+
+
+def test_serving_page_account_covers_every_step():
+    """pages_needed_kv8 is the largest page count along the way, with and
+    without a budget, by playing the rule step by step."""
+    import random
+
+    from bit_kv_cache_int2_gb300.serving import kv8_history, pages_needed_kv8
+
+    rng = random.Random(0)
+    for _ in range(300):
+        prefix, gen = rng.randint(0, 3000), rng.randint(1, 1500)
+        budget = rng.choice([None, 0, rng.randint(0, 2500)])
+        L, H = prefix, kv8_history(prefix)
+        peak = H
+        for _ in range(gen):
+            L += 1
+            H = max(H, kv8_history(L))
+            peak = max(peak, H)
+            if budget is not None and H - budget >= 256:
+                gone = (H - budget) // 256 * 256
+                L, H = L - gone, H - gone
+        want = pages_needed_kv8(prefix, gen, budget=budget)
+        assert -(-peak // 64) <= want, (prefix, gen, budget)
+        if budget is None:
+            assert want == -(-peak // 64)
+
+
+def test_scheduler_returns_pages_a_backend_no_longer_needs():
+    from bit_kv_cache_int2_gb300.serving import PagePool, Request, Scheduler
+
+    class Shrinking:
+        def __init__(self):
+            self.left = {}
+
+        def admit(self, slot, req):
+            self.left[slot] = len(req.pages)
+
+        def move(self, src, dst):
+            self.left[dst] = self.left.pop(src)
+
+        def step(self, active):
+            for slot in range(len(active)):
+                self.left[slot] = max(1, self.left[slot] - 1)
+
+        def kept_pages(self, slot):
+            return self.left[slot]
+
+    pool = PagePool(12)
+    sched = Scheduler(pool, 2, Shrinking(), 16, need=lambda prefix, gen: 6)
+    for i in range(5):
+        sched.submit(Request(rid=i, prefix=0, gen=4 + i))
+    done = sched.run()
+    assert sorted(r.rid for r in done) == list(range(5))
+    assert pool.available == 12 and len(set(pool._free)) == 12
