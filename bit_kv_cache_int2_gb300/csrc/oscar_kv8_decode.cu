@@ -74,7 +74,9 @@ constexpr int WROW = D * 2;
 constexpr int STAGE_BYTES = (KV8_HEAD_BYTES + 127) / 128 * 128;
 static_assert(STAGE_BYTES >= 64 * WROW, "a window unit fits a stage");
 constexpr int MAX_STAGES = 13;
-constexpr int SMEM_LIMIT = 227 * 1024;
+// An SM has 228 KB: two of the merge's CTAs fit beside a decode CTA, so that the
+// merge can plan while the decode runs, and the next decode start under the merge.
+constexpr int SMEM_LIMIT = 215 * 1024;
 
 // ------------------------------------------------------------------ the math
 struct State {
@@ -686,12 +688,14 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
 }
 
 // -------------------------------------------------------------------- merge
-// grid (B Hkv, G + slices of the weights): CTA y < G writes the output of the
-// kv head's query head y, the others update a slice of the block weights.
+// grid (B Hkv, G / heads + slices of the weights), heads = 2^log_heads: the first CTAs
+// write the output of `heads` query heads each, MT / 32 / heads warps to a head; the others update
+// a slice of the block weights.
 // What is in the records of a (request, kv head) follows from the lengths, so
 // it is worked out while the decode kernel still runs.
-__global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
+__global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_heads) {
   __shared__ __align__(16) float wo[MT / 32][D];
+  __shared__ float scale[MT / 32];
   __shared__ float tot_m[MAX_G], tot_r[MAX_G];
   const CacheView& cv = a.cv;
   const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv, G = cv.G;
@@ -717,13 +721,17 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   }
   pdl_wait();
   const float* recs = a.part + ((size_t)i0 + seg) * G * PART_STRIDE;
-  if (blockIdx.y < G) {
-    const float* rec = recs + blockIdx.y * PART_STRIDE;
+  const int heads = 1 << log_heads, outs = G >> log_heads;
+  if ((int)blockIdx.y < outs) {
+    const int per = (MT / 32) >> log_heads;  // warps to a head
+    const int own_hd = (warp << log_heads) / (MT / 32), first = warp & (per - 1);
+    const int hd = (blockIdx.y << log_heads) + own_hd;
+    const float* rec = recs + hd * PART_STRIDE;
     const size_t stride = (size_t)G * PART_STRIDE;
     float4 y[4];  // the warp's first records, while the maxima are found
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = warp + j * (MT / 32);
+      const int i = first + j * per;
       y[j] = i < n ? *(const float4*)(rec + i * stride + PART_O + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float m = -INFINITY, M = -INFINITY, l = 0.f;
@@ -755,23 +763,26 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
     if (!none) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (warp + j * (MT / 32) < n) add(y[j], warp + j * (MT / 32));
+        if (first + j * per < n) add(y[j], first + j * per);
 #pragma unroll 4
-      for (int i = warp + MT / 8; i < n; i += MT / 32) add(*(const float4*)(rec + i * stride + PART_O + 4 * lane), i);
+      for (int i = first + 4 * per; i < n; i += per) add(*(const float4*)(rec + i * stride + PART_O + 4 * lane), i);
     }
     *(float4*)&wo[warp][4 * lane] = o;
+    if (lane == 0) scale[warp] = none ? 0.f : ex2(M - m) / l;
+    const size_t row = (size_t)b * cv.Hq + (size_t)h * G + (blockIdx.y << log_heads);
+    if (a.lse && first == 0 && lane == 0) a.lse[row + own_hd] = none ? -INFINITY : (m + log2f(l)) * LN2;
     __syncthreads();
-    if (threadIdx.x < D / 2) {
-      float x = 0.f, y = 0.f;
+    for (int e = threadIdx.x; e < heads * (D / 2); e += MT) {
+      const int w0 = e / (D / 2) * per, c = e % (D / 2);
+      float x = 0.f, z = 0.f;
 #pragma unroll
-      for (int w = 0; w < MT / 32; ++w) {
-        x += wo[w][2 * threadIdx.x];
-        y += wo[w][2 * threadIdx.x + 1];
-      }
-      const float f = none ? 0.f : ex2(M - m) / l;
-      const size_t row = (size_t)b * cv.Hq + (size_t)h * G + blockIdx.y;
-      ((__nv_bfloat162*)(a.out + row * D))[threadIdx.x] = __floats2bfloat162_rn(x * f, y * f);
-      if (a.lse && threadIdx.x == 0) a.lse[row] = none ? -INFINITY : (m + log2f(l)) * LN2;
+      for (int w = 0; w < MT / 32; ++w)
+        if (w < per) {
+          const float2 v = *(const float2*)&wo[w0 + w][2 * c];
+          x += v.x;
+          z += v.y;
+        }
+      ((__nv_bfloat162*)(a.out + row * D))[e] = __floats2bfloat162_rn(x * scale[w0], z * scale[w0]);
     }
     return;
   }
@@ -798,7 +809,7 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a) {
   __syncthreads();
   if (tot_m[0] == -INFINITY) return;  // nothing was attended to
   float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req);
-  const int slice = blockIdx.y - G, slices = gridDim.y - G;
+  const int slice = blockIdx.y - outs, slices = gridDim.y - outs;
   auto gather = [&](int rec) {
     const Sums sums = sums_at(a, seg, rec);
     float4 y[MAX_G], x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -886,8 +897,12 @@ cudaError_t launch_kv8_decode(const Kv8Decode& a, int type, cudaStream_t st, Pro
     slices = (a.cv.max_pages_per_req + MT - 1) / MT;
     if (slices > 16) slices = 16;
   }
+  // a CTA per query head while that is one wave (three CTAs an SM; the records are
+  // few and their latency counts), else as many heads as it takes
+  int log_heads = 0;
+  while (1 << log_heads < a.cv.G && segs * (a.cv.G >> log_heads) > 3 * a.grid) ++log_heads;
   prof_begin(prof, OSCAR_KERNEL_KV8_MERGE, st);
-  e = launch_pdl(kv8_merge_kernel, dim3(segs, a.cv.G + slices), dim3(MT), 0, st, a);
+  e = launch_pdl(kv8_merge_kernel, dim3(segs, (a.cv.G >> log_heads) + slices), dim3(MT), 0, st, a, log_heads);
   prof_end(prof, OSCAR_KERNEL_KV8_MERGE, st);
   return e;
 }
