@@ -401,10 +401,12 @@ struct Cursor {
 // set).  A whole warp calls it; every warp finds its CTA's share by itself.  Early,
 // before the wait, the lengths may change under it: then the answer is of no
 // use, but every read stays in range.
-__device__ __forceinline__ int cta_share(Cursor& c, const CacheView& cv, int B, uint32_t i, uint32_t grid,
+// `mine`: request `lane`, as it was read.
+__device__ __forceinline__ int cta_share(Cursor& c, Segment& mine, const CacheView& cv, int B, uint32_t i, uint32_t grid,
                                          bool early) {
   const int lane = threadIdx.x & 31;
   Segment own = segment_or_none(cv, B, lane, early);
+  mine = own;
   uint32_t units = (uint32_t)(own.units * cv.Hkv), sum;
   uint32_t below = warp_scan(units, &sum);
   unsigned long long W = sum;
@@ -541,31 +543,44 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
   }
   fence_proxy_async();
   __syncthreads();
-  // The CTA's share and the warp's first two units, twice: before the wait, from
-  // lengths and pages that the kernel before may still change, only to have the
-  // code and the data at hand (the L2 prefetch is a hint); then for good.
+  // The CTA's share and the warp's first units are found before the wait, from
+  // lengths and pages that the kernel before may still change, to have the code
+  // and the data at hand (the L2 prefetch is a hint).  After it they stand if
+  // every request still has the units it had (a step seldom changes them), with
+  // the lengths and the page read again, together: one trip to the L2 instead of
+  // two; else they are found again.
   const bool two = warp + KW < NS;  // the warp fills two stages at the start
   Cursor c, ic;                     // the CTA's first unit; the warp's next unit to copy, and its page
-  int count, next, pid = 0;
+  int count, next = warp, pid = 0;
 #pragma unroll 1
   for (bool early = true;; early = false) {
-    count = cta_share(c, cv, B, blockIdx.x, a.grid, early);
-    next = warp;
+    Segment mine;
+    count = cta_share(c, mine, cv, B, blockIdx.x, a.grid, early);
+    ic = c;
     bool more = next < count;
-    if (more) {
-      ic = c;
-      more = cursor_forward(ic, cv, B, next, early);
-      if (more) pid = cursor_page(ic, cv, early);
-    }
+    if (more) more = cursor_forward(ic, cv, B, next, early);
+    if (more) pid = cursor_page(ic, cv, early);
     if (!early) break;
     if (lane == 0 && more) {
       prefetch_unit(ic, cv, pid);
-      if (two && next + KW < count && cursor_forward(ic, cv, B, KW, true))
-        prefetch_unit(ic, cv, cursor_page(ic, cv, true));
+      Cursor ahead = ic;
+      if (two && next + KW < count && cursor_forward(ahead, cv, B, KW, true))
+        prefetch_unit(ahead, cv, cursor_page(ahead, cv, true));
     }
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();  // after the wait: what the merge reads before its own wait is there
+    if (B <= 32 && (next >= count || (more && ic.b == c.b))) {
+      if (more) pid = cursor_page(ic, cv);
+      const Segment now = segment_or_none(cv, B, lane);
+      if (__all_sync(0xffffffffu, now.units == mine.units && now.win == mine.win)) {
+        if (count > 0) {
+          c.sg = make_segment(__shfl_sync(0xffffffffu, now.L, c.b), __shfl_sync(0xffffffffu, now.H, c.b));
+          if (more) ic.sg = c.sg;
+        }
+        break;
+      }
+    }
   }
   if (count == 0) return;
   auto issue_next = [&](int stage, int step) {  // then moves on by `step` units
