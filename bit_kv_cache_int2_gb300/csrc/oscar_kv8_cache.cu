@@ -300,18 +300,19 @@ __global__ void __launch_bounds__(AW * 32) append_small_kernel(Kv8Append a) {
 // do the window; the others AP_SHARE tasks per warp of the blocks that fall out
 // of the window at once: they have new tokens only and are quantised straight
 // from the input, a warp per block, kv head and side.  Each warp copies its next
-// rows to shared memory (cp.async, AP_DEPTH tasks ahead) while it works on the
-// present ones.  CTAs are small and many, two to an SM: SMs differ in how fast
-// the memory serves them, and one even share for each SM left a fifth of the
-// time idle.  append_lengths_kernel writes the lengths.
+// rows to shared memory (cp.async) while it works on the present ones.  CTAs are
+// small and many, six to an SM: SMs differ in how fast the memory serves them, and
+// one even share for each SM left a fifth of the time idle.  append_lengths_kernel
+// writes the lengths.
 // Bound by memory: a 100K prompt of 8 kv heads (412 MB read, 205 MB written) takes
-// 105 us with all launches, 5.9 TB/s; a plain kernel that reads and writes as much
-// in order reaches 6.8.
+// 99 us with all launches, 6.2 TB/s; a plain kernel that reads and writes as much in
+// order reaches 6.8.  16 warps an SM with three stages each: 105; shares of 12 or 16
+// tasks: 103 to 106; even shares, one CTA per SM: 115.
 // A request that is refused keeps its window and lengths; places behind the end
 // of its history may have been written.
-constexpr int PW = 8;        // warps per CTA
+constexpr int PW = 4;        // warps per CTA
 constexpr int AP_SHARE = 8;  // tasks per warp
-constexpr int AP_DEPTH = 3;
+constexpr int AP_DEPTH = 2;
 constexpr int AP_ROW = D * 2 + 16;  // a row's place: rows start in different banks
 constexpr int AP_STAGE = KV8_BLK * AP_ROW;
 
@@ -320,7 +321,7 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(PW * 32, 2) append_kernel(Kv8Append a, int spans) {
+__global__ void __launch_bounds__(PW * 32, 6) append_kernel(Kv8Append a, int spans) {
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
   pdl_launch_dependents();  // after the wait: append_lengths_kernel looks before its own
