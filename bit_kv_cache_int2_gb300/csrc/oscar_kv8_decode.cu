@@ -664,6 +664,11 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
       S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 4);
       S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 8);
       S.l[hc] += __shfl_xor_sync(0xffffffffu, S.l[hc], 16);
+      // the maxima pass NaN over, l does not: a warp that saw nothing else must not count as one without tokens
+      if (S.l[hc] != 0.f) {
+        if (S.m[hc] == -INFINITY) S.m[hc] = 0.f;
+        if (S.M[hc] == -INFINITY) S.M[hc] = 0.f;
+      }
       const int hd = 2 * tq + hc;
       if (hd < G) {
         float* x = comb + (warp * G + hd) * PART_STRIDE;

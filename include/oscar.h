@@ -500,7 +500,8 @@ oscar_status oscar_append_bf16_history(oscar_ctx* ctx, const oscar_cache* cache,
  * values, s = max(max|x|, 2^-100) / qmax, and codes c = x / s rounded to the
  * nearest value of the type, ties to even, exactly (of x·qmax / max|x|, not of
  * a rounded quotient); x is read back as c·s.  A block that holds an infinity
- * or NaN has the scale NaN: every output that sees it is NaN.
+ * or NaN has the scale NaN: every output that sees it is NaN (an infinite value
+ * in the BF16 regions comes out as an infinity or NaN).
  *   OSCAR_KV8_E4M3: qmax = 448, c an e4m3 floating-point number;
  *   OSCAR_KV8_INT8: qmax = 127, c a signed integer, -127 .. 127.
  *

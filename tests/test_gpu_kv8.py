@@ -34,6 +34,8 @@ def ok(p):
     (2, [700, 3, 255, 256, 257, 1]),
     (1, [64, 256, 272, 1, 1000, 31]),
     (5, [79, 250, 33, 300]),
+    (12, [1, 600, 1, 20]),
+    (16, [700, 1, 300]),
 ])
 def test_append_leaves_the_oracles_state(kind, Hkv, steps):
     p = Pair(kind, Hkv, 1, 2, 40, seed=len(steps))
@@ -240,6 +242,64 @@ def test_decode_shows_a_nan_block_only_where_it_is(kind=oscar.KV8_INT8):
         p.close()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,where", [(321, "block"), (640, "page"), (70, "sink"), (200, "window"), (5, "all")])
+def test_decode_shows_nan_where_nothing_else_is_near(kind, n, where):
+    """NaN keys that fill a block alone in its page, a whole page, a unit of the
+    sink or window, or all there is: the outputs that see them are NaN, and lse."""
+    p = Pair(kind, 2, 2, 2, 8)
+    try:
+        k, v = p.draw(n)
+        at = {"block": (64, 80), "page": (128, 192), "sink": (32, 64), "window": (160, 192), "all": (0, n)}[where]
+        k[1, at[0]:at[1], 1] = float("nan")
+        p.append(n, (k, v))
+        out, lse = p.decode(p.query(), weights=False)
+        nan = torch.isnan(out.float()).all(-1).cpu().view(2, 2, 2)
+        assert nan[1, 1].all() and torch.isnan(lse.cpu().view(2, 2, 2)[1, 1]).all()
+        assert not nan[0].any() and not nan[1, 0].any() and not torch.isnan(lse[0]).any()
+        ok(p)
+    finally:
+        p.close()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_decode_with_a_query_that_is_not_finite(bad, kind=oscar.KV8_INT8):
+    p = lengths_pair(kind, 2, 4, [5, 900], seed=77)
+    try:
+        q = p.query()
+        q[:, 3, 17] = bad
+        out, lse = p.decode(q, weights=False)
+        o, ls = out.float().cpu(), lse.cpu()
+        assert torch.isnan(o[:, 3]).all() and torch.isnan(ls[:, 3]).all()
+        rest = [h for h in range(8) if h != 3]
+        assert torch.isfinite(o[:, rest]).all() and torch.isfinite(ls[:, rest]).all()
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_decode_of_lengths_no_append_leaves(kind=oscar.KV8_E4M3):
+    """Empty outputs and OSCAR_ERR_STATE for them, the others as ever."""
+    p = lengths_pair(kind, 2, 2, [500, 500, 500, 500, 500], seed=78)
+    try:
+        p.cache["seq_lens"][0] = 900       # a window of 644 tokens
+        p.cache["hist_lens"][1] += 8       # half a block
+        p.cache["hist_lens"][2] = 16 * 64  # more than there is
+        p.cache["seq_lens"][3] = -5
+        q = p.query()
+        before = p.weights.clone()
+        out, lse = p.decode(q, 1.0)
+        assert oscar.oscar_get_error(p.ctx) == oscar.ERR_STATE
+        assert bool((out[:4] == 0).all()) and bool(torch.isneginf(lse[:4]).all())
+        assert torch.equal(p.weights[:4], before[:4])
+        one = Pair.__new__(Pair)
+        one.__dict__.update(p.__dict__)
+        one.B, one.req = 1, p.req[4:]
+        check_decode(one, q[4:], out[4:], lse[4:])
+    finally:
+        p.close()
+
+
 def test_decode_leaves_bad_pages_out(kind=oscar.KV8_E4M3):
     p = lengths_pair(kind, 2, 2, [800, 800, 321], seed=9)
     try:
@@ -320,6 +380,36 @@ def test_evict_ties_and_odd_weights(values):
                 r.w_hist[h] = [0.0] * (r.H // 16)
         p.weights[:, :, 16:] = 0
         p.check_state()
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_evict_more_blocks_than_the_selection_keeps(kind=oscar.KV8_INT8):
+    """A history beyond 800K tokens, whose last weights the selection reads again."""
+    n = 54000
+    p = Pair(kind, 1, 1, 1, n // 4 + 2, seed=5, dirty=False)
+    try:
+        g = torch.Generator(device="cuda").manual_seed(3)
+        p.cache["hist_lens"][0] = 16 * n
+        p.cache["seq_lens"][0] = 16 * n + 64 + 250
+        p.cache["pool"].copy_(torch.randint(0, 256, p.cache["pool"].shape, dtype=torch.uint8, device="cuda", generator=g))
+        w = (torch.randint(0, 3000, (n,), device="cuda", generator=g).float() / 3000) ** 4  # many ties
+        p.weights[0, 0, 16:16 + n] = w
+        blocks = p.cache["pool"].view(-1, 16416)[p.cache["page_table"][0].long()][:, :16384].reshape(-1, 4096).clone()
+        budget = 16 * 20000
+        e = (16 * n - budget) // 256 * 16
+        keep = n - e
+        gone = torch.zeros(n, dtype=torch.bool, device="cuda")
+        gone[torch.sort(w, stable=True)[1][:e]] = True
+        idx = torch.arange(n, device="cuda")
+        holes, ends = (gone & (idx < keep)).nonzero()[:, 0], (~gone & (idx >= keep)).nonzero()[:, 0]
+        oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, budget, p.scratch, 1)
+        assert p.cache["hist_lens"].tolist() == [16 * keep]
+        w[holes], blocks[holes] = w[ends], blocks[ends]
+        assert torch.equal(p.weights[0, 0, 16:16 + keep], w[:keep])
+        got = p.cache["pool"].view(-1, 16416)[p.cache["page_table"][0].long()][:, :16384].reshape(-1, 4096)
+        assert torch.equal(got[:keep], blocks[:keep])
         ok(p)
     finally:
         p.close()
@@ -416,6 +506,22 @@ def test_captured_steps_replay(kind=oscar.KV8_INT8):
                     r.evict(256, w[b, :, 16:])
         st.synchronize()
         p.check_state(weight_tol=2 * worst)
+        ok(p)
+    finally:
+        p.close()
+
+
+def test_requests_may_share_pages_when_read(kind=oscar.KV8_E4M3):
+    """A common prefix: the second request's table names the first one's pages."""
+    p = lengths_pair(kind, 2, 4, [1344, 0], seed=24)
+    try:
+        for x in p.cache:
+            if x != "pool":
+                p.cache[x][1] = p.cache[x][0]
+        p.req[1] = p.req[0]
+        q = p.query()
+        out, lse = p.decode(q, weights=False)
+        check_decode(p, q, out, lse)
         ok(p)
     finally:
         p.close()
