@@ -408,9 +408,9 @@ __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
 // ------------------------------------------------------------------ eviction
 constexpr int EVICT_HELD = 50 * 1024;  // keys kept in shared memory (200 KB)
 
-// Unsigned keys in the order of the floats, NaN last.
+// Unsigned keys in the order of the floats, -0 as 0, NaN last.
 __device__ __forceinline__ uint32_t order_key(float w) {
-  const uint32_t u = __float_as_uint(w);
+  const uint32_t u = __float_as_uint(__fadd_rn(w, 0.f));
   if (w != w) return 0xffffffffu;
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
