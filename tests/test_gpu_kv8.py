@@ -505,6 +505,87 @@ def test_captured_steps_replay(kind=oscar.KV8_INT8):
         p.close()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,Hkv,G,start", [(1, 8, 4, 5000), (3, 2, 8, 330), (40, 2, 1, 700)])
+def test_back_to_back_equals_one_at_a_time(kind, B, Hkv, G, start):
+    """Kernels of one call start before the call before has ended: 150 steps,
+    chunks and evictions without a pause give the same bits, outputs, weights and
+    state, as with a synchronisation after every call."""
+    def play(pause):
+        p = Pair(kind, Hkv, G, B, -(-(start + 900) // 64), seed=6, dirty=False)
+        g = torch.Generator(device="cuda").manual_seed(8)
+        rand = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+        try:
+            outs = []
+            k, v = rand(B, start, Hkv, 128), rand(B, start, Hkv, 128)
+            oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, start, B, weights=p.weights)
+            steps = [(rand(B, T, Hkv, 128), rand(B, T, Hkv, 128), rand(B, Hkv * G, 128), T)
+                     for T in ([1] * 40 + [37]) * 4]
+            torch.cuda.synchronize()
+            for i, (k, v, q, T) in enumerate(steps):
+                out, lse = torch.empty_like(q), torch.empty(B, Hkv * G, device="cuda")
+                oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, T, B, weights=p.weights)
+                if pause:
+                    torch.cuda.synchronize()
+                oscar.oscar_decode_kv8(p.ctx, p.cache, kind, q, out, lse, p.scratch, B, weights=p.weights, decay=0.99)
+                if pause:
+                    torch.cuda.synchronize()
+                if i % 50 == 20:
+                    oscar.oscar_evict_kv8(p.ctx, p.cache, p.weights, start // 2, p.scratch, B)
+                    if pause:
+                        torch.cuda.synchronize()
+                outs += [out, lse]
+            torch.cuda.synchronize()
+            ok(p)
+            return outs + [p.weights, p.cache["seq_lens"], p.cache["hist_lens"], p.cache["pool"], p.cache["ring_k"],
+                           p.cache["ring_v"]]
+        finally:
+            p.close()
+
+    for a, b in zip(play(False), play(True)):
+        assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
+
+
+def test_between_int2_calls_without_a_pause(kind=oscar.KV8_INT8):
+    """8-bit and INT2 calls of one context in turn on a stream: the INT2 decode
+    reads its lengths before its own wait, so no 8-bit kernel may let it start
+    before the INT2 append has ended."""
+    def play(pause):
+        p = Pair(kind, 2, 4, 2, 40, seed=9, dirty=False)
+        int2 = oscar.alloc_cache(p.cfg)
+        int2["page_table"].copy_(torch.arange(80).int().view(2, 40))
+        sc = oscar.alloc_scratch(p.cfg)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        rand = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+        sync = torch.cuda.synchronize if pause else lambda: None
+        try:
+            k, v = rand(2, 1000, 2, 128), rand(2, 1000, 2, 128)
+            oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, 1000, 2, weights=p.weights)
+            oscar.oscar_import_tokens(p.ctx, 0, int2, k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous(), 2, 1000)
+            steps = [(rand(2, 1, 2, 128), rand(2, 1, 2, 128), rand(2, 8, 128)) for _ in range(120)]
+            torch.cuda.synchronize()
+            outs = []
+            for k, v, q in steps:
+                a, b = torch.empty_like(q), torch.empty_like(q)
+                oscar.oscar_append(p.ctx, 0, int2, k, v, 2)
+                sync()
+                oscar.oscar_append_kv8(p.ctx, p.cache, kind, k, v, 1, 2, weights=p.weights)
+                sync()
+                oscar.oscar_decode(p.ctx, 0, int2, q, a, None, sc, 2)
+                sync()
+                oscar.oscar_decode_kv8(p.ctx, p.cache, kind, q, b, None, p.scratch, 2, weights=p.weights)
+                sync()
+                outs += [a, b]
+            torch.cuda.synchronize()
+            ok(p)
+            return outs + [int2["seq_lens"], p.cache["seq_lens"], p.weights]
+        finally:
+            p.close()
+
+    for a, b in zip(play(False), play(True)):
+        torch.testing.assert_close(a, b, rtol=2.0 ** -7, atol=2.0 ** -9)  # (INT2 partials may join in another order)
+
+
 def test_requests_may_share_pages_when_read(kind=oscar.KV8_E4M3):
     """A common prefix: the second request's table names the first one's pages."""
     p = lengths_pair(kind, 2, 4, [1344, 0], seed=24)
