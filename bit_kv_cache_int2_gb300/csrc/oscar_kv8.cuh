@@ -59,6 +59,13 @@ __device__ __forceinline__ uint8_t* kv8_head(const CacheView& cv, int pid, int h
   return cv.pool + (size_t)pid * cv.page_bytes + (size_t)h * KV8_HEAD_BYTES;
 }
 
+// Larger magnitudes of two BF16 pairs; NaN if one is.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b32 t;\n abs.bf16x2 t, %2;\n max.NaN.bf16x2 %0, %1, t;\n}\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // ---------------------------------------------------------------- launchers
 struct Kv8Append {
   CacheView cv;

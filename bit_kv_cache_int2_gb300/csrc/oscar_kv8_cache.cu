@@ -100,13 +100,6 @@ __device__ __forceinline__ uint32_t codes2(uint64_t x, Factor k) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Larger magnitudes of two BF16 pairs; NaN if one is.
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("{\n .reg .b32 t;\n abs.bf16x2 t, %2;\n max.NaN.bf16x2 %0, %1, t;\n}\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // A warp quantises one side of a block and writes codes and scale.
 template <int TYPE>
 __device__ __forceinline__ void quantise_side(const SideRows& S, int side, uint8_t* block, float* scale, int lane) {

@@ -28,11 +28,17 @@ namespace {
 constexpr int KW = 8;   // warps per decode CTA
 constexpr int MT = 256; // threads per merge CTA
 // A partial record holds per query head: the largest logit m (base 2) and
-// l = sum 2^(s - m); the largest M of t = s + log2 s_V and o = sum 2^(t - M) c_V.
-// The two maxima differ because 2^(t - M) goes through fp16 on its way into
-// the product: the factor s_V must not push it out of range, however the
-// scales of the blocks differ.
+// l = sum 2^(s - m); and M and o = sum 2^(s - M) v.  M is P_TOP below the largest
+// t = s + log2 a, a the size of what the weight is multiplied with: a block's s_V,
+// whose codes go up to 448 or 127, or a window token's own largest magnitude over
+// 2^8.  The history's 2^(t - M) goes through fp16 on its way into the product
+// with c_V; so what takes its bits is only a token that counts for more in the
+// output, never one with a larger logit alone, whichever region it is in and
+// whatever the values' size.  fp16 has 11 bits down to 2^-14 and none below 2^-25:
+// with P_TOP = 15 tokens keep all bits down to 2^-29 of the largest, and what is
+// lost below 2^-40 of it is nothing to the sum of a million.
 constexpr int REC_M = 0, REC_L = 1, REC_T = 2;
+constexpr float P_TOP = 15.f;
 
 // ------------------------------------------------------------- the work list
 // The work is a sequence of units, 16 KB each: for every (request, kv head) in
@@ -174,20 +180,19 @@ __device__ __forceinline__ void codes_fp16(uint32_t w, uint32_t& lo, uint32_t& h
 
 // One online-softmax step over NT tiles of 16 tokens.  s: the logits in base 2,
 // -inf where there is no token (at least one token is there), rows gid and
-// gid + 8, heads 2tq and 2tq + 1; lv: log2 of each tile's value scale.  On
-// return p holds 2^(t - M) and sum[t][hc] this thread's part of the tile's
-// sum of 2^(s - m).
-template <int NT>
-__device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], const float (&lv)[NT], float (&p)[NT][4],
-                                             float (&sum)[NT][2]) {
+// gid + 8, heads 2tq and 2tq + 1; lv: log2 a of the two rows.  On return p holds
+// 2^(t - M) (SCALED, for codes) or 2^(s - M) (for values themselves), and sum[t][hc]
+// this thread's part of the tile's sum of 2^(s - m).
+template <bool SCALED, int NT>
+__device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], const float (&lv)[NT][2],
+                                             float (&p)[NT][4], float (&sum)[NT][2]) {
 #pragma unroll
   for (int hc = 0; hc < 2; ++hc) {
     float ms = -INFINITY, mt = -INFINITY;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float x = fmaxf(s[t][hc], s[t][hc + 2]);
-      ms = fmaxf(ms, x);
-      mt = fmaxf(mt, x + lv[t]);
+      ms = fmaxf(ms, fmaxf(s[t][hc], s[t][hc + 2]));
+      mt = fmaxf(mt, fmaxf(s[t][hc] + lv[t][0], s[t][hc + 2] + lv[t][1]));
     }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -198,6 +203,7 @@ __device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], 
       S.l[hc] *= ex2(S.m[hc] - ms);
       S.m[hc] = ms;
     }
+    mt -= P_TOP;
     if (mt > S.M[hc]) {
       const float al = ex2(S.M[hc] - mt);
       S.M[hc] = mt;
@@ -211,8 +217,8 @@ __device__ __forceinline__ void softmax_step(State& S, const float (&s)[NT][4], 
     for (int t = 0; t < NT; ++t) {
       sum[t][hc] = ex2(s[t][hc] - S.m[hc]) + ex2(s[t][hc + 2] - S.m[hc]);
       S.l[hc] += sum[t][hc];
-      p[t][hc] = ex2(s[t][hc] + lv[t] - S.M[hc]);
-      p[t][hc + 2] = ex2(s[t][hc + 2] + lv[t] - S.M[hc]);
+      p[t][hc] = ex2((SCALED ? s[t][hc] + lv[t][0] : s[t][hc]) - S.M[hc]);
+      p[t][hc + 2] = ex2((SCALED ? s[t][hc + 2] + lv[t][1] : s[t][hc + 2]) - S.M[hc]);
     }
   }
 }
@@ -257,11 +263,11 @@ template <int TYPE, bool WEIGHTS, bool FULL>
 __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_t* page, int nb, int lane, int G,
                                           const Sums& w) {
   const int gid = lane >> 2, tq = lane & 3;
-  float s[4][4], lv[4];
+  float s[4][4], lv[4][2];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     s[t][0] = s[t][1] = s[t][2] = s[t][3] = -INFINITY;
-    lv[t] = 0.f;
+    lv[t][0] = lv[t][1] = 0.f;
     if (FULL || t < nb) {
       float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -277,13 +283,13 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
       }
       const float2 sc = *(const float2*)(page + KV8_OFF_SCALES + 8 * t);
       // the append makes no scale below 2^-109; a zero (a page that nothing wrote) must not become -inf
-      lv[t] = sc.y < 1.17549435e-38f ? -126.f : lg2(sc.y);
+      lv[t][0] = lv[t][1] = sc.y < 1.17549435e-38f ? -126.f : lg2(sc.y);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[t][e] = a[e] * (Q.alpha[e & 1] * sc.x);
     }
   }
   float p[4][4], sum[4][2];
-  softmax_step<4>(S, s, lv, p, sum);
+  softmax_step<true>(S, s, lv, p, sum);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     if (FULL || t < nb) {
@@ -309,16 +315,29 @@ __device__ __forceinline__ void page_step(State& S, const Query& Q, const uint8_
 // of the first 16 and the first n1 of the last 16 are there.  The others may
 // hold anything: their logits become -inf and their values 0.
 // The weights go into the product as two BF16 parts (16 bits together): the
-// newest tokens often carry most of the weight.
+// newest tokens often carry most of the weight.  A weight 2^(s - M) may be far above
+// 1, where the values are small: their product is not, and BF16 takes it.
 template <bool WEIGHTS>
 __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint8_t* K, const uint8_t* V, int n0, int n1,
                                             int lane, int G, bool sums, const Sums& w) {
   const int gid = lane >> 2, tq = lane & 3;
-  float s[2][4];
-  const float lv[2] = {0.f, 0.f};
+  // lane i: log2 of row i's largest magnitude over 2^8 (rows start at different
+  // pieces, so that the banks do; a row that is not finite counts as 1: what it
+  // gives is not finite anyway)
+  uint32_t mx = 0;
+#pragma unroll 8
+  for (int j = 0; j < 16; ++j) {
+    const uint4 x = *(const uint4*)(V + lane * WROW + 16 * ((lane + j) & 15));
+    mx = max_abs2(max_abs2(max_abs2(max_abs2(mx, x.x), x.y), x.z), x.w);
+  }
+  mx = max(mx >> 16, mx & 0xffffu);
+  const float row = mx >= 0x7f80u ? -8.f : lg2(fmaxf(__uint_as_float(mx << 16), KV8_TINY)) - 8.f;
+  float s[2][4], lv[2][2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = t ? n1 : n0;
+    lv[t][0] = __shfl_sync(0xffffffffu, row, 16 * t + gid);
+    lv[t][1] = __shfl_sync(0xffffffffu, row, 16 * t + 8 + gid);
     float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -331,7 +350,7 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
     for (int e = 0; e < 4; ++e) s[t][e] = (e < 2 ? gid : gid + 8) < n ? a[e] * Q.alpha[e & 1] : -INFINITY;
   }
   float p[2][4], sum[2][2];
-  softmax_step<2>(S, s, lv, p, sum);
+  softmax_step<false>(S, s, lv, p, sum);
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int n = t ? n1 : n0;
@@ -726,7 +745,7 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
 // it is worked out while the decode kernel still runs.
 __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_heads) {
   __shared__ __align__(16) float wo[MT / 32][D];
-  __shared__ float scale[MT / 32];
+  __shared__ float scale[2][MT / 32];
   __shared__ float tot_m[MAX_G], tot_r[MAX_G];
   const CacheView& cv = a.cv;
   const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv, G = cv.G;
@@ -799,7 +818,11 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_head
       for (int i = first + 4 * per; i < n; i += per) add(*(const float4*)(rec + i * stride + PART_O + 4 * lane), i);
     }
     *(float4*)&wo[warp][4 * lane] = o;
-    if (lane == 0) scale[warp] = none ? 0.f : ex2(M - m) / l;
+    if (lane == 0) {  // 2^(M - m) / l in two factors: values of 2^-100 with a leading logit would be lost in one
+      const float f = ex2(0.5f * (M - m));
+      scale[0][warp] = none ? 0.f : f;
+      scale[1][warp] = none ? 0.f : f / l;
+    }
     const size_t row = (size_t)b * cv.Hq + (size_t)h * G + (blockIdx.y << log_heads);
     if (a.lse && first == 0 && lane == 0) a.lse[row + own_hd] = none ? -INFINITY : (m + log2f(l)) * LN2;
     __syncthreads();
@@ -813,7 +836,7 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_head
           x += v.x;
           z += v.y;
         }
-      ((__nv_bfloat162*)(a.out + row * D))[e] = __floats2bfloat162_rn(x * scale[w0], z * scale[w0]);
+      ((__nv_bfloat162*)(a.out + row * D))[e] = __floats2bfloat162_rn(x * scale[0][w0] * scale[1][w0], z * scale[0][w0] * scale[1][w0]);
     }
     return;
   }
