@@ -39,6 +39,9 @@ constexpr int MT = 256; // threads per merge CTA
 // lost below 2^-40 of it is nothing to the sum of a million.
 constexpr int REC_M = 0, REC_L = 1, REC_T = 2;
 constexpr float P_TOP = 15.f;
+// A record that says its part was not read (a wait ran out): m = 0, l = LOST_L,
+// M = NaN, which make the output and lse NaN.  A sum of powers is never LOST_L.
+constexpr float LOST_L = -INFINITY;
 
 // ------------------------------------------------------------- the work list
 // The work is a sequence of units, 16 KB each: for every (request, kv head) in
@@ -702,9 +705,14 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
       }
     }
     __syncthreads();
-    if (issued[MAX_STAGES]) break;
     float* rec = a.part + ((size_t)blockIdx.x + seg) * G * PART_STRIDE;
-    for (int e = threadIdx.x; e < G * D; e += KW * 32) {
+    const bool lost = issued[MAX_STAGES];  // a wait ran out: this part and the CTA's later ones are not read
+    if (lost) {
+      mine = count;
+      if (threadIdx.x < G)
+        *(float4*)(rec + threadIdx.x * PART_STRIDE) = make_float4(0.f, LOST_L, __uint_as_float(0x7fffffffu), 0.f);
+    }
+    for (int e = lost ? G * D : threadIdx.x; e < G * D; e += KW * 32) {
       const int hd = e / D, ch = e % D;
       float m = -INFINITY, M = -INFINITY;
 #pragma unroll
@@ -843,8 +851,10 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_head
   // weights: every head's total first
   for (int hd = warp; hd < G; hd += MT / 32) {
     float m = -INFINITY, l = 0.f;
+    bool lost = false;
     for (int i = lane; i < n; i += 32) {
       const float2 x = *(const float2*)(recs + ((size_t)i * G + hd) * PART_STRIDE);
+      lost |= x.y == LOST_L;
       const float mn = fmaxf(m, x.x);
       if (x.x != -INFINITY) l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
       m = mn;
@@ -855,13 +865,14 @@ __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_head
     l = m == -INFINITY ? 0.f : l * ex2(m - gm);
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    lost = __any_sync(0xffffffffu, lost);
     if (lane == 0) {
-      tot_m[hd] = gm;
+      tot_m[hd] = lost ? -INFINITY : gm;
       tot_r[hd] = 1.f / l;
     }
   }
   __syncthreads();
-  if (tot_m[0] == -INFINITY) return;  // nothing was attended to
+  if (tot_m[0] == -INFINITY) return;  // nothing was attended to, or not all of it was read
   float* w = a.weights + (size_t)seg * (KV8_RING_BLOCKS + (size_t)KV8_PAGE_BLOCKS * cv.max_pages_per_req);
   const int slice = blockIdx.y - outs, slices = gridDim.y - outs;
   auto gather = [&](int rec) {

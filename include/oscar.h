@@ -568,7 +568,9 @@ oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
  *   decay : finite, >= 0 (1: plain sums); not used without weights
  * Requests with no token give zeros and lse = -inf, and their weights stay.
  * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad page,
- * whose tokens are left out (their blocks' weights only decay). */
+ * whose tokens are left out (their blocks' weights only decay);
+ * OSCAR_ERR_TIMEOUT: the (request, KV head)s of which a piece was not read get
+ * NaN as outputs and lse, and their weights stay. */
 oscar_status oscar_decode_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, void* out,
                               float* lse, float* weights, float decay, void* scratch, size_t scratch_bytes,
                               int batch, oscar_stream_t stream);
