@@ -35,8 +35,12 @@ struct Kv8Req {
   bool ok;
 };
 
-// early: read past the L1, by a kernel that looks before its wait at values that
-// may still change.
+// early: read past the L1, by a kernel that looks before its wait.  Where the kernel
+// before may still change the lengths (the decode after an append), they are a guess
+// to be checked.  Where it does not and released this one only after its own wait (the
+// merge, the lengths of an append), whatever wrote them had ended and stood in the L2
+// before this kernel could start, and a line that an SM's L1 still has from before
+// is passed by.
 __device__ __forceinline__ Kv8Req kv8_req(const CacheView& cv, int b, bool early = false) {
   Kv8Req r;
   r.L = early ? __ldcg(cv.seq_lens + b) : cv.seq_lens[b];

@@ -156,9 +156,9 @@ struct AppendPlan {
   int err;
 };
 
-__device__ __forceinline__ AppendPlan append_lengths(const CacheView& cv, int b, int T) {
+__device__ __forceinline__ AppendPlan append_lengths(const CacheView& cv, int b, int T, bool early = false) {
   AppendPlan p;
-  const Kv8Req r = kv8_req(cv, b);
+  const Kv8Req r = kv8_req(cv, b, early);
   p.L = r.L;
   p.H = r.H;
   p.err = r.ok ? 0 : OSCAR_ERR_STATE;
@@ -174,12 +174,13 @@ __device__ __forceinline__ AppendPlan append_lengths(const CacheView& cv, int b,
 }
 
 // And the pages that take the blocks.  Every thread of the block calls it.
-__device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, int T) {
-  AppendPlan p = append_lengths(cv, b, T);
+__device__ __forceinline__ AppendPlan append_plan(const CacheView& cv, int b, int T, bool early = false) {
+  AppendPlan p = append_lengths(cv, b, T, early);
   int bad = 0;
   if (!p.err && p.H1 > p.H)
     for (int pg = p.H / PAGE + (int)threadIdx.x; pg < (p.H1 + PAGE - 1) / PAGE; pg += blockDim.x) {
-      const int id = cv.page_table[(size_t)b * cv.max_pages_per_req + pg];
+      const int32_t* at = cv.page_table + (size_t)b * cv.max_pages_per_req + pg;
+      const int id = early ? __ldcg(at) : *at;
       if (id < 0) bad |= 1;
       if (id >= cv.num_pages) bad |= 2;
     }
@@ -384,10 +385,11 @@ __global__ void __launch_bounds__(PW * 32, 6) append_kernel(Kv8Append a, int spa
 }
 
 // After append_kernel, which leaves the lengths as they are: the plan is made
-// again while that still runs.
+// again while that still runs, past the L1 (kv8_req).  Made after the wait it was 0.5 us
+// more for a chunk, 2.5 us for a prompt of 100K.
 __global__ void __launch_bounds__(128) append_lengths_kernel(Kv8Append a) {
   pdl_launch_dependents();
-  const AppendPlan p = append_plan(a.cv, blockIdx.x, a.T);
+  const AppendPlan p = append_plan(a.cv, blockIdx.x, a.T, true);
   pdl_wait();
   if (threadIdx.x != 0) return;
   if (p.err) {

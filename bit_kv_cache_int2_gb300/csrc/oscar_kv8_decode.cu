@@ -750,33 +750,42 @@ __global__ void __launch_bounds__(KW * 32, 1) kv8_decode_kernel(Kv8Decode a) {
 // write the output of `heads` query heads each, MT / 32 / heads warps to a head; the others update
 // a slice of the block weights.
 // What is in the records of a (request, kv head) follows from the lengths, so
-// it is worked out while the decode kernel still runs.
+// one warp works it out while the decode kernel still runs, reading past the L1
+// (kv8_req).  A second look at the lengths after the wait took 0.3 to 0.5 us more.
 __global__ void __launch_bounds__(MT) kv8_merge_kernel(Kv8Decode a, int log_heads) {
   __shared__ __align__(16) float wo[MT / 32][D];
   __shared__ float scale[2][MT / 32];
   __shared__ float tot_m[MAX_G], tot_r[MAX_G];
+  __shared__ int4 plan;
   const CacheView& cv = a.cv;
   const int seg = blockIdx.x, b = seg / cv.Hkv, h = seg % cv.Hkv, G = cv.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  const Segment sg = segment_of(cv, b);
-  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0 && !kv8_req(cv, b).ok) record_error(cv.err, OSCAR_ERR_STATE);
-  Balanced bl;
-  bl.W = 0;
-  bl.wch = 0;
-  long long before = 0;
-  for (int r0 = 0; r0 < a.B; r0 += 32) {
-    const uint32_t x = (uint32_t)(segment_or_none(cv, a.B, r0 + lane).units * cv.Hkv);
-    bl.W += __reduce_add_sync(0xffffffffu, x);
-    before += __reduce_add_sync(0xffffffffu, r0 + lane < b ? x : 0u);
+  if (warp == 0) {
+    const Kv8Req r = kv8_req(cv, b, true);
+    const Segment sg = make_segment(r.L, r.H);
+    if (h == 0 && blockIdx.y == 0 && lane == 0 && !r.ok) record_error(cv.err, OSCAR_ERR_STATE);
+    Balanced bl;
+    bl.W = 0;
+    bl.wch = 0;
+    long long before = 0;
+    for (int r0 = 0; r0 < a.B; r0 += 32) {
+      const uint32_t x = (uint32_t)(segment_or_none(cv, a.B, r0 + lane, true).units * cv.Hkv);
+      bl.W += __reduce_add_sync(0xffffffffu, x);
+      before += __reduce_add_sync(0xffffffffu, r0 + lane < b ? x : 0u);
+    }
+    bl.n = (int)(bl.W < a.grid ? bl.W : a.grid);
+    const long long s0 = before + (long long)h * sg.units;
+    int i0 = 0, n = 0;
+    if (sg.units) {
+      i0 = balanced_owner(bl, s0);
+      n = balanced_owner(bl, s0 + sg.units - 1) - i0 + 1;
+    }
+    if (lane == 0) plan = make_int4(i0, n, r.L, r.H);
   }
-  bl.n = (int)(bl.W < a.grid ? bl.W : a.grid);
-  const long long s0 = before + (long long)h * sg.units;
-  int i0 = 0, n = 0;  // records i0 .. i0 + n - 1, one of each CTA that had a part
-  if (sg.units) {
-    i0 = balanced_owner(bl, s0);
-    n = balanced_owner(bl, s0 + sg.units - 1) - i0 + 1;
-  }
+  __syncthreads();
+  const int i0 = plan.x, n = plan.y;  // records i0 .. i0 + n - 1, one of each CTA that had a part
+  const Segment sg = make_segment(plan.z, plan.w);
   pdl_wait();
   const float* recs = a.part + ((size_t)i0 + seg) * G * PART_STRIDE;
   const int heads = 1 << log_heads, outs = G >> log_heads;
