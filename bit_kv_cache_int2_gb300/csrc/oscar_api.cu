@@ -934,9 +934,9 @@ oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
   const oscar_status s = kv8_check(ctx, cache, weights, batch);
   if (s != OSCAR_OK) return s;
   if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
-  if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) || T < 0 || T > (1 << 24))
-    return OSCAR_ERR_INVALID_ARG;
-  if (T == 0) return OSCAR_OK;
+  if (T < 0 || T > (1 << 24)) return OSCAR_ERR_INVALID_ARG;
+  if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
+  if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16)) return OSCAR_ERR_INVALID_ARG;
   for (int b0 = 0; b0 < batch; b0 += KV8_MAX_REQUESTS) {
     const int n = batch - b0 < KV8_MAX_REQUESTS ? batch - b0 : KV8_MAX_REQUESTS;
     Kv8Append a;
@@ -959,10 +959,10 @@ oscar_status oscar_decode_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
   const oscar_status s = kv8_check(ctx, cache, weights, batch);
   if (s != OSCAR_OK) return s;
   if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
-  if (!q || !out || !scratch || !aligned(q, 16) || !aligned(out, 16) || !aligned(scratch, 256) ||
-      (lse && !aligned(lse, 4)) || (weights && !(decay >= 0.f && std::isfinite(decay))))
+  if (!scratch || !aligned(scratch, 256) || (weights && !(decay >= 0.f && std::isfinite(decay))))
     return OSCAR_ERR_INVALID_ARG;
-  if (batch == 0) return OSCAR_OK;
+  if (batch == 0) return OSCAR_OK;  // an array without elements may have no address
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return OSCAR_ERR_INVALID_ARG;
   const int Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads, P = ctx->cfg.max_pages_per_req;
   const int grid = ctx->num_sms < KV8_MAX_GRID ? ctx->num_sms : KV8_MAX_GRID;
   const int per = kv8_decode_requests(batch, Hkv, ctx->G, P, weights != nullptr);

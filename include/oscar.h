@@ -547,7 +547,8 @@ oscar_status oscar_layout_kv8(const oscar_config* cfg, oscar_kv8_layout_info* ou
  * a whole prompt into an empty request, with the same result as T calls with
  * one token each.
  *   k_new, v_new : device bf16 [batch][T][num_kv_heads][128] (or pinned host
- *                  memory, read in place); 0 <= T <= 2^24
+ *                  memory, read in place); 0 <= T <= 2^24.  With T = 0 or batch = 0
+ *                  nothing is done, and the pointers may be NULL
  *   type : an oscar_kv8_type, the same for the life of a cache
  *   weights : block weights, or NULL
  * Device errors: OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad page
@@ -561,7 +562,7 @@ oscar_status oscar_append_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
  * and recent window.  q, out, lse, scratch and batch as in oscar_decode
  * (scratch: oscar_layout_kv8's scratch_bytes; 256-byte aligned, no initial
  * contents needed, not to be shared by calls that may overlap, also of two
- * captured graphs).
+ * captured graphs).  With batch = 0 nothing is done, and q and out may be NULL.
  *   weights : block weights, or NULL.  With w the softmax weights of a block's
  *             16 tokens summed over them and over the KV head's query heads,
  *             every block that holds a token gets  entry = decay·entry + w.

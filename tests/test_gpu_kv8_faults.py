@@ -72,3 +72,22 @@ def test_a_wait_that_may_run_out_takes_whole_heads(polls, kind=oscar.KV8_INT8):
             assert torch.equal(p.weights[lost], base[lost]) and torch.equal(p.weights[~lost], good_w[~lost])
     finally:
         p.close()
+
+
+def test_calls_without_tokens_or_requests(kind=oscar.KV8_E4M3):
+    """Tensors without elements have no address: the last, empty chunk of a prompt,
+    or a step in which no request is active, is nothing to do and no error."""
+    p = Pair(kind, 2, 2, 2, 12, seed=3)
+    try:
+        p.append(400)
+        k = torch.zeros(2, 400, 2, 128, dtype=torch.bfloat16, device="cuda")
+        q = torch.zeros(0, 4, 128, dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros(0, 4, device="cuda")
+        assert k[:, 400:].data_ptr() == 0 and q.data_ptr() == 0
+        oscar.oscar_append_kv8(p.ctx, p.cache, kind, k[:, 400:], k[:, 400:], 0, 2, weights=p.weights)
+        oscar.oscar_append_kv8(p.ctx, p.cache, kind, k[:0], k[:0], 400, 0, weights=p.weights)
+        oscar.oscar_decode_kv8(p.ctx, p.cache, kind, q, torch.empty_like(q), lse, p.scratch, 0, weights=p.weights)
+        p.check_state()
+        assert oscar.oscar_get_error(p.ctx) == 0
+    finally:
+        p.close()
