@@ -189,6 +189,8 @@ class DeviceBackend:
                  decay=1.0, on_evict=None):
         import torch
 
+        if fmt not in ("int2", "bf16", *KV8_KINDS):
+            raise ValueError(f"unknown history format {fmt!r}")
         self.kind = KV8_KINDS.get(fmt)
         if budget is not None and (self.kind is None or budget < 0):
             raise ValueError("a budget needs 8-bit history and is not negative")

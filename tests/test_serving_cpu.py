@@ -181,3 +181,12 @@ def test_device_backend_feeds_each_slot_its_own_next_token(monkeypatch):
     assert sorted(r.rid for r in done) == [0, 1, 2, 3, 4]
     assert sum(checks) == sum(r.gen for r in reqs) and max(checks) == B
     assert backend.gen_cap == 6  # grew for the 6-token request
+
+
+@pytest.mark.parametrize("fmt", ["int4", "fp8", "E4M3", "", None])
+def test_device_backend_refuses_an_unknown_format(fmt):
+    """Not taken for BF16 pages at admission and INT2 pages in the step."""
+    from bit_kv_cache_int2_gb300 import serving
+
+    with pytest.raises(ValueError, match="format"):
+        serving.DeviceBackend(fmt, None, None, {}, None)
