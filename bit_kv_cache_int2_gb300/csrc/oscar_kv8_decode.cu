@@ -325,8 +325,7 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
                                             int lane, int G, bool sums, const Sums& w) {
   const int gid = lane >> 2, tq = lane & 3;
   // lane i: log2 of row i's largest magnitude over 2^8 (rows start at different
-  // pieces, so that the banks do; a row that is not finite counts as 1: what it
-  // gives is not finite anyway)
+  // pieces, so that the banks do)
   uint32_t mx = 0;
 #pragma unroll 8
   for (int j = 0; j < 16; ++j) {
@@ -334,7 +333,16 @@ __device__ __forceinline__ void window_step(State& S, const Query& Q, const uint
     mx = max_abs2(max_abs2(max_abs2(max_abs2(mx, x.x), x.y), x.z), x.w);
   }
   mx = max(mx >> 16, mx & 0xffffu);
-  const float row = mx >= 0x7f80u ? -8.f : lg2(fmaxf(__uint_as_float(mx << 16), KV8_TINY)) - 8.f;
+  if (mx >= 0x7f80u && (lane & 15) < (lane < 16 ? n0 : n1)) {
+    // an infinity or NaN shows in its own channel: the others go by the row's finite values
+    mx = 0;
+#pragma unroll 1
+    for (int j = 0; j < D; ++j) {
+      const uint32_t x = ((const uint16_t*)(V + lane * WROW))[j] & 0x7fffu;
+      if (x < 0x7f80u) mx = max(mx, x);
+    }
+  }
+  const float row = mx >= 0x7f80u ? 0.f : lg2(fmaxf(__uint_as_float(mx << 16), KV8_TINY)) - 8.f;
   float s[2][4], lv[2][2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {

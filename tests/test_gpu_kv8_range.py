@@ -124,3 +124,24 @@ def test_decode_with_a_region_of_other_size(kind, where):
             assert oscar.oscar_get_error(p.ctx) == 0
         finally:
             p.close()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -60, 2.0 ** 60])
+@pytest.mark.parametrize("at", [3, N - 30])
+def test_decode_shows_a_bad_value_in_its_own_channel(bad, size, at, kind=oscar.KV8_INT8):
+    """One infinity or NaN among the values of the sink or window: the other channels
+    are as without, whatever the values' size."""
+    p, q = fill(kind, 19, N, size, 0, None, 1, seed=11)
+    try:
+        region, row = ("sink_v", at) if at < 64 else ("ring_v", (at - 64) % 256)
+        was = p.cache[region][:, :, row, 5].clone()
+        p.cache[region][:, :, row, 5] = bad
+        out, lse = p.decode(q)
+        assert not bool(torch.isfinite(out[..., 5]).any())
+        p.cache[region][:, :, row, 5] = was
+        out[..., 5] = p.decode(q)[0][..., 5]
+        check(p, q, out, lse)
+        assert oscar.oscar_get_error(p.ctx) == 0
+    finally:
+        p.close()
