@@ -433,8 +433,8 @@ __device__ __forceinline__ int warps_scan(int v, int* red, int* all) {
 // loops are hardly unrolled).  A digit is 11 bits: the weights fall apart into
 // about a hundred first digits, and the second digit nearly always decides
 // (eight bits took four passes of 0.7 us).  For 530 blocks it takes 4 us, for 6000
-// 9 us; a cluster of four CTAs per (request, kv head) with one histogram lost more
-// in its barriers than it saved.
+// 9 us; with a cluster of four CTAs per (request, kv head) and one histogram a whole
+// eviction of 6000 blocks took 60.5 us instead of 62.1, one of 530 13.2 instead of 10.4.
 template <int ET>
 __global__ void __launch_bounds__(ET) evict_select_kernel(Kv8Evict a, int held) {
   extern __shared__ __align__(16) uint32_t keys[];

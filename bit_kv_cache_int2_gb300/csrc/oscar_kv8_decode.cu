@@ -15,10 +15,11 @@
 // columns, so tensor cores are 17% and issue slots 30% busy at the memory's
 // rate: tcgen05, whose smallest tile has 64 rows of one operand and 8 columns,
 // would take the codes through shared or tensor memory once more for nothing.
-// Measured (device time, with the merge; share of the measured 6.79 TB/s):
-// 8 x 131K tokens, 8 query heads a kv head, weights 321 us (0.99); 32 requests of
-// 8K to 32K, weights 207 us (0.95); one of 100K 33.0 us (0.92); 2 x 131K with 2 kv
-// heads 22.2 us (0.79); one of 1K 7.4 us, five trips to the memory and two launches.
+// Measured (device time, with the merge; share of the measured 6.79 TB/s; cards differ):
+// 8 x 131K tokens, 8 query heads a kv head, weights 322 to 330 us (0.99 to 0.97); 32
+// requests of 8K to 32K, weights 207 to 211 us (0.95 to 0.93); one of 100K 33.0 to 33.5
+// us (0.92 to 0.91); 2 x 131K with 2 kv heads 22.4 us (0.78); one of 1K 7.4 us, five
+// trips to the memory and two launches.
 #include "oscar_kv8.cuh"
 
 namespace oscar {
@@ -94,8 +95,9 @@ constexpr int WROW = D * 2;
 constexpr int STAGE_BYTES = (KV8_HEAD_BYTES + 127) / 128 * 128;
 static_assert(STAGE_BYTES >= 64 * WROW, "a window unit fits a stage");
 constexpr int MAX_STAGES = 13;
-// An SM has 228 KB: two of the merge's CTAs fit beside a decode CTA, so that the
-// merge can plan while the decode runs, and the next decode start under the merge.
+// An SM has 228 KB: what is left of them, and without weights of the registers (173
+// of the decode's threads, 80 of the merge's), lets a CTA of the merge plan beside a
+// decode CTA; with weights it comes when that ends.
 constexpr int SMEM_LIMIT = 215 * 1024;
 
 // ------------------------------------------------------------------ the math

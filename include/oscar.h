@@ -617,6 +617,8 @@ oscar_status oscar_debug_rotate(oscar_ctx* ctx, int layer, int which,
  *   (the recent window holds 0..256 tokens), ceil(H / 64) <= max_pages_per_req,
  *   and each of its first ceil(H / 64) page-table entries is in [0, num_pages)
  *   and used by no other history slot of the batch.
+ * (A cache with 8-bit history also needs H to be a multiple of 16, which is not
+ * checked here.)
  *   seq_lens, hist_lens : host int32 [batch]
  *   page_table : host int32 [batch][max_pages_per_req]
  *   bad_request : host int out (or NULL), the first failing request, -1 if none.
