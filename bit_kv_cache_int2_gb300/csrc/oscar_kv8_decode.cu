@@ -34,8 +34,8 @@ constexpr int MT = 256; // threads per merge CTA
 // whose codes go up to 448 or 127, or a window token's own largest magnitude over
 // 2^8.  The history's 2^(t - M) goes through fp16 on its way into the product
 // with c_V; so what takes its bits is only a token that counts for more in the
-// output, never one with a larger logit alone, whichever region it is in and
-// whatever the values' size.  fp16 has 11 bits down to 2^-14 and none below 2^-25:
+// output (in the history with its block's largest value), not one with a larger
+// logit alone, whatever the values' size.  fp16 has 11 bits down to 2^-14 and none below 2^-25:
 // with P_TOP = 15 tokens keep all bits down to 2^-29 of the largest, and what is
 // lost below 2^-40 of it is nothing to the sum of a million.
 constexpr int REC_M = 0, REC_L = 1, REC_T = 2;
