@@ -13,6 +13,7 @@
 
 #include "oscar_internal.cuh"
 #include "oscar_kv8.cuh"
+#include "oscar_rope.cuh"
 
 using namespace oscar;
 
@@ -1009,6 +1010,158 @@ oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* we
     if (e != cudaSuccess) return cuda_status(e);
   }
   return OSCAR_OK;
+}
+
+size_t oscar_prefill_kv8_scratch_bytes(const oscar_config* cfg) {
+  return check_cfg(cfg) == OSCAR_OK && kv8_supported(*cfg) ? kv8_prefill_scratch() : 0;
+}
+
+oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, const void* k,
+                               const void* v, int T, void* out, float* lse, void* scratch, size_t scratch_bytes,
+                               int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_prefill_kv8");
+  const oscar_status s = kv8_check(ctx, cache, nullptr, batch);
+  if (s != OSCAR_OK) return s;
+  if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
+  if (T < 0 || T > (1 << 24)) return OSCAR_ERR_INVALID_ARG;
+  if (!scratch || !aligned(scratch, 256) || scratch_bytes < kv8_prefill_scratch()) return OSCAR_ERR_INVALID_ARG;
+  if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
+  if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      (lse && !aligned(lse, 4)))
+    return OSCAR_ERR_INVALID_ARG;
+  const int Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads;
+  for (int b0 = 0; b0 < batch; b0 += KV8_MAX_REQUESTS) {
+    Kv8Prefill a;
+    a.cv = kv8_rows(ctx, cache, b0);
+    const size_t tok = (size_t)b0 * T;
+    a.q = (const __nv_bfloat16*)q + tok * Hq * D;
+    a.k = (const __nv_bfloat16*)k + tok * Hkv * D;
+    a.v = (const __nv_bfloat16*)v + tok * Hkv * D;
+    a.out = (__nv_bfloat16*)out + tok * Hq * D;
+    a.lse = lse ? lse + tok * Hq : nullptr;
+    a.B = batch - b0 < KV8_MAX_REQUESTS ? batch - b0 : KV8_MAX_REQUESTS;
+    a.T = T;
+    const cudaError_t e = launch_kv8_prefill(a, type, (cudaStream_t)stream, &ctx->prof);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return OSCAR_OK;
+}
+
+oscar_status oscar_read_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, int first, int n, int order,
+                            void* K, void* V, int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_read_kv8");
+  const oscar_status s = kv8_check(ctx, cache, nullptr, batch);
+  if (s != OSCAR_OK) return s;
+  if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
+  if (order != OSCAR_ORDER_HEADS && order != OSCAR_ORDER_TOKENS) return OSCAR_ERR_INVALID_ARG;
+  if (first < 0 || n < 0 || (long long)first + n > (1 << 30)) return OSCAR_ERR_INVALID_ARG;
+  if (n == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
+  if (!K || !V || !aligned(K, 16) || !aligned(V, 16)) return OSCAR_ERR_INVALID_ARG;
+  for (int b0 = 0; b0 < batch; b0 += KV8_MAX_REQUESTS) {
+    Kv8Read a;
+    a.cv = kv8_rows(ctx, cache, b0);
+    const size_t off = (size_t)b0 * n * ctx->cfg.num_kv_heads * D;
+    a.K = (__nv_bfloat16*)K + off;
+    a.V = (__nv_bfloat16*)V + off;
+    a.first = first;
+    a.n = n;
+    a.order = order;
+    const int B = batch - b0 < KV8_MAX_REQUESTS ? batch - b0 : KV8_MAX_REQUESTS;
+    const cudaError_t e = launch_kv8_read(a, type, B, (cudaStream_t)stream, &ctx->prof);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return OSCAR_OK;
+}
+
+oscar_status oscar_make_rope(const oscar_rope_config* c, oscar_rope_table* out) {
+  if (!c || !out) return OSCAR_ERR_INVALID_ARG;
+  if (c->layout != OSCAR_ROPE_HALF && c->layout != OSCAR_ROPE_INTERLEAVED) return OSCAR_ERR_INVALID_ARG;
+  if (c->scaling < OSCAR_ROPE_PLAIN || c->scaling > OSCAR_ROPE_YARN) return OSCAR_ERR_INVALID_ARG;
+  if (c->dims < 16 || c->dims > D || c->dims % 16) return OSCAR_ERR_UNSUPPORTED;
+  const bool scaled = c->scaling != OSCAR_ROPE_PLAIN;
+  const bool by_turns = c->scaling == OSCAR_ROPE_BANDS || c->scaling == OSCAR_ROPE_YARN;
+  if (!(std::isfinite(c->theta) && c->theta > 1.0) || !std::isfinite(c->size)) return OSCAR_ERR_INVALID_ARG;
+  if (scaled && !(std::isfinite(c->factor) && c->factor > 0.0)) return OSCAR_ERR_INVALID_ARG;
+  double low = c->low, high = c->high;
+  if (by_turns) {
+    if (!(std::isfinite(c->trained) && c->trained > 0.0)) return OSCAR_ERR_INVALID_ARG;
+    if (low == 0.0 && high == 0.0) {
+      low = 1.0;
+      high = c->scaling == OSCAR_ROPE_BANDS ? 4.0 : 32.0;
+    }
+    if (!(low > 0.0 && high > low && std::isfinite(high))) return OSCAR_ERR_INVALID_ARG;
+  }
+  const double pi = 3.14159265358979323846, dims = c->dims, f = scaled ? c->factor : 1.0;
+  const int n = c->dims / 2;
+  const double theta = c->scaling == OSCAR_ROPE_NTK ? c->theta * pow(f, dims / (dims - 2.0)) : c->theta;
+  double a = 0.0, b = 0.0;
+  if (c->scaling == OSCAR_ROPE_YARN) {
+    const auto pair_of = [&](double turns) { return dims * log(c->trained / (turns * 2.0 * pi)) / (2.0 * log(theta)); };
+    a = fmax(floor(pair_of(high)), 0.0);
+    b = fmin(ceil(pair_of(low)), n - 1.0);
+  }
+  oscar_rope_table t = {};
+  for (int i = 0; i < n; ++i) {
+    double w = pow(theta, -2.0 * i / dims);
+    if (c->scaling == OSCAR_ROPE_LINEAR) {
+      w /= f;
+    } else if (by_turns) {
+      const double keep = c->scaling == OSCAR_ROPE_BANDS ? (c->trained * w / (2.0 * pi) - low) / (high - low)
+                                                         : 1.0 - (i - a) / fmax(b - a, 0.001);
+      const double k = fmin(fmax(keep, 0.0), 1.0);
+      w = w * k + w / f * (1.0 - k);
+    }
+    // turns a position; whole turns do not count
+    const double turns = w / (2.0 * pi);
+    if (!std::isfinite(turns)) return OSCAR_ERR_INVALID_ARG;
+    t.turn[i] = (uint64_t)((turns - floor(turns)) * 18446744073709551616.0);
+  }
+  t.size = (float)(c->size != 0.0 ? c->size : c->scaling == OSCAR_ROPE_YARN && f > 1.0 ? 0.1 * log(f) + 1.0 : 1.0);
+  t.layout = c->layout;
+  t.dims = c->dims;
+  *out = t;
+  return OSCAR_OK;
+}
+
+oscar_status oscar_rope(oscar_ctx* ctx, const oscar_rope_table* table, const void* qkv, long long row,
+                        const int32_t* positions, const void* gamma_q, const void* gamma_k, float eps, int T,
+                        void* q, void* k, void* v, int batch, oscar_stream_t stream) {
+  const CallRange nvtx_range("oscar_rope");
+  if (!ctx || !table || batch < 0 || batch > ctx->cfg.max_batch || T < 0 || T > (1 << 24)) return OSCAR_ERR_INVALID_ARG;
+  if ((table->layout != OSCAR_ROPE_HALF && table->layout != OSCAR_ROPE_INTERLEAVED) || table->dims < 16 ||
+      table->dims > D || table->dims % 16)
+    return OSCAR_ERR_INVALID_ARG;
+  const int Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads;
+  if (row < (long long)(Hq + 2 * Hkv) * D || row % 8 || row > (1LL << 40)) return OSCAR_ERR_INVALID_ARG;
+  if (!gamma_q != !gamma_k || (gamma_q && !(eps >= 0.f && std::isfinite(eps)))) return OSCAR_ERR_INVALID_ARG;
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (dev != ctx->device) return OSCAR_ERR_INVALID_ARG;
+  if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
+  if (!qkv || !positions || !q || !k || !v || !aligned(qkv, 16) || !aligned(positions, 4) || !aligned(gamma_q, 16) ||
+      !aligned(gamma_k, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16))
+    return OSCAR_ERR_INVALID_ARG;
+  RopeArgs a;
+  memcpy(a.turn, table->turn, sizeof a.turn);
+  a.qkv = (const __nv_bfloat16*)qkv;
+  a.row = row;
+  a.positions = positions;
+  a.gamma_q = (const __nv_bfloat16*)gamma_q;
+  a.gamma_k = (const __nv_bfloat16*)gamma_k;
+  a.q = (__nv_bfloat16*)q;
+  a.k = (__nv_bfloat16*)k;
+  a.v = (__nv_bfloat16*)v;
+  a.eps = eps;
+  a.size = table->size;
+  a.B = batch;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.layout = table->layout;
+  a.dims = table->dims;
+  e = launch_rope(a, ctx->num_sms, (cudaStream_t)stream, &ctx->prof);
+  return e == cudaSuccess ? OSCAR_OK : cuda_status(e);
 }
 
 oscar_status oscar_quantize_rotated_f32(const float* x, int n, int group_size, float clip,

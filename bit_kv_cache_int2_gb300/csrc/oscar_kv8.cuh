@@ -104,6 +104,23 @@ struct Kv8Evict {
 __host__ __device__ __forceinline__ size_t kv8_evict_stride(int max_pages) { return 4 + 4 * (size_t)max_pages; }
 cudaError_t launch_kv8_evict(const Kv8Evict& a, int B, int num_sms, cudaStream_t st, Profiler* prof);
 
+struct Kv8Read {
+  CacheView cv;
+  __nv_bfloat16 *K, *V;  // [B][Hkv][n][128] or [B][n][Hkv][128]
+  int first, n, order;
+};
+cudaError_t launch_kv8_read(const Kv8Read& a, int type, int B, cudaStream_t st, Profiler* prof);
+
+struct Kv8Prefill {
+  CacheView cv;
+  const __nv_bfloat16 *q, *k, *v;  // [B][T][Hq or Hkv][128]
+  __nv_bfloat16* out;              // [B][T][Hq][128]
+  float* lse;                      // [B][T][Hq] or null
+  int B, T;
+};
+cudaError_t launch_kv8_prefill(const Kv8Prefill& a, int type, cudaStream_t st, Profiler* prof);
+size_t kv8_prefill_scratch();
+
 // The largest number of 16 KB units a request may have: the work list counts
 // 32 requests in 32 bits.
 constexpr long long KV8_MAX_UNITS = 1 << 26;

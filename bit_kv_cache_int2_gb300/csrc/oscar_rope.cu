@@ -1,0 +1,154 @@
+// Rotary positions (sm_103a): a layer's fused projection becomes queries, keys
+// and values, its query and key heads normalised (optional) and turned.
+//
+// Angles.  A pair's speed is a 64-bit fixed-point number of turns a position, so
+// position·speed mod 2^64 is the angle in turns, exactly: whole turns fall off
+// the top, whatever the position.  Its upper 32 bits as a signed fraction in
+// [-1/2, 1/2) give cosine and sine to fp32's precision.
+//
+// Eight lanes share a head, 16 channels (eight pairs) each, so a warp has four
+// heads at a time; cosines and sines are made once per token and warp.
+#include "oscar_internal.cuh"
+#include "oscar_rope.cuh"
+
+namespace oscar {
+
+namespace {
+
+constexpr int RW = 4;      // warps per CTA
+constexpr int HEADS = 4;   // heads a warp has at a time
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& x, float* f) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = lo_f(w[i]);
+    f[2 * i + 1] = hi_f(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+// Lane u of a head's eight has two groups of eight channels.  HALF: groups u and
+// u + dims/16, whose channels are each other's partners, for u < dims/16; the
+// groups behind dims, two by two, for the others.  INTERLEAVED: groups 2u, 2u + 1.
+// A warp takes heads 4·part, 4·(part + parts), .. of its token.
+template <int LAYOUT, bool NORM>
+__global__ void __launch_bounds__(RW * 32) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ uint64_t turn[64];
+  const int lane = threadIdx.x & 31, u = lane & 7, np = a.dims >> 4;
+  if (threadIdx.x < 64) turn[threadIdx.x] = a.turn[threadIdx.x];
+  __syncthreads();
+  const bool turned = LAYOUT == OSCAR_ROPE_HALF ? u < np : true;
+  const int ga = LAYOUT == OSCAR_ROPE_HALF && turned ? u : 2 * u;
+  const int gb = LAYOUT == OSCAR_ROPE_HALF && turned ? u + np : 2 * u + 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  float wq[16], wk[16];
+  if (NORM) {
+    unpack8(((const uint4*)a.gamma_q)[ga], wq);
+    unpack8(((const uint4*)a.gamma_q)[gb], wq + 8);
+    unpack8(((const uint4*)a.gamma_k)[ga], wk);
+    unpack8(((const uint4*)a.gamma_k)[gb], wk + 8);
+  }
+  const int heads = a.Hq + 2 * a.Hkv;
+  const long long tasks = (long long)a.B * a.T * a.parts, step = (long long)gridDim.x * RW;
+  for (long long task = (long long)blockIdx.x * RW + (threadIdx.x >> 5); task < tasks; task += step) {
+    const long long tok = task / a.parts;
+    const int part = (int)(task - tok * a.parts);
+    const int b = (int)(tok / a.T), t = (int)(tok - (long long)b * a.T);
+    const uint64_t pos = (uint64_t)((long long)a.positions[b] + t);
+    float cs[8], sn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // HALF: channels 8u + i and its partner; INTERLEAVED: the pairs of 16u .. 16u + 15
+      const int p = 8 * u + i;
+      if (2 * p < a.dims) {
+        const int ph = (int)(uint32_t)((pos * turn[p]) >> 32);
+        sincospif((float)ph * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31: half turns
+        sn[i] *= a.size;
+        cs[i] *= a.size;
+      } else {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+      }
+    }
+    const __nv_bfloat16* row = a.qkv + tok * a.row;
+    for (int h = HEADS * part + (lane >> 3); h < ((heads + HEADS - 1) & ~(HEADS - 1)); h += HEADS * a.parts) {
+      const bool in = h < heads;
+      uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+      if (in) {
+        xa = ((const uint4*)(row + (size_t)h * D))[ga];
+        xb = ((const uint4*)(row + (size_t)h * D))[gb];
+      }
+      if (in && h >= a.Hq + a.Hkv) {
+        uint4* to = (uint4*)(a.v + (tok * a.Hkv + h - a.Hq - a.Hkv) * D);
+        to[ga] = xa;
+        to[gb] = xb;
+      }
+      float f[16];
+      unpack8(xa, f);
+      unpack8(xb, f + 8);
+      if (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const bool isq = h < a.Hq;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] *= r * (isq ? wq[i] : wk[i]);
+      }
+      if (!in || h >= a.Hq + a.Hkv) continue;
+      float g[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = LAYOUT == OSCAR_ROPE_HALF ? i : 2 * i, y = LAYOUT == OSCAR_ROPE_HALF ? i + 8 : 2 * i + 1;
+        g[x] = f[x] * cs[i] - f[y] * sn[i];
+        g[y] = f[y] * cs[i] + f[x] * sn[i];
+      }
+      uint4* to = (uint4*)(h < a.Hq ? a.q + (tok * a.Hq + h) * D : a.k + (tok * a.Hkv + h - a.Hq) * D);
+      // channels that do not turn pass as they are (x - 0·y would lose them next to an infinity)
+      const bool ta = LAYOUT == OSCAR_ROPE_HALF ? turned : 16 * u < a.dims, tb = ta;
+      to[ga] = ta ? pack8(g) : pack8(f);
+      to[gb] = tb ? pack8(g + 8) : pack8(f + 8);
+    }
+  }
+}
+
+template <int LAYOUT>
+cudaError_t launch_layout(const RopeArgs& a, int ctas, cudaStream_t st) {
+  return a.gamma_q ? launch_pdl(rope_kernel<LAYOUT, true>, dim3(ctas), dim3(RW * 32), 0, st, a)
+                   : launch_pdl(rope_kernel<LAYOUT, false>, dim3(ctas), dim3(RW * 32), 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeArgs a, int num_sms, cudaStream_t st, Profiler* prof) {
+  const long long tokens = (long long)a.B * a.T, groups = (a.Hq + 2 * a.Hkv + HEADS - 1) / HEADS;
+  // a token's heads over several warps while there are few tokens
+  const long long warps = 32ll * num_sms;
+  long long parts = (warps + tokens - 1) / tokens;
+  if (parts > groups) parts = groups;
+  a.parts = (int)parts;
+  long long ctas = (tokens * parts + RW - 1) / RW;
+  if (ctas > 8ll * num_sms) ctas = 8ll * num_sms;
+  prof_begin(prof, OSCAR_KERNEL_PREFILL_PREP, st);
+  const cudaError_t e = a.layout == OSCAR_ROPE_HALF ? launch_layout<OSCAR_ROPE_HALF>(a, (int)ctas, st)
+                                                    : launch_layout<OSCAR_ROPE_INTERLEAVED>(a, (int)ctas, st);
+  prof_end(prof, OSCAR_KERNEL_PREFILL_PREP, st);
+  return e;
+}
+
+}  // namespace oscar

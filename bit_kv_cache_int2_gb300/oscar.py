@@ -55,6 +55,15 @@ WAIT_POLLS_DEFAULT = 1 << 22
 KV8_BLOCK = 16  # tokens per scale block of a cache with 8-bit history
 KV8_E4M3 = 0
 KV8_INT8 = 1
+ORDER_HEADS = 0   # dense keys and values [batch][Hkv][n][128]
+ORDER_TOKENS = 1  # [batch][n][Hkv][128]
+ROPE_HALF = 0         # channel pairs (i, i + dims / 2)
+ROPE_INTERLEAVED = 1  # (2i, 2i + 1)
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_NTK = 2
+ROPE_BANDS = 3
+ROPE_YARN = 4
 
 
 class OscarError(RuntimeError):
@@ -79,6 +88,15 @@ class oscar_layout_info(ctypes.Structure):
 class oscar_kv8_layout_info(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in (
         "head_bytes", "page_bytes", "off_scales", "weights_floats", "scratch_bytes")]
+
+
+class oscar_rope_config(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("dims", ctypes.c_int), ("scaling", ctypes.c_int)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "trained", "low", "high", "size")]
+
+
+class oscar_rope_table(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * 64), ("size", ctypes.c_float), ("layout", ctypes.c_int), ("dims", ctypes.c_int)]
 
 
 class oscar_cache(ctypes.Structure):
@@ -123,6 +141,16 @@ _SIGS = {
                           ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
     "oscar_evict_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                          ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_prefill_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                           ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                           ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_prefill_kv8_scratch_bytes": ([ctypes.POINTER(oscar_config)], ctypes.c_size_t),
+    "oscar_read_kv8": ([ctypes.c_void_p, ctypes.POINTER(oscar_cache), ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
+    "oscar_make_rope": ([ctypes.POINTER(oscar_rope_config), ctypes.POINTER(oscar_rope_table)], ctypes.c_int),
+    "oscar_rope": ([ctypes.c_void_p, ctypes.POINTER(oscar_rope_table), ctypes.c_void_p, ctypes.c_longlong, ctypes.c_void_p,
+                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                    ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p], ctypes.c_int),
     "oscar_quantize_rotated_f32": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "oscar_debug_rotate": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
@@ -602,6 +630,92 @@ def bind_evict_kv8(ctx, cache: dict, weights, budget, scratch, batch, stream=Non
     return call
 
 
+def oscar_prefill_kv8(ctx, cache: dict, kv_type, q, k, v, T, out, lse, scratch, batch, stream=None):
+    """T new tokens per request (q [batch][T][Hq][128], k, v [batch][T][Hkv][128]) attend to a
+    cache with 8-bit history and causally to one another.  The chunk is not stored."""
+    cs = _cache_struct(cache)
+    _check(lib().oscar_prefill_kv8(ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(k), _ptr(v), T, _ptr(out), _ptr(lse),
+                                   _ptr(scratch), scratch.numel() * scratch.element_size(), batch, _stream(stream)),
+           "oscar_prefill_kv8")
+
+
+def bind_prefill_kv8(ctx, cache: dict, kv_type, q, k, v, T, out, lse, scratch, batch, stream=None):
+    """oscar_prefill_kv8 with every argument marshalled once: returns a
+    no-argument callable."""
+    cs = _cache_struct(cache)
+    args = (ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(k), _ptr(v), T, _ptr(out), _ptr(lse), _ptr(scratch),
+            scratch.numel() * scratch.element_size(), batch, _stream(stream))
+    fn = lib().oscar_prefill_kv8
+
+    def call():
+        _check(fn(*args), "oscar_prefill_kv8")
+
+    call._keep = cs
+    return call
+
+
+def oscar_read_kv8(ctx, cache: dict, kv_type, first, n, K, V, batch, order=ORDER_HEADS, stream=None):
+    """The cached tokens at places first .. first + n - 1 of each request as dense bf16 keys and
+    values, [batch][Hkv][n][128] or (ORDER_TOKENS) [batch][n][Hkv][128]; rows behind a
+    request's end stay as they are."""
+    cs = _cache_struct(cache)
+    _check(lib().oscar_read_kv8(ctx, ctypes.byref(cs), kv_type, first, n, order, _ptr(K), _ptr(V), batch, _stream(stream)),
+           "oscar_read_kv8")
+
+
+def bind_read_kv8(ctx, cache: dict, kv_type, first, n, K, V, batch, order=ORDER_HEADS, stream=None):
+    """oscar_read_kv8 with every argument marshalled once: returns a no-argument callable."""
+    cs = _cache_struct(cache)
+    args = (ctx, ctypes.byref(cs), kv_type, first, n, order, _ptr(K), _ptr(V), batch, _stream(stream))
+    fn = lib().oscar_read_kv8
+
+    def call():
+        _check(fn(*args), "oscar_read_kv8")
+
+    call._keep = cs
+    return call
+
+
+def make_rope(layout=ROPE_HALF, dims=HEAD_DIM, theta=1e6, scaling=ROPE_PLAIN, factor=1.0, trained=0.0, low=0.0, high=0.0,
+              size=0.0) -> oscar_rope_table:
+    """The turning speeds of a model's rotary positions (host only; made once)."""
+    cfg = oscar_rope_config(layout, dims, scaling, theta, factor, trained, low, high, size)
+    out = oscar_rope_table()
+    _check(lib().oscar_make_rope(ctypes.byref(cfg), ctypes.byref(out)), "oscar_make_rope")
+    return out
+
+
+def _rope_args(ctx, table, qkv, positions, T, q, k, v, batch, gamma_q, gamma_k, eps, row, stream):
+    if row is None and qkv is not None:  # from one token's row to the next in a [batch][T][heads][128] or [batch][T][row] array
+        row = qkv.stride(0) if T == 1 else qkv.stride(1)
+        if T > 1 and batch > 1 and qkv.stride(0) != T * row:
+            raise ValueError("the tokens' rows are not evenly apart")
+        if any(n > 1 and qkv.stride(i) != step for i, n, step in ((qkv.dim() - 1, qkv.shape[-1], 1),
+                                                                  (2, qkv.shape[2] if qkv.dim() == 4 else 1, HEAD_DIM))):
+            raise ValueError("a token's row is not dense")
+    return (ctx, ctypes.byref(table), _ptr(qkv), row or 0, _ptr(positions), _ptr(gamma_q), _ptr(gamma_k), eps, T, _ptr(q),
+            _ptr(k), _ptr(v), batch, _stream(stream))
+
+
+def oscar_rope(ctx, table, qkv, positions, T, q, k, v, batch, gamma_q=None, gamma_k=None, eps=1e-6, row=None, stream=None):
+    """Splits a projection's rows (qkv [batch][T][Hq + 2 Hkv][128]) into q, k and v, normalises query
+    and key heads (with gammas, bf16 [128]) and turns them by positions[b] + t (int32 [batch])."""
+    _check(lib().oscar_rope(*_rope_args(ctx, table, qkv, positions, T, q, k, v, batch, gamma_q, gamma_k, eps, row, stream)),
+           "oscar_rope")
+
+
+def bind_rope(ctx, table, qkv, positions, T, q, k, v, batch, gamma_q=None, gamma_k=None, eps=1e-6, row=None, stream=None):
+    """oscar_rope with every argument marshalled once: returns a no-argument callable."""
+    args = _rope_args(ctx, table, qkv, positions, T, q, k, v, batch, gamma_q, gamma_k, eps, row, stream)
+    fn = lib().oscar_rope
+
+    def call():
+        _check(fn(*args), "oscar_rope")
+
+    call._keep = table
+    return call
+
+
 def oscar_quantize_rotated_f32(x, group_size, clip, which, codes, sz, stream=None):
     _check(lib().oscar_quantize_rotated_f32(_ptr(x), x.shape[0], group_size, float(clip), which, _ptr(codes),
                                             _ptr(sz), _stream(stream)), "oscar_quantize_rotated_f32")
@@ -684,11 +798,12 @@ def alloc_scratch(cfg: oscar_config, device="cuda", prefill=False):
     return torch.empty((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 
-def alloc_scratch_kv8(cfg: oscar_config, device="cuda"):
-    """Working memory of oscar_decode_kv8 and oscar_evict_kv8 (one at a time)."""
+def alloc_scratch_kv8(cfg: oscar_config, device="cuda", prefill=False):
+    """Working memory of oscar_decode_kv8 and oscar_evict_kv8, or (prefill) of
+    oscar_prefill_kv8 (one call at a time)."""
     import torch
 
-    n = oscar_layout_kv8(cfg).scratch_bytes
+    n = lib().oscar_prefill_kv8_scratch_bytes(ctypes.byref(cfg)) if prefill else oscar_layout_kv8(cfg).scratch_bytes
     return torch.empty((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 

@@ -593,6 +593,130 @@ oscar_status oscar_decode_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type
 oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* weights, int budget,
                              void* scratch, size_t scratch_bytes, int batch, oscar_stream_t stream);
 
+/* Chunk attention over a cache with 8-bit history: for each b < batch, T new
+ * tokens attend to the request's cache as it stands (sink, 8-bit history, recent
+ * window) and causally to the chunk itself (chunk token t sees chunk tokens
+ * 0..t), one softmax over all of them per (token, query head): a few drafted
+ * tokens, a chunk, or a whole prompt over an empty cache.  The chunk is NOT
+ * stored: oscar_append_kv8 does that, with the same k and v, afterwards.
+ *   q    : device bf16 [batch][T][num_q_heads][128]
+ *   k, v : device bf16 [batch][T][num_kv_heads][128], the chunk's keys and values
+ *   T    : 0 .. 2^24, the same for every request.  With T = 0 or batch = 0 nothing is
+ *          done, and the pointers may be NULL
+ *   out  : device bf16 [batch][T][num_q_heads][128], not overlapping an input
+ *   lse  : device float [batch][T][num_q_heads] natural-log log-sum-exp of the
+ *          scaled logits, or NULL
+ *   scratch : device buffer of at least oscar_prefill_kv8_scratch_bytes bytes,
+ *          256-byte aligned, no initial contents needed; not to be shared by
+ *          calls that may overlap, also of two captured graphs
+ * q, k, v, out are device memory, 16-byte aligned.  A value that is not finite
+ * shows in the rows that see its token and in no other.
+ * A request whose lengths no append can have left (OSCAR_ERR_STATE) counts as
+ * empty: its tokens see the chunk alone.  Other device errors:
+ * OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad history page, whose
+ * tokens are left out; OSCAR_ERR_TIMEOUT: rows that were not computed are NaN. */
+oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, const void* k,
+                               const void* v, int T, void* out, float* lse, void* scratch, size_t scratch_bytes,
+                               int batch, oscar_stream_t stream);
+
+/* Scratch of oscar_prefill_kv8 for any T and any batch up to max_batch, 0 for a
+ * configuration that oscar_layout_kv8 refuses.  Host only. */
+size_t oscar_prefill_kv8_scratch_bytes(const oscar_config* cfg);
+
+/* Order of dense keys and values. */
+typedef enum {
+  OSCAR_ORDER_HEADS = 0, /* [batch][num_kv_heads][n][128], as the bulk imports take them     */
+  OSCAR_ORDER_TOKENS = 1 /* [batch][n][num_kv_heads][128], as oscar_append_kv8 takes them    */
+} oscar_order;
+
+/* Reads cached tokens back: those at places first .. first + n - 1 of each request
+ * b < batch (its sink, history and window in that order; after an eviction places
+ * are no longer positions), as dense bf16 keys and values: history as code·scale
+ * in fp32 rounded to BF16 (NaN for a block that held a value that is not finite),
+ * sink and window as they are.
+ *   first, n : >= 0, first + n <= 2^30;  order : an oscar_order
+ *   K, V : device bf16 in that order, 16-byte aligned.  Rows of places behind the
+ *          end of a request are left as they were.
+ * With n = 0 or batch = 0 nothing is done, and K and V may be NULL.
+ * Device errors: OSCAR_ERR_STATE for a request whose lengths no append can have
+ * left (all its rows are left as they were), OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE
+ * for a missing or bad page (the rows of its tokens are). */
+oscar_status oscar_read_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, int first, int n, int order,
+                            void* K, void* V, int batch, oscar_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, the step from a layer's fused projection to the calls above
+ * (the pages take queries and keys as they come out of it).  Channel pair i of a
+ * head is turned by the angle position·w_i.  With n = dims / 2 pairs,
+ * w_i = theta^(-2i / dims), f = factor and the turns t_i = trained·w_i / 2π of a
+ * pair over the positions that the model was trained on:
+ *   OSCAR_ROPE_PLAIN   w_i
+ *   OSCAR_ROPE_LINEAR  w_i / f
+ *   OSCAR_ROPE_NTK     w_i with theta·f^(dims / (dims - 2)) for theta
+ *   OSCAR_ROPE_BANDS   (1 - c) w_i / f + c w_i, c = (t_i - low) / (high - low) in 0..1
+ *   OSCAR_ROPE_YARN    the same with c = 1 - (i - a) / max(b - a, 0.001) in 0..1,
+ *                      a = max(floor(i(high)), 0), b = min(ceil(i(low)), n - 1) and
+ *                      i(t) = dims ln(trained / 2πt) / (2 ln theta), the (real) pair
+ *                      that makes t turns */
+typedef enum {
+  OSCAR_ROPE_HALF = 0,       /* pair i: channels i and i + dims / 2 */
+  OSCAR_ROPE_INTERLEAVED = 1 /* pair i: channels 2i and 2i + 1      */
+} oscar_rope_layout;
+
+typedef enum {
+  OSCAR_ROPE_PLAIN = 0,
+  OSCAR_ROPE_LINEAR = 1,
+  OSCAR_ROPE_NTK = 2,
+  OSCAR_ROPE_BANDS = 3,
+  OSCAR_ROPE_YARN = 4
+} oscar_rope_scaling;
+
+typedef struct {
+  int layout;       /* an oscar_rope_layout                                          */
+  int dims;         /* turned channels, the head's first ones: 16, 32, .. 128        */
+  int scaling;      /* an oscar_rope_scaling                                         */
+  double theta;     /* > 1                                                           */
+  double factor;    /* > 0; not used by OSCAR_ROPE_PLAIN                             */
+  double trained;   /* > 0; used by OSCAR_ROPE_BANDS and OSCAR_ROPE_YARN             */
+  double low, high; /* turns, 0 < low < high; 0, 0: 1 and 4 (BANDS), 1 and 32 (YARN) */
+  double size;      /* what cosine and sine are multiplied by; 0: 1, for OSCAR_ROPE_YARN
+                       0.1 ln(factor) + 1 (1 where factor < 1)                       */
+} oscar_rope_config;
+
+typedef struct {
+  uint64_t turn[64]; /* w_i / 2π in units of 2^-64 turns a position */
+  float size;
+  int layout, dims;
+} oscar_rope_table;
+
+/* The table of a configuration.  Host only; made once per model.
+ * OSCAR_ERR_UNSUPPORTED for other dims, OSCAR_ERR_INVALID_ARG for other values. */
+oscar_status oscar_make_rope(const oscar_rope_config* config, oscar_rope_table* out);
+
+/* Splits the projection of T new tokens of each request b < batch into queries,
+ * keys and values, normalises query and key heads (with gamma_q and gamma_k:
+ * x·gamma / sqrt(mean(x²) + eps) over a head's 128 channels) and turns them by
+ * their positions; fp32, rounded once to BF16.  Values are copied.
+ *   qkv : device bf16 [batch][T][row], token rows of num_q_heads query heads, then
+ *         num_kv_heads key heads, then num_kv_heads value heads, 128 channels each
+ *   row : elements from one token's row to the next: at least
+ *         (num_q_heads + 2 num_kv_heads)·128, a multiple of 8
+ *   positions : device int32 [batch], the position of each request's first new
+ *         token; token t is at positions[b] + t.  Any values (angles are exact to
+ *         2^-24 of a turn); after an eviction they differ from seq_lens
+ *   gamma_q, gamma_k : device bf16 [128], or both NULL: no norm
+ *   eps : >= 0 and finite; not used without gammas
+ *   T : 0 .. 2^24.  With T = 0 or batch = 0 nothing is done, and the pointers may be NULL
+ *   q : device bf16 [batch][T][num_q_heads][128];  k, v : [batch][T][num_kv_heads][128],
+ *         what oscar_prefill_kv8, oscar_append_kv8 and, with T = 1, the decode
+ *         calls take.  Not overlapping qkv
+ * All arrays 16-byte aligned (positions: 4).  The context's device must be the
+ * current device (OSCAR_ERR_INVALID_ARG otherwise).  `table` is host memory, read
+ * before the call returns. */
+oscar_status oscar_rope(oscar_ctx* ctx, const oscar_rope_table* table, const void* qkv, long long row,
+                        const int32_t* positions, const void* gamma_q, const void* gamma_k, float eps, int T,
+                        void* q, void* k, void* v, int batch, oscar_stream_t stream);
+
 /* Test hook: the demotion's quantiser and packer on given rotated fp32
  * vectors, so that codes and bytes can be compared bit for bit.
  *   x : device float [n][128] rotated channels
@@ -645,12 +769,12 @@ int oscar_last_cuda_error(void);
  * reset != 0 forgets everything recorded so far. */
 typedef enum {
   OSCAR_KERNEL_APPEND = 0,      /* append / demote                      */
-  OSCAR_KERNEL_IMPORT = 1,      /* all bulk-import kernels              */
+  OSCAR_KERNEL_IMPORT = 1,      /* all bulk-import kernels, read back   */
   OSCAR_KERNEL_DECODE_PREP = 2, /* q rotation, work-counter reset       */
   OSCAR_KERNEL_DECODE_MAIN = 3, /* split-K decode over history + window */
   OSCAR_KERNEL_DECODE_MERGE = 4,/* partial merge + un-rotation          */
   OSCAR_KERNEL_STEP = 5,        /* oscar_decode_step's append + q rotation */
-  OSCAR_KERNEL_PREFILL_PREP = 6,  /* prefill: q rotation and scaling       */
+  OSCAR_KERNEL_PREFILL_PREP = 6,  /* prefill: q rotation and scaling; rotary positions */
   OSCAR_KERNEL_PREFILL_ATTN = 7,  /* prefill: split attention over regions */
   OSCAR_KERNEL_PREFILL_MERGE = 8, /* prefill: split merge + un-rotation    */
   OSCAR_KERNEL_KV8_APPEND = 9,  /* 8-bit history: append                   */

@@ -135,6 +135,25 @@ class Request:
                         self.w_ring[h, slot] = self.w_ring[h, slot] * decay + win[j:j + BLK].sum()
         return out, lse, ps
 
+    def chunk(self, q, k, v):
+        """T new tokens over the request and causally over one another: q [T][Hkv][G][128],
+        k, v [T][Hkv][128] -> (out, lse, p [Hkv][T][G][L + T])."""
+        T, _, G, _ = q.shape
+        out, lse = np.zeros(q.shape), np.zeros(q.shape[:3])
+        ps = np.zeros((self.Hkv, T, G, self.L + T))
+        with np.errstate(invalid="ignore", over="ignore"):
+            for h in range(self.Hkv):
+                K, V = self.tokens(h)
+                K, V = np.concatenate([K, k[:, h]]), np.concatenate([V, v[:, h]])
+                for t in range(T):
+                    n = self.L + t + 1
+                    z = q[t, h].astype(np.float64) @ K[:n].T / np.sqrt(D)
+                    m = z.max(1, keepdims=True)
+                    e = np.exp(z - m)
+                    ps[h, t, :, :n] = e / e.sum(1, keepdims=True)
+                    out[t, h], lse[t, h] = ps[h, t, :, :n] @ V[:n], m[:, 0] + np.log(e.sum(1))
+        return out, lse, ps
+
     def evict(self, budget, weights):
         """weights [Hkv][blocks]: the fp32 values that decide."""
         e = max(self.H - budget, 0) // RING * 16
