@@ -1013,7 +1013,7 @@ oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* we
 }
 
 size_t oscar_prefill_kv8_scratch_bytes(const oscar_config* cfg) {
-  return check_cfg(cfg) == OSCAR_OK && kv8_supported(*cfg) ? kv8_prefill_scratch() : 0;
+  return check_cfg(cfg) == OSCAR_OK && kv8_supported(*cfg) ? kv8_prefill_scratch(KV8_PREFILL_MAX_GRID).total : 0;
 }
 
 oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, const void* q, const void* k,
@@ -1024,7 +1024,9 @@ oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int typ
   if (s != OSCAR_OK) return s;
   if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
   if (T < 0 || T > (1 << 24)) return OSCAR_ERR_INVALID_ARG;
-  if (!scratch || !aligned(scratch, 256) || scratch_bytes < kv8_prefill_scratch()) return OSCAR_ERR_INVALID_ARG;
+  const int grid = ctx->num_sms < KV8_PREFILL_MAX_GRID ? ctx->num_sms : KV8_PREFILL_MAX_GRID;
+  const Kv8PrefillScratch sl = kv8_prefill_scratch(grid);
+  if (!scratch || !aligned(scratch, 256) || scratch_bytes < sl.total) return OSCAR_ERR_INVALID_ARG;
   if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
       (lse && !aligned(lse, 4)))
@@ -1041,6 +1043,10 @@ oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int typ
     a.lse = lse ? lse + tok * Hq : nullptr;
     a.B = batch - b0 < KV8_MAX_REQUESTS ? batch - b0 : KV8_MAX_REQUESTS;
     a.T = T;
+    a.splits = (int4*)scratch;
+    a.part = (float*)((uint8_t*)scratch + sl.off_part);
+    a.grid = grid;
+    a.wait_polls = ctx->wait_polls;
     const cudaError_t e = launch_kv8_prefill(a, type, (cudaStream_t)stream, &ctx->prof);
     if (e != cudaSuccess) return cuda_status(e);
   }

@@ -116,10 +116,16 @@ struct Kv8Prefill {
   const __nv_bfloat16 *q, *k, *v;  // [B][T][Hq or Hkv][128]
   __nv_bfloat16* out;              // [B][T][Hq][128]
   float* lse;                      // [B][T][Hq] or null
-  int B, T;
+  int4* splits;                    // scratch [grid]: the unit that begins in a CTA's part and ends in a later one's
+  float* part;                     // scratch [grid][2][256][PART_STRIDE]: m, l, M, o (oscar_kv8_prefill.cu)
+  int B, T, grid, wait_polls;
+};
+constexpr int KV8_PREFILL_MAX_GRID = 160;  // CTAs (one per SM) that the scratch has records for
+struct Kv8PrefillScratch {
+  size_t off_part, total;
 };
 cudaError_t launch_kv8_prefill(const Kv8Prefill& a, int type, cudaStream_t st, Profiler* prof);
-size_t kv8_prefill_scratch();
+Kv8PrefillScratch kv8_prefill_scratch(int grid);
 
 // The largest number of 16 KB units a request may have: the work list counts
 // 32 requests in 32 bits.

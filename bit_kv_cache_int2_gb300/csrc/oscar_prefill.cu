@@ -21,6 +21,7 @@
 //  prefill_merge_kernel  per 8 rows: combines the history slices, un-rotates
 //                        them by R_V^T and merges the window partial.
 #include "oscar_internal.cuh"
+#include "oscar_tcgen05.cuh"
 
 namespace oscar {
 namespace {
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(PrefillArgs a) {
 // (N = 144, a multiple of 16).  O is rescaled lazily: only when a row maximum
 // grows by more than LAZY (log2 units); until then P may reach 2^LAZY.
 namespace tc {
+using namespace tcgen05;
 constexpr int THREADS = 576;
 constexpr int DQ0 = 256;    // first producer thread
 constexpr int MMA_WARP = 16, TMA_WARP = 17;
@@ -695,87 +697,10 @@ static_assert(OFF_KV % 1024 == 0 && KV_BYTES % 1024 == 0 && K_BYTES % 1024 == 0,
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(OFF_BAR % 8 == 0 && OFF_INFO % 8 == 0, "alignment");
 
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 B apart (the leading offset is unused for this layout).
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc));
-}
-
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"((uint32_t)__cvta_generic_to_shared(bar))
-               : "memory");
-}
-
-#define OSCAR_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
-                    "=r"(r[i + 6]), "=r"(r[i + 7])
-// 32 consecutive 32-bit TMEM columns of this warp's 32 lanes, one lane per thread
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : OSCAR_R8(0), OSCAR_R8(8), OSCAR_R8(16), OSCAR_R8(24)
-      : "r"(taddr));
-}
-#undef OSCAR_R8
-
-#define OSCAR_W8(i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
-                    "r"(v[i + 6]), "r"(v[i + 7])
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      OSCAR_W8(0), OSCAR_W8(8), OSCAR_W8(16), OSCAR_W8(24)
-      : "memory");
-}
-#undef OSCAR_W8
-// One 32-bit TMEM column of this warp's 32 lanes (waits for it).
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" : "+r"(r)::"memory");
-  return __uint_as_float(r);
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
 __device__ __forceinline__ uint32_t ex2_h2(uint32_t x) {
   uint32_t y;
   asm("ex2.approx.f16x2 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Bounded wait that also gives up as soon as another role has aborted.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const uint32_t a = (uint32_t)__cvta_generic_to_shared(bar);
-  for (int it = 0; it < (1 << 22); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((it & 63) == 63 && *abort_flag) return false;
-  }
-  *abort_flag = 1;
-  return false;
 }
 
 // The 128 threads of a producer group agree on a wait's outcome (named
@@ -791,18 +716,6 @@ __device__ __forceinline__ bool group_all(uint32_t id, bool ok) {
       : "memory");
   return r != 0;
 }
-
-// TMEM loads complete at tcgen05.wait::ld; the registers pass through the
-// wait so that no use of them is scheduled before it.
-#define OSCAR_P8(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), \
-                    "+r"(r[i + 6]), "+r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" : OSCAR_P8(0), OSCAR_P8(8), OSCAR_P8(16), OSCAR_P8(24)::"memory");
-}
-__device__ __forceinline__ void regs_after(uint32_t (&r)[32]) {
-  asm volatile("" : OSCAR_P8(0), OSCAR_P8(8), OSCAR_P8(16), OSCAR_P8(24)::"memory");
-}
-#undef OSCAR_P8
 
 // K chunk I (channels 64A + 8I .. +7) of token tr: words 2D + A, D = 0..3.
 template <int I>
