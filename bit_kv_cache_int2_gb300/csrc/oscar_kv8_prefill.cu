@@ -13,10 +13,10 @@
 // (S of each row tile 128 columns, P over the first half of its S, O 128), Q, K, V
 // in shared memory, 128-byte swizzled.  Warps:
 //   0-7   softmax, four for each row tile, a thread per row
-//   8-11  producers: history codes from global memory through registers to FP16
+//   8-15  producers, one for each block of 16 tokens: history codes from global memory through registers to FP16
 //         tiles (both code types are exact there), BF16 tokens by cp.async as they
 //         are; K and V tiles alternate in a ring of five
-//   12    the MMAs: S of the step after next is issued behind O of this one, so the
+//   16    the MMAs: S of the step after next is issued behind O of this one, so the
 //         tensor cores work on one row tile while the other's softmax runs
 // Steps (a row tile and a token tile) go to the two softmax groups in turn.  A unit
 // of at most 128 rows has one row tile: then its token tiles go to the groups in
@@ -43,30 +43,47 @@ namespace {
 using namespace tcgen05;
 
 constexpr int ROWS = 256, TILE = 128;
-constexpr int THREADS = 416, PROD0 = 256, MMA_WARP = 12;
+constexpr int PROD_WARPS = 8, PROD = 32 * PROD_WARPS;  // a warp for each 16-token block of a tile
+constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 17-19 fill the MMA warp's group up
+// Registers a thread: 256·144 + 256·80 + 128·32 = the 640·96 of the launch.
+constexpr int REGS_SOFTMAX = 144, REGS_PROD = 80, REGS_MMA = 32;
 constexpr int NBUF = 5, REGION = 16384, BUF = 2 * REGION;  // a tile: two regions of 64 channels, [128 rows][128 B]
-constexpr int NINFO = 4, NALPHA = 3;
+constexpr int NINFO = 4, NALPHA = 3, NUNIT = 8;
 constexpr int OFF_Q = 0, OFF_BUF = 2 * BUF, OFF_BAR = OFF_BUF + NBUF * BUF;
 enum {
   B_FULL = 0, B_EMPTY = B_FULL + NBUF, B_INFO = B_EMPTY + NBUF, B_S = B_INFO + NINFO, B_P = B_S + 2, B_O = B_P + 2,
-  B_QFULL = B_O + 2, B_QEMPTY, B_DRAIN, NBARS
+  B_QFULL = B_O + 2, B_QEMPTY, B_OTHER, B_TAKEN, B_DRAIN, NBARS
 };
 // A token tile's scales: x = S·a·(2^exponent of the row), b = log2 s_V.
 struct Info {
   float2 cs[8];
-  uint8_t valid[4], nanv[4];  // two bits a producer warp: blocks that count, blocks whose value scale is NaN
-  uint32_t pad[2];
+  uint8_t marks[8];  // of the blocks: 1 it counts, 2 its value scale is NaN
+  uint32_t flags, pad;
 };
-constexpr int OFF_INFO = OFF_BAR + 192, OFF_ALPHA = OFF_INFO + NINFO * (int)sizeof(Info);
-constexpr int OFF_XCH = OFF_ALPHA + NALPHA * ROWS, OFF_MISC = OFF_XCH + TILE * 12;
+constexpr uint32_t ALL_COUNT = 0x01010101u;  // four marks
+// What the MMA warp needs to know of a token tile.
+enum { F_HIST = 1, F_TWO = 2, F_NEWQ = 4, F_ENDQ = 8, F_ENDU = 16 };
+// A unit, as the softmax needs it (one producer follows the work list for all: its
+// state does not fit into the registers of a softmax thread).
+struct alignas(16) Unit {
+  int tiles, hist;  // its tiles in this part, the first of them history
+  int line;         // of the BF16 tokens in its first other tile, those that its first row sees
+  int flags;        // U_TWO: two row tiles; U_BEGINS, U_ENDS: it does so in this part
+  int b, h, t0, t1; // tokens t0 .. t1 - 1
+  int c0, c1;       // chunk tokens in this part's tiles
+  int pad[2];
+};
+enum { U_TWO = 1, U_BEGINS = 2, U_ENDS = 4 };
+constexpr int OFF_INFO = OFF_BAR + 208, OFF_UNIT = OFF_INFO + NINFO * (int)sizeof(Info), OFF_ALPHA = OFF_UNIT + NUNIT * (int)sizeof(Unit);
+constexpr int OFF_XCH = OFF_ALPHA + NALPHA * ROWS, OFF_MISC = OFF_XCH + TILE * 8;
 struct Misc {
   uint32_t tmem;
-  int abort, bad_v, n;
-  long long lo, hi, at, W;
+  int abort, bad_v, pad0;
+  long long lo, hi, at;
   int b, h, rt, pad;
 };
 constexpr int SMEM = OFF_MISC + (int)sizeof(Misc);
-static_assert(NBARS * 8 <= 192 && sizeof(Info) == 80 && OFF_XCH % 4 == 0 && OFF_MISC % 8 == 0, "layout");
+static_assert(NBARS * 8 <= 208 && sizeof(Info) == 80 && sizeof(Unit) == 48 && OFF_UNIT % 16 == 0 && OFF_XCH % 8 == 0 && OFF_MISC % 8 == 0, "layout");
 static_assert(SMEM <= 227 * 1024, "shared memory");
 constexpr int S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float C0 = INV_SQRT_D * LOG2E;
@@ -152,13 +169,9 @@ struct Walk {
   __device__ int line_begin() const { return i0 > r.nh ? i0 : r.nh; }
 };
 
-// What the merge needs to know of the unit that begins in a CTA's part and ends
-// in a later one's.
-struct Split {
-  int b, h, rt, last;  // last: the CTA with its last tile, -1: no such unit
-};
-
-// By warp 0: the CTA's part.  pre: [B] in shared memory.
+// By warp 0: the CTA's part, and (splits) the unit that begins in it and ends in a later
+// one's: request, head, unit and the CTA with its last tile, -1 if there is none.
+// pre: [B] in shared memory.
 __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
   const Geo g(a);
   const CacheView& cv = a.cv;
@@ -182,20 +195,24 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     W += __shfl_sync(0xffffffffu, inc, 31);
   }
   __syncwarp();
-  if (lane) return;
   Balanced bl;
   bl.W = W;
   bl.n = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
-  m->W = W;
-  m->n = bl.n;
-  m->lo = m->hi = m->at = 0;
-  if ((int)blockIdx.x >= bl.n) return;
-  m->lo = balanced_lo(bl, blockIdx.x);
-  m->hi = balanced_lo(bl, blockIdx.x + 1);
-  const int b = balanced_request(pre, a.B, m->lo);
+  const bool any = (int)blockIdx.x < bl.n;
+  const long long lo = any ? balanced_lo(bl, blockIdx.x) : 0, hi = any ? balanced_lo(bl, blockIdx.x + 1) : 0;
+  if (lane == 0) {
+    m->lo = lo;
+    m->hi = hi;
+    m->at = 0;
+    if (!any) a.splits[blockIdx.x] = make_int4(0, 0, 0, -1);
+  }
+  if (!any || lane > 1) return;
+  // lane 0 finds the part's first unit, lane 1 its last
+  const long long at = lane == 0 ? lo : hi - 1;
+  const int b = balanced_request(pre, a.B, at);
   Lens r;
   r.load(cv, b);
-  const long long per = r.per_head(g), in = m->lo - pre[b];
+  const long long per = r.per_head(g), in = at - pre[b];
   const int h = (int)(in / per);
   const long long x = in - h * per;
   int rt = 0, top = g.RT - 1;
@@ -203,10 +220,17 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     const int mid = (rt + top + 1) >> 1;
     if (r.before(g, mid) <= x) rt = mid; else top = mid - 1;
   }
-  m->b = b;
-  m->h = h;
-  m->rt = rt;
-  m->at = pre[b] + h * per + r.before(g, rt);
+  const long long begin = pre[b] + h * per + r.before(g, rt);
+  if (lane == 0) {
+    m->b = b;
+    m->h = h;
+    m->rt = rt;
+    m->at = begin;
+  } else {
+    const int t1 = g.T - rt * g.c < g.c ? g.T : (rt + 1) * g.c;
+    const long long end = begin + r.nh + (r.w + t1 + TILE - 1) / TILE;
+    a.splits[blockIdx.x] = make_int4(b, h, rt, begin >= lo && end > hi ? balanced_owner(bl, end - 1) : -1);
+  }
 }
 
 // -------------------------------------------------------------------- producers
@@ -304,9 +328,10 @@ struct Producer {
   uint8_t* smem;
   uint64_t* bars;
   Misc* misc;
-  int t, wp, lane;  // thread of 128, warp of 4
+  int t, wp, lane;  // thread of 256, warp of 8
   bool ok = true;
-  int gt = 0, qn = 0;  // token tiles, loads of Q
+  int gt = 0, qn = 0, un = 0;  // token tiles, loads of Q, units
+  bool told = false;           // this unit is published
   // Copies under way whose barrier has not been told: at most two.  cut: tokens
   // from, to of a V tile whose values are zeroed where they are not finite.
   struct Pending {
@@ -326,8 +351,8 @@ struct Producer {
   __device__ void tell(const Pending& p) {
     if (p.from < p.to) {  // this thread's own pieces
 #pragma unroll 1
-      for (int i = 0; i < 16; ++i) {
-        const int tok = 8 * i + (t >> 4), ch = t & 15;
+      for (int i = 0; i < 8; ++i) {
+        const int tok = 16 * i + (t >> 4), ch = t & 15;
         uint4* x = (uint4*)(smem + OFF_BUF + p.buf * BUF + (ch >> 3) * REGION + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
         if (tok < p.from || tok >= p.to) continue;
         uint32_t w[4] = {x->x, x->y, x->z, x->w};
@@ -366,15 +391,30 @@ struct Producer {
     npend = 0;
   }
 
-  __device__ void info(float2 cs, int valid, int nanv) {
-    Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
-    if (lane < 2) f->cs[2 * wp + lane] = cs;
+  // With the unit's first tile.  NUNIT: the place's last unit lies six tiles or more behind
+  // the last tile whose O is done, so both softmax groups have left it.
+  __device__ void publish(const Walk& u) {
+    told = true;
+    if (t != 0) return;
+    Unit* x = (Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
+    x->tiles = u.i1 - u.i0;
+    x->hist = max(u.hist_end() - u.i0, 0);
+    const int s0 = (u.line_begin() - u.r.nh) * TILE;
+    x->line = u.r.w + u.t0 + 1 - s0;
+    const bool begins = u.i0 == 0, ends = u.i1 == u.n;
+    x->flags = (u.two ? U_TWO : 0) | (begins ? U_BEGINS : 0) | (ends ? U_ENDS : 0);
+    x->b = u.b, x->h = u.h, x->t0 = u.t0, x->t1 = u.t1;
+    x->c0 = s0 - u.r.w, x->c1 = (u.i1 - u.r.nh) * TILE - u.r.w;
+  }
+  __device__ void info(const Walk& u, float2 cs, int mark, uint32_t flags) {
+    if (!told) publish(u);
     if (lane == 0) {
-      f->valid[wp] = (uint8_t)valid;
-      f->nanv[wp] = (uint8_t)nanv;
+      Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
+      f->cs[wp] = cs;
+      f->marks[wp] = (uint8_t)mark;
+      if (wp == 0) f->flags = flags;
+      arrive(&bars[B_INFO + (gt & (NINFO - 1))]);
     }
-    __syncwarp();
-    if (lane == 0) arrive(&bars[B_INFO + (gt & (NINFO - 1))]);
   }
 
   // Rows of the unit, 16 lanes a row: token and head of row i, 16-byte piece t & 15.
@@ -395,17 +435,17 @@ struct Producer {
     int8_t* al = (int8_t*)(smem + OFF_ALPHA) + qn % NALPHA * ROWS;
     const int rows = u.two ? ROWS : TILE;
 #pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 32) {
+    for (int r0 = 0; r0 < rows; r0 += 64) {
       uint4 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         bool on;
-        const uint4* p = q_piece(u, r0 + 8 * i + (t >> 4), on);
+        const uint4* p = q_piece(u, r0 + 16 * i + (t >> 4), on);
         x[i] = on ? *p : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 8 * i + (t >> 4);
+        const int row = r0 + 16 * i + (t >> 4);
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         uint32_t mx = 0;
 #pragma unroll
@@ -433,60 +473,49 @@ struct Producer {
     arrive(&bars[B_QFULL]);
   }
 
-  // The page of tile `i` that this warp's blocks are in: -1 if none counts.
+  // The page of this warp's block of tile `i`: -1 if the block does not count.
   __device__ int page_of(const Walk& u, int i) const {
-    const int pg = 2 * i + (wp >> 1);
-    if (i >= u.hist_end() || pg * PAGE >= u.r.H) return -1;
-    const int id = a.cv.page_table[(size_t)u.b * a.cv.max_pages_per_req + pg];
+    if (i >= u.hist_end() || (8 * i + wp) * KV8_BLK >= u.r.H) return -1;
+    const int id = a.cv.page_table[(size_t)u.b * a.cv.max_pages_per_req + 2 * i + (wp >> 2)];
     if (id >= 0 && id < a.cv.num_pages) return id;
-    if (lane == 0 && !(wp & 1)) record_error(a.cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+    if (lane == 0) record_error(a.cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
     return -1;
   }
 
   __device__ void history(const Walk& u) {
-    const int end = u.hist_end(), sub = 2 * wp % KV8_PAGE_BLOCKS;
-    Codes k[2], v[2];
+    const int end = u.hist_end(), sub = wp % KV8_PAGE_BLOCKS;
+    Codes k, v;
     float2 sc = make_float2(0.f, 0.f);
     int now = page_of(u, u.i0), next = page_of(u, u.i0 + 1);
-    int valid = 0;
-    auto on = [&](int i, int pid, int j) { return pid >= 0 && (8 * i + 2 * wp + j) * KV8_BLK < u.r.H; };
-    auto load_k = [&](int i, int pid) {
+    auto load_k = [&](int pid) {
       const uint8_t* base = kv8_head(a.cv, pid < 0 ? 0 : pid, u.h);
-      valid = (int)on(i, pid, 0) + 2 * (int)on(i, pid, 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_codes<0>(k[j], base + (sub + j) * KV8_BLOCK_BYTES, valid >> j & 1, lane);
-      if (lane < 2 && (valid >> lane & 1)) sc = __ldcg((const float2*)(base + KV8_OFF_SCALES) + sub + lane);
+      load_codes<0>(k, base + sub * KV8_BLOCK_BYTES, pid >= 0, lane);
+      if (pid >= 0) sc = __ldcg((const float2*)(base + KV8_OFF_SCALES) + sub);
     };
-    auto load_v = [&](int i, int pid) {
-      const uint8_t* base = kv8_head(a.cv, pid < 0 ? 0 : pid, u.h);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) load_codes<1>(v[j], base + (sub + j) * KV8_BLOCK_BYTES, on(i, pid, j), lane);
+    auto load_v = [&](int pid) {
+      load_codes<1>(v, kv8_head(a.cv, pid < 0 ? 0 : pid, u.h) + sub * KV8_BLOCK_BYTES, pid >= 0, lane);
     };
-    load_k(u.i0, now);
-    load_v(u.i0, now);
+    load_k(now);
+    load_v(now);
     load_q16(u);
+    const uint32_t base = saddr(smem + OFF_BUF);
+#pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
-      const int after = page_of(u, i + 2);
-      const uint32_t kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
+      const int after = page_of(u, i + 2), kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
       if (!wait_empty(2 * gt)) return;
-      {
-        const bool bad = lane < 2 && (valid >> lane & 1) && sc.y != sc.y;
-        const uint32_t nanv = __ballot_sync(0xffffffffu, bad);
-        float lsv = bad || !(lane < 2 && (valid >> lane & 1)) ? 0.f : log2f(sc.y);
-        info(make_float2(sc.x * C0, lsv), valid, (int)nanv);
-      }
-      const uint32_t kt = saddr(smem + OFF_BUF) + kb * BUF, vt = saddr(smem + OFF_BUF) + vb * BUF;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) store_k<TYPE>(kt, k[j], 2 * wp + j, lane);
+      const bool bad = now >= 0 && sc.y != sc.y;
+      info(u, make_float2(sc.x * C0, now < 0 || bad ? 0.f : log2f(sc.y)), now < 0 ? 0 : bad ? 3 : 1,
+           F_HIST | (u.two ? F_TWO : 0) | (i == u.i0 ? F_NEWQ : 0) | (i + 1 == end ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0));
+      store_k<TYPE>(base + kb * BUF, k, wp, lane);
       fence_proxy_async();
       arrive(&bars[B_FULL + kb]);
-      load_k(i + 1, next);
+      load_k(next);
       if (!wait_empty(2 * gt + 1)) return;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) store_v<TYPE>(vt, v[j], 2 * wp + j, lane);
+      store_v<TYPE>(base + vb * BUF, v, wp, lane);
       fence_proxy_async();
       arrive(&bars[B_FULL + vb]);
-      load_v(i + 1, next);
+      load_v(next);
+      now = next;
       next = after;
     }
   }
@@ -498,7 +527,7 @@ struct Producer {
     if (qn > 0 && !wait(B_QEMPTY, qn - 1)) return;
     const int rows = u.two ? ROWS : TILE;
 #pragma unroll 4
-    for (int row = t >> 4; row < rows; row += 8) {
+    for (int row = t >> 4; row < rows; row += 16) {
       bool on;
       const uint4* p = q_piece(u, row, on);
       copy16(q_place(row), p, on);
@@ -513,15 +542,17 @@ struct Producer {
       for (int side = 0; side < 2; ++side) {
         const int item = 2 * gt + side, buf = item % NBUF;
         if (!wait_empty(item)) return;
-        if (side == 0) info(make_float2(C0, 0.f), 3, 0);
+        if (side == 0)
+          info(u, make_float2(C0, 0.f), 1,
+               (u.two ? F_TWO : 0) | (i == u.line_begin() ? F_NEWQ : 0) | (i + 1 == u.i1 ? F_ENDQ | F_ENDU : 0));
         const __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
         const __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
         const __nv_bfloat16* fresh = (side ? a.v : a.k) + ((size_t)u.b * u.geo.T * cv.Hkv + u.h) * D;
         const int ch = t & 15;
         const uint32_t to = saddr(smem + OFF_BUF) + buf * BUF + (ch >> 3) * REGION;
 #pragma unroll 4
-        for (int j = 0; j < 16; ++j) {
-          const int tok = 8 * j + (t >> 4), s = s0 + tok;
+        for (int j = 0; j < 8; ++j) {
+          const int tok = 16 * j + (t >> 4), s = s0 + tok;
           const bool on = s < all;
           const __nv_bfloat16* p = s < nsink   ? sink + (size_t)s * D
                                    : s < u.r.w ? ring + (size_t)((u.r.H + s - nsink) & (RECENT - 1)) * D
@@ -538,7 +569,8 @@ struct Producer {
 
   __device__ void run() {
     Walk u(a, misc);
-    for (; u.more() && ok; u.next()) {
+    for (; u.more() && ok; u.next(), ++un) {
+      told = false;
       if (u.i0 < u.hist_end()) history(u);
       if (ok && u.line_begin() < u.i1) line(u);
     }
@@ -546,88 +578,119 @@ struct Producer {
   }
 };
 
+
 // -------------------------------------------------------------------- MMA issue
-struct Steps {
-  Walk u;
-  int tile, half, g, gt;
-  __device__ Steps(const Kv8Prefill& a, const Misc* m) : u(a, m), tile(u.more() ? u.i0 : 0), half(0), g(0), gt(0) {}
-  __device__ bool more() const { return u.more(); }
-  __device__ bool hist() const { return tile < u.r.nh; }
-  __device__ void advance() {
-    ++g;
-    if (u.two && !half) {
-      half = 1;
-      return;
-    }
-    half = 0;
-    ++gt;
-    if (++tile == u.i1) {
-      u.next();
-      if (u.more()) tile = u.i0;
-    }
-  }
-};
+// A whole warp, one lane elected for the instructions: with every value the same in
+// all lanes (`same` tells the compiler so) an MMA takes the 64 cycles of its
+// arithmetic, issued from a divergent branch 150.  It learns what a tile is from
+// the producers' flags: anything slower than the MMAs would hold them up.
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint64_t hi) { return hi | lo; }
+__device__ __forceinline__ uint32_t same(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// Loops: the warp comes by once a step, and unrolled it would wait for its
+// instructions, which the other warps' code has pushed out of the cache.
+__device__ __forceinline__ void scores_mma(uint32_t d, uint32_t q, uint32_t k, uint64_t hi, uint32_t id) {
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half, q += REGION >> 4, k += REGION >> 4)
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) mma_ss(d, desc(q + 2 * ks, hi), desc(k + 2 * ks, hi), id, half | ks);
+}
+__device__ __forceinline__ void values_mma(uint32_t d, uint32_t p, uint32_t v, uint64_t hi, uint32_t id, uint32_t add) {
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half, p += 32, v += 4 * (2048 >> 4))
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) mma_ts(d, p + 8 * kk, desc(v + kk * (2048 >> 4), hi), id, add | half | kk);
+}
 
 __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
   uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
   Misc* misc = (Misc*)(smem + OFF_MISC);
-  const uint32_t tmem = misc->tmem, qbase = saddr(smem + OFF_Q), bbase = saddr(smem + OFF_BUF);
-  Steps s(a, misc), p(a, misc);
-  bool new_q = true, started[2] = {false, false};
-  int qn = 0, np[2] = {0, 0};
-  auto wait = [&](int bar, int phase) { return wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls); };
+  const Info* infos = (const Info*)(smem + OFF_INFO);
+  const uint32_t tmem = same(misc->tmem), qlo = saddr(smem + OFF_Q) >> 4, blo = saddr(smem + OFF_BUF) >> 4;
+  const uint64_t hi = sdesc(0), hi_mn = sdesc_mn(0, REGION);
+  const int total = (int)same((uint32_t)(misc->hi - misc->lo));
+  // of S and of O: tiles done, second row tile's turn, step, ring place and its phase
+  struct {
+    int tile, half, step, buf, phase;
+    uint32_t flags;
+  } s = {0, 0, 0, 0, 0, 0}, p = {0, 0, 0, 1, 0, 0};
+  uint32_t started = 0, pphase = 0, qphase = 0;
+  auto wait = [&](int bar, uint32_t phase) {
+    return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
+  };
   auto scores = [&]() -> bool {
-    const bool hist = s.hist();
-    if (new_q && !wait(B_QFULL, qn++)) return false;
-    const int item = 2 * s.gt, buf = item % NBUF, w = s.g & 1;
-    if (!s.half && !wait(B_FULL + buf, item / NBUF)) return false;
-    fence_after();
-    const uint32_t q = qbase + (s.u.two ? w : 0) * BUF, k = bbase + buf * BUF, id = idesc(hist ? 0 : 1, 0);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t off = (ks >> 2) * REGION + (ks & 3) * 32;
-      mma_ss(tmem + S_COL + TILE * w, sdesc(q + off), sdesc(k + off), id, ks > 0);
+    if (!s.half) {
+      if (!wait(B_FULL + s.buf, s.phase)) return false;
+      s.flags = same(infos[s.tile & (NINFO - 1)].flags);
+      if (s.flags & F_NEWQ) {
+        if (!wait(B_QFULL, qphase)) return false;
+        qphase ^= 1;
+      }
     }
-    commit(&bars[B_S + w]);
-    const long long at = s.u.at;
-    const int gt = s.gt;
-    s.advance();
-    if (s.gt != gt) commit(&bars[B_EMPTY + buf]);
-    new_q = !s.more() || s.u.at != at || s.hist() != hist;
-    if (new_q) commit(&bars[B_QEMPTY]);
+    fence_after();
+    const uint32_t w = s.step & 1, q = qlo + (s.flags & F_TWO ? w * (BUF >> 4) : 0), k = blo + s.buf * (BUF >> 4);
+    const uint32_t d = tmem + S_COL + TILE * w;
+    const bool last = !(s.flags & F_TWO) || s.half;  // of the tile's steps
+    if (elect()) {
+      scores_mma(d, q, k, hi, s.flags & F_HIST ? idesc(0, 0) : idesc(1, 0));
+      commit(&bars[B_S + w]);
+      if (last) commit(&bars[B_EMPTY + s.buf]);
+      if (last && (s.flags & F_ENDQ)) commit(&bars[B_QEMPTY]);
+    }
+    __syncwarp();
+    ++s.step;
+    s.half = !last;
+    if (last) {
+      ++s.tile;
+      s.buf += 2;
+      if (s.buf >= NBUF) s.buf -= NBUF, s.phase ^= 1;
+    }
     return true;
   };
   auto values = [&]() -> bool {
-    const int w = p.g & 1, item = 2 * p.gt + 1, buf = item % NBUF;
-    if (!wait(B_P + w, np[w]++)) return false;
-    if (!p.half && !wait(B_FULL + buf, item / NBUF)) return false;
+    const uint32_t w = p.step & 1;
+    if (!wait(B_P + w, pphase >> w)) return false;
+    pphase ^= 1u << w;
+    if (!p.half) {
+      if (!wait(B_FULL + p.buf, p.phase)) return false;
+      p.flags = same(infos[p.tile & (NINFO - 1)].flags);
+    }
     fence_after();
-    const uint32_t v = bbase + buf * BUF, id = idesc(p.hist() ? 0 : 1, 1);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-      mma_ts(tmem + O_COL + TILE * w, tmem + S_COL + TILE * w + 8 * kk, sdesc_mn(v + kk * 2048, REGION), id, started[w] || kk > 0);
-    started[w] = true;
-    const long long at = p.u.at;
-    const int gt = p.gt;
-    p.advance();
-    if (p.gt != gt) commit(&bars[B_EMPTY + buf]);
-    if (!p.more() || p.u.at != at) {
-      for (int i = 0; i < 2; ++i) {
-        if (started[i]) commit(&bars[B_O + i]);
-        started[i] = false;
-      }
+    const uint32_t v = blo + p.buf * (BUF >> 4), d = tmem + O_COL + TILE * w, add = started >> w & 1;
+    const bool last = !(p.flags & F_TWO) || p.half, end = last && (p.flags & F_ENDU);
+    started |= 1u << w;
+    if (elect()) {
+      values_mma(d, tmem + S_COL + TILE * w, v, hi_mn, p.flags & F_HIST ? idesc(0, 1) : idesc(1, 1), add);
+      if (last) commit(&bars[B_EMPTY + p.buf]);
+      if (end && (started & 1)) commit(&bars[B_O]);
+      if (end && (started & 2)) commit(&bars[B_O + 1]);
+    }
+    __syncwarp();
+    if (end) started = 0;
+    ++p.step;
+    p.half = !last;
+    if (last) {
+      ++p.tile;
+      p.buf += 2;
+      if (p.buf >= NBUF) p.buf -= NBUF, p.phase ^= 1;
     }
     return true;
   };
   bool ok = true;
   for (int i = 0; i < 2; ++i)
-    if (ok && s.more()) ok = scores();
-  while (ok && p.more()) {
+    if (ok && s.tile < total) ok = scores();
+  while (ok && p.tile < total) {
     ok = values();
-    if (ok && s.more()) ok = scores();
+    if (ok && s.tile < total) ok = scores();
   }
   // all that was issued has ended before the tensor memory is given back
-  commit(&bars[B_DRAIN]);
+  if (elect()) commit(&bars[B_DRAIN]);
+  __syncwarp();
   mbar_wait(&bars[B_DRAIN], 0);
 }
 
@@ -651,43 +714,145 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16]) 
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {  // and waits
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+               "tcgen05.wait::ld.sync.aligned;\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(at)
+               : "memory");
+}
+
 // A row's running state.
 struct Row {
   float m, l, M;
 };
 
-// Tokens of a tile that a row takes: `seen` first ones, and of those the blocks in `valid`.
-// P of the tile to tensor memory, sums into the state.  EVERY: all of them.
-template <bool F16, bool EVERY>
-__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, int seen, uint32_t valid,
-                                      uint32_t nanv, bool first) {
-  float cb[8], mb[8];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two fp32 values in one register pair: one instruction works on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A tile for one row, in 32-column pieces of S, which are read twice: for the maximum
+// and for the exponentials (all 128 would not fit into the registers, and a spilled
+// one goes to the L2 here: shared memory has taken the L1).
+// Tokens that the row takes: `seen` first ones, and of those the blocks whose mark says so.
+// EVERY: all of them.
+template <bool EVERY>
+__device__ __forceinline__ void hide(uint32_t (&r)[32], int c, const Info* f, int seen) {
+  if (!EVERY) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tmem_ld32(sa + 32 * c, r);
-    tmem_ld_wait_regs(r);
+    for (int j = 0; j < 32; ++j)
+      if (!(f->marks[2 * c + (j >> 4)] & 1) || 32 * c + j >= seen) r[j] = 0xff800000u;  // -infinity
+  }
+}
+// The scales of a tile's blocks in registers, read before S is awaited (from shared
+// memory, which the MMAs and the producers keep busy, each takes some 240 cycles):
+// four blocks at hand, four to come.
+struct Scales {
+  float4 at[2], to[2];  // (factor of the logits, log2 s_V) of two blocks
+  __device__ __forceinline__ void load(const Info* f, float al) {
+    const float4* x = (const float4*)f->cs;
+    at[0] = x[0], at[1] = x[1], to[0] = x[2], to[1] = x[3];
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-      const int b = 2 * c + hb;
-      float m0 = -INFINITY, m1 = -INFINITY;
+    for (int i = 0; i < 2; ++i) at[i].x *= al, at[i].z *= al, to[i].x *= al, to[i].z *= al;
+  }
+  __device__ __forceinline__ void turn() {
 #pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const float x = __uint_as_float(r[16 * hb + j]), y = __uint_as_float(r[16 * hb + j + 1]);
-        m0 = fmaxf(m0, EVERY || 16 * b + j < seen ? x : -INFINITY);
-        m1 = fmaxf(m1, EVERY || 16 * b + j + 1 < seen ? y : -INFINITY);
-      }
-      mb[b] = EVERY || (valid >> b & 1) ? fmaxf(m0, m1) : -INFINITY;
+    for (int i = 0; i < 2; ++i) {
+      const float4 x = at[i];
+      at[i] = to[i];
+      to[i] = x;
     }
   }
-  float mx = NONE, tx = NONE;
+};
+// Largest logit so far, and the same with the value scale.
+__device__ __forceinline__ void largest(const uint32_t (&r)[32], const float4& cs, float& mx, float& tx) {
+  float y[2];
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    const float2 cs = f->cs[b];
-    cb[b] = cs.x * al;
-    const float x = mb[b] * cb[b];
-    mx = fmaxf(mx, x);
-    tx = fmaxf(tx, x + cs.y);
+  for (int hb = 0; hb < 2; ++hb) {
+    auto x = [&](int j) { return __uint_as_float(r[16 * hb + j]); };
+    float m0 = fmaxf(x(0), x(1)), m1 = fmaxf(x(2), x(3));
+#pragma unroll
+    for (int j = 4; j < 16; j += 4) {
+      m0 = max3(m0, x(j), x(j + 1));
+      m1 = max3(m1, x(j + 2), x(j + 3));
+    }
+    y[hb] = fmaxf(m0, m1);
+  }
+  y[0] *= cs.x;
+  y[1] *= cs.z;
+  mx = max3(mx, y[0], y[1]);
+  tx = max3(tx, y[0] + cs.y, y[1] + cs.w);
+}
+template <bool F16, bool EVERY>
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[32], int c, Row& st, uint32_t sa, const Info* f, const float4& cs, int seen) {
+  uint32_t o[16];
+#pragma unroll
+  for (int hb = 0; hb < 2; ++hb) {
+    const int b = 2 * c + hb, mark = EVERY ? 1 : f->marks[b];
+    const float shift = max_nan((hb ? cs.w : cs.y) - st.M, -st.m - FAR), cb = hb ? cs.z : cs.x;
+    const uint64_t cb2 = pair(cb, cb), shift2 = pair(shift, shift);
+    uint64_t sum = 0;  // two zeros
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      float y, z;
+      unpair(fma2(pair(__uint_as_float(r[16 * hb + j]), __uint_as_float(r[16 * hb + j + 1])), cb2, shift2), y, z);
+      y = ex2(y);
+      z = ex2(z);
+      if (!EVERY) {
+        if (!(mark & 1) || 16 * b + j >= seen) y = 0.f;
+        if (!(mark & 1) || 16 * b + j + 1 >= seen) z = 0.f;
+      }
+      sum = add2(sum, pair(y, z));
+      if (!EVERY && (mark & 2)) y = z = NAN;
+      o[8 * hb + j / 2] = pack2<F16>(y, z);
+    }
+    float s0, s1;
+    unpair(sum, s0, s1);
+    st.l = fmaf(s0 + s1, ex2(-shift - st.m), st.l);
+  }
+  tmem_st16(sa + 16 * c, o);
+}
+
+// P of the tile to tensor memory, sums into the state.
+template <bool F16, bool EVERY>
+__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, Scales& sc, int seen, bool first) {
+  uint32_t r0[32], r1[32];
+  float mx = NONE, tx = NONE;
+  tmem_ld32(sa, r0);
+  tmem_ld_wait_regs(r0);
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    tmem_ld32(sa + 32 * (c + 1), r1);
+    hide<EVERY>(r0, c, f, seen);
+    largest(r0, sc.at[0], mx, tx);
+    tmem_ld_wait_regs(r1);
+    tmem_ld32(sa + 32 * (c ^ 2), r0);  // the third piece, then the first again
+    hide<EVERY>(r1, c + 1, f, seen);
+    largest(r1, sc.at[1], mx, tx);
+    sc.turn();
+    tmem_ld_wait_regs(r0);
   }
   const float mn = fmaxf(st.m, mx);
   st.l *= ex2(st.m - mn);
@@ -699,41 +864,23 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
     st.M = Mn;
     // S of this step is complete, so is every MMA issued before it: O has all steps before
 #pragma unroll 1
-    for (int c = 0; c < TILE; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(oa + c, v);
-      tmem_ld_wait_regs(v);
+    for (int c = 0; c < TILE; c += 16) {
+      uint32_t v[16];
+      tmem_ld16(oa + c, v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * g);
-      tmem_st32(oa + c, v);
+      for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * g);
+      tmem_st16(oa + c, v);
     }
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32], o[16];
-    tmem_ld32(sa + 32 * c, r);
-    tmem_ld_wait_regs(r);
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-      const int b = 2 * c + hb;
-      const float shift = max_nan(f->cs[b].y - st.M, -st.m - FAR);
-      float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        float x = ex2(fmaf(__uint_as_float(r[16 * hb + j]), cb[b], shift));
-        float y = ex2(fmaf(__uint_as_float(r[16 * hb + j + 1]), cb[b], shift));
-        if (!EVERY) {
-          if (!(valid >> b & 1) || 16 * b + j >= seen) x = 0.f;
-          if (!(valid >> b & 1) || 16 * b + j + 1 >= seen) y = 0.f;
-        }
-        sum0 += x;
-        sum1 += y;
-        if (!EVERY && (nanv >> b & 1)) x = y = NAN;
-        o[8 * hb + j / 2] = pack2<F16>(x, y);
-      }
-      st.l = fmaf(sum0 + sum1, ex2(-shift - st.m), st.l);
-    }
-    tmem_st16(sa + 16 * c, o);
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    tmem_ld32(sa + 32 * (c + 1), r1);
+    exponentials<F16, EVERY>(r0, c, st, sa, f, sc.at[0], seen);
+    tmem_ld_wait_regs(r1);
+    if (c == 0) tmem_ld32(sa + 64, r0);
+    exponentials<F16, EVERY>(r1, c + 1, st, sa, f, sc.at[1], seen);
+    sc.turn();
+    tmem_ld_wait_regs(r0);
   }
   tmem_st_wait();
 }
@@ -750,43 +897,44 @@ __device__ __noinline__ void add_bad(const Kv8Prefill& a, int b, int h, int j0, 
   }
 }
 
-// The rows of a unit, or (part) their record.  oa: this group's O; other: the
-// second group's, to be joined (its factor g1), or 0.
-__device__ __forceinline__ void write_row(const Kv8Prefill& a, const Walk& u, const Row& st, uint32_t oa, float g0, uint32_t other,
-                                          float g1, int row, float* rec, bool bad_v, bool ok) {
-  const int G = a.cv.G, tok = u.t0 + row / G;
-  const bool on = tok < u.t1;
-  const size_t at = ((size_t)u.b * u.geo.T + (on ? tok : u.t0)) * a.cv.Hq + u.h * G + row % G;
-  const float lg = log2f(st.l);
-  float f = rec ? 1.f : st.l == 0.f ? 0.f : ex2(st.M - st.m - lg);
-  if (!ok) f = NAN;
-  int j0 = 0, j1 = 0;
-  if (bad_v) {
-    const int s0 = (u.line_begin() - u.r.nh) * TILE - u.r.w, s1 = (u.i1 - u.r.nh) * TILE - u.r.w;
-    j0 = max(u.t0 + 1, s0);
-    j1 = min(tok + 1, s1);
-  }
+__device__ float* record(const Kv8Prefill& a, int cta, int slot, int row) {
+  return a.part + ((size_t)(2 * cta + slot) * ROWS + row) * PART_STRIDE;
+}
+
+// A row of a unit (lg: its log2 of the sum of exponentials), or its record where the
+// unit is not whole here.  O = g0·[oa] + g1·[ob].
+__device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, int row, float lg, float M, uint32_t oa, float g0,
+                                          uint32_t ob, float g1, bool bad_v) {
+  const int G = a.cv.G, tok = u->t0 + row / G;
+  const bool on = tok < u->t1, whole = (u->flags & (U_BEGINS | U_ENDS)) == (U_BEGINS | U_ENDS);
+  const size_t at = ((size_t)u->b * a.T + (on ? tok : u->t0)) * a.cv.Hq + u->h * G + row % G;
+  float* rec = record(a, blockIdx.x, u->flags & U_BEGINS ? 1 : 0, row);
+  const float f = !whole ? 1.f : lg == -INFINITY ? 0.f : ex2(M - lg);  // nothing seen: zeros, and -infinity as the lse
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
-    {
-      uint32_t v[32];
-      if (g0 != 0.f) {
-        tmem_ld32(oa + c, v);
-        tmem_ld_wait_regs(v);
-      }
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = g0 != 0.f ? __uint_as_float(v[j]) * g0 : 0.f;
+    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+    uint32_t v[32];
+    if (g0 != 0.f) {
+      tmem_ld32(oa + c, v);
+      tmem_ld_wait_regs(v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[j]) * g0;
     }
-    if (other) {
-      uint32_t v[32];
-      tmem_ld32(other + c, v);
+    if (ob) {
+      tmem_ld32(ob + c, v);
       tmem_ld_wait_regs(v);
 #pragma unroll
       for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(v[j]), g1, o[j]);
     }
-    if (bad_v && on) add_bad(a, u.b, u.h, j0, j1, c, o);
-    if (on && rec) {
+    if (bad_v && on) {
+      float x[32];
+      for (int j = 0; j < 32; ++j) x[j] = o[j];
+      add_bad(a, u->b, u->h, max(u->t0 + 1, u->c0), min(tok + 1, u->c1), c, x);
+      for (int j = 0; j < 32; ++j) o[j] = x[j];
+    }
+    if (on && !whole) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
         *(float4*)(rec + PART_O + c + j) = make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
@@ -803,61 +951,92 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Walk& u, co
     }
     __syncwarp();
   }
-  if (on && rec) {
-    rec[0] = st.m;
-    rec[1] = ok ? st.l : NAN;
-    rec[2] = st.M;
+  if (on && !whole) {
+    rec[0] = lg;
+    rec[1] = M;
   } else if (on && a.lse) {
-    a.lse[at] = ok ? (st.l == 0.f ? -INFINITY : (st.m + lg) * LN2) : NAN;
+    a.lse[at] = lg * LN2;
   }
   __syncwarp();
 }
 
-__device__ float* record(const Kv8Prefill& a, int cta, int slot, int row) {
-  return a.part + ((size_t)(2 * cta + slot) * ROWS + row) * PART_STRIDE;
+// After a wait that ran out: NaN in the group's rows of unit `un` of the part and those behind it.
+__device__ __noinline__ void abandon(const Kv8Prefill& a, const Misc* m, int un, int wg, int row) {
+  const int G = a.cv.G;
+  int i = 0;
+  for (Walk u(a, m); u.more(); u.next(), ++i) {
+    const int urow = (u.two ? TILE * wg : 0) + row, tok = u.t0 + urow / G;
+    if (i < un || (!u.two && wg == 1) || tok >= u.t1) continue;
+    if (u.i0 > 0 || u.i1 < u.n) {
+      record(a, blockIdx.x, u.i0 == 0 ? 1 : 0, urow)[0] = NAN;
+      continue;
+    }
+    const size_t at = ((size_t)u.b * a.T + tok) * a.cv.Hq + u.h * G + urow % G;
+    for (int c = 0; c < D; ++c) a.out[at * D + c] = __float2bfloat16_rn(NAN);
+    if (a.lse) a.lse[at] = NAN;
+  }
+}
+
+// log2 of 2^a + 2^b.
+__device__ __forceinline__ float add_logs(float a, float b) {
+  const float m = fmaxf(a, b);
+  return m == -INFINITY ? (a == b ? m : NAN) : m + log2f(ex2(a - m) + ex2(b - m));
 }
 
 __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
   uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
   Misc* misc = (Misc*)(smem + OFF_MISC);
-  const int warp = tid >> 5, wg = warp >> 2, row = tid & 127;
-  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, tmem = misc->tmem + lanes;
+  const int warp = tid >> 5, wg = warp >> 2, row = tid & 127, G = a.cv.G;
+  const uint32_t tmem = misc->tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t sa = tmem + S_COL + TILE * wg, oa = tmem + O_COL + TILE * wg;
-  float* xch = (float*)(smem + OFF_XCH) + row * 3;
+  const int total = (int)(misc->hi - misc->lo);
   auto wait = [&](int bar, int phase) {
     return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
   };
   bool ok = true;
-  int g = 0, gt = 0, ns = 0, no = 0, qn = 0;
-  Split split = {0, 0, 0, -1};
-  Walk u(a, misc);
-  for (; u.more(); u.next()) {
-    const int nt = u.i1 - u.i0, hist_end = u.hist_end();
-    const int urow = (u.two ? TILE * wg : 0) + row, trow = u.t0 + urow / a.cv.G;
+  // token tiles and steps done; this group's S and O so far; exchanges; units, loads of Q
+  int gt = 0, g = 0, ns = 0, no = 0, nx = 0, un = 0, qn = 0;
+  while (gt < total) {
+    if (ok) ok = wait(B_INFO + (gt & (NINFO - 1)), gt / NINFO);
+    if (!ok) break;
+    const Unit* u = (const Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
+    const int tiles = u->tiles, hist = u->hist, two = u->flags & U_TWO;
+    const int urow = (two ? TILE * wg : 0) + row, line = u->line + urow / G;
     Row st = {NONE, 0.f, NONE};
     float al = 0.f;
     int cnt = 0;
-    for (int i = u.i0 + (u.two ? 0 : (wg - g) & 1); i < u.i1 && ok; i += u.two ? 1 : 2) {
-      const int tile = gt + i - u.i0;
-      ok = wait(B_INFO + (tile & (NINFO - 1)), tile / NINFO) && wait(B_S + wg, ns);
+    for (int i = two ? 0 : (wg - g) & 1; i < tiles; i += two ? 1 : 2) {
+      const int tile = gt + i;
+      ok = wait(B_INFO + (tile & (NINFO - 1)), tile / NINFO);
+      if (!ok) break;
+      const Info* f = (const Info*)(smem + OFF_INFO) + (tile & (NINFO - 1));
+      Scales sc;
+      bool every;
+      int seen = TILE;
+      if (i < hist) {
+        // the row's exponent is there when Q is, which the first S tells
+        if (cnt > 0) sc.load(f, al);
+        const uint32_t* marks = (const uint32_t*)f->marks;
+        every = marks[0] == ALL_COUNT && marks[1] == ALL_COUNT;
+      } else {
+        sc.load(f, 1.f);
+        seen = line - (i - hist) * TILE;
+        every = __all_sync(0xffffffffu, seen >= TILE);
+      }
+      ok = wait(B_S + wg, ns);
       if (!ok) break;
       ++ns;
       fence_after();
-      const Info* f = (const Info*)(smem + OFF_INFO) + (tile & (NINFO - 1));
-      if (i < u.r.nh) {
-        if (cnt == 0) al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
-        uint32_t valid = 0, nanv = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          valid |= (uint32_t)f->valid[j] << (2 * j);
-          nanv |= (uint32_t)f->nanv[j] << (2 * j);
-        }
-        if (valid == 0xff && nanv == 0) weigh<true, true>(st, sa, oa, f, al, TILE, valid, nanv, cnt == 0);
-        else weigh<true, false>(st, sa, oa, f, al, TILE, valid, nanv, cnt == 0);
+      if (i < hist && cnt == 0) {
+        al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
+        sc.load(f, al);
+      }
+      if (i < hist) {
+        if (every) weigh<true, true>(st, sa, oa, f, sc, TILE, cnt == 0);
+        else weigh<true, false>(st, sa, oa, f, sc, TILE, cnt == 0);
       } else {
-        const int seen = u.r.w + trow + 1 - (i - u.r.nh) * TILE;
-        if (__all_sync(0xffffffffu, seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, TILE, 0xff, 0, cnt == 0);
-        else weigh<false, false>(st, sa, oa, f, 1.f, seen, 0xff, 0, cnt == 0);
+        if (every) weigh<false, true>(st, sa, oa, f, sc, TILE, cnt == 0);
+        else weigh<false, false>(st, sa, oa, f, sc, seen, cnt == 0);
       }
       fence_before();
       __syncwarp();
@@ -869,43 +1048,41 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
       ++no;
       fence_after();
     }
-    const bool begins = u.i0 == 0, ends = u.i1 == u.n;
-    if (begins && !ends) {
-      Balanced bl;
-      bl.W = misc->W;
-      bl.n = misc->n;
-      split = {u.b, u.h, u.rt, balanced_owner(bl, u.at + u.n - 1)};
-    }
-    float* rec = begins && ends ? nullptr : record(a, blockIdx.x, begins ? 1 : 0, urow);
-    const bool bad_v = *(volatile int*)&misc->bad_v != 0 && u.line_begin() < u.i1;
-    if (u.two) {
-      write_row(a, u, st, oa, 1.f, 0, 0.f, urow, rec, bad_v, ok);
+    const bool bad_v = *(volatile int*)&misc->bad_v != 0 && tiles > hist;
+    float lg = st.l == 0.f ? -INFINITY : st.m + log2f(st.l);
+    if (!ok) break;
+    if (two) {
+      write_row(a, u, urow, lg, st.M, oa, 1.f, 0, 0.f, bad_v);
     } else {
+      float2* other = (float2*)(smem + OFF_XCH) + row;
       if (wg == 1) {
-        xch[0] = st.m;
-        xch[1] = ok ? st.l : NAN;
-        xch[2] = cnt > 0 ? st.M : -INFINITY;
-      }
-      fence_before();
-      asm volatile("bar.sync 3, 256;\n" ::: "memory");
-      fence_after();
-      if (wg == 0) {
-        const float m1 = xch[0], l1 = xch[1], M1 = xch[2];
-        const bool one = M1 != -INFINITY;  // the other group had a tile
-        Row j;
-        j.m = fmaxf(st.m, m1);
-        j.l = st.l * ex2(st.m - j.m) + l1 * ex2(m1 - j.m);
-        j.M = cnt > 0 ? fmaxf(st.M, M1) : M1;
-        write_row(a, u, j, oa, cnt > 0 ? ex2(st.M - j.M) : 0.f, one ? oa + TILE : 0, one ? ex2(M1 - j.M) : 0.f, urow, rec, bad_v, ok);
+        *other = make_float2(lg, cnt > 0 ? st.M : -INFINITY);
         fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) arrive(&bars[B_OTHER]);
+        ok = wait(B_TAKEN, nx);
+        if (!ok) break;
+      } else {
+        ok = wait(B_OTHER, nx);
+        if (!ok) break;
+        fence_after();
+        const float2 x = *other;
+        const bool one = x.y != -INFINITY;  // the other group had a tile
+        const float M = cnt > 0 ? fmaxf(st.M, x.y) : x.y;
+        write_row(a, u, urow, add_logs(lg, x.x), M, oa, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
+                  one ? ex2(x.y - M) : 0.f, bad_v);
+        fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) arrive(&bars[B_TAKEN]);
       }
-      asm volatile("bar.sync 3, 256;\n" ::: "memory");
+      ++nx;
     }
-    gt += nt;
-    g += u.two ? 2 * nt : nt;
-    qn += (int)(u.i0 < hist_end) + (int)(u.line_begin() < u.i1);
+    gt += tiles;
+    g += two ? 2 * tiles : tiles;
+    qn += (int)(hist > 0) + (int)(tiles > hist);
+    ++un;
   }
-  if (tid == 0) a.splits[blockIdx.x] = make_int4(split.b, split.h, split.rt, split.last);
+  if (!ok) abandon(a, misc, un, wg, row);
 }
 
 template <int TYPE>
@@ -913,7 +1090,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
   Misc* misc = (Misc*)(smem + OFF_MISC);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = (int)same(tid >> 5);
   if (saddr(smem) & 1023) {  // the swizzled tiles begin on 1024 bytes; there is no room to move them
     if (tid == 0) {
       a.splits[blockIdx.x] = make_int4(0, 0, 0, -1);
@@ -923,17 +1100,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(&bars[B_FULL + i], 128);
+      mbar_init(&bars[B_FULL + i], PROD);
       mbar_init(&bars[B_EMPTY + i], 1);
     }
-    for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], 4);
+    for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], PROD_WARPS);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_S + i], 1);
       mbar_init(&bars[B_P + i], 4);
       mbar_init(&bars[B_O + i], 1);
     }
-    mbar_init(&bars[B_QFULL], 128);
+    mbar_init(&bars[B_QFULL], PROD);
     mbar_init(&bars[B_QEMPTY], 1);
+    mbar_init(&bars[B_OTHER], 4);
+    mbar_init(&bars[B_TAKEN], 4);
     mbar_init(&bars[B_DRAIN], 1);
     misc->abort = misc->bad_v = 0;
   }
@@ -950,12 +1129,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   __syncthreads();
   fence_after();
   const uint32_t tmem = misc->tmem;
-  if (warp == MMA_WARP) {
-    if (tid % 32 == 0) issue(a, smem);
-    __syncwarp();
+  if (warp >= MMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_MMA));
+    if (warp == MMA_WARP) issue(a, smem);
   } else if (tid >= PROD0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_PROD));
     Producer<TYPE>(a, smem, tid).run();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_SOFTMAX));
     softmax(a, smem, tid);
   }
   fence_before();
@@ -978,20 +1159,24 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8Pr
   const int tok = d.z * (ROWS / G) + row / G;
   if (tok >= a.T) return;
   const int first = blockIdx.x, n = d.w - first + 1;
-  float m = NONE, L = 0.f;
-  for (int k = lane; k < n; k += 32) m = fmaxf(m, record(a, first + k, k == 0, row)[0]);
-  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  float m = -INFINITY, L = 0.f;
+  bool nan = false;
   for (int k = lane; k < n; k += 32) {
-    const float* r = record(a, first + k, k == 0, row);
-    L += r[1] * ex2(r[0] - m);
+    const float x = record(a, first + k, k == 0, row)[0];
+    m = fmaxf(m, x);
+    nan |= x != x;
   }
+  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  nan = __any_sync(0xffffffffu, nan);
+  const bool none = m == -INFINITY && !nan;  // nothing seen
+  for (int k = lane; k < n; k += 32) L += ex2(record(a, first + k, k == 0, row)[0] - m);
   for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-  const float lg = log2f(L);
+  const float lg = nan ? NAN : none ? -INFINITY : m + log2f(L);
   float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int k = 0; k < n; ++k) {
     const float* r = record(a, first + k, k == 0, row);
-    const float f = L == 0.f ? 0.f : ex2(r[2] - m - lg);
+    const float f = none ? 0.f : ex2(r[1] - lg);
     const float4 x = *(const float4*)(r + PART_O + 4 * lane);
     o[0] = fmaf(x.x, f, o[0]);
     o[1] = fmaf(x.y, f, o[1]);
@@ -1000,7 +1185,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8Pr
   }
   const size_t at = ((size_t)d.x * a.T + tok) * a.cv.Hq + d.y * G + row % G;
   *(uint2*)(a.out + at * D + 4 * lane) = make_uint2(pack2<false>(o[0], o[1]), pack2<false>(o[2], o[3]));
-  if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (m + lg) * LN2;
+  if (lane == 0 && a.lse) a.lse[at] = lg * LN2;
 }
 
 template <int TYPE>
