@@ -51,7 +51,7 @@ constexpr int NBUF = 5, REGION = 16384, BUF = 2 * REGION;  // a tile: two region
 constexpr int NINFO = 4, NALPHA = 3, NUNIT = 8;
 constexpr int OFF_Q = 0, OFF_BUF = 2 * BUF, OFF_BAR = OFF_BUF + NBUF * BUF;
 enum {
-  B_FULL = 0, B_EMPTY = B_FULL + NBUF, B_INFO = B_EMPTY + NBUF, B_S = B_INFO + NINFO, B_P = B_S + 2, B_O = B_P + 2,
+  B_FULL = 0, B_EMPTY = B_FULL + NBUF, B_INFO = B_EMPTY + NBUF, B_S = B_INFO + NINFO, B_P = B_S + 2, B_O = B_P + 4,
   B_QFULL = B_O + 2, B_QEMPTY, B_OTHER, B_TAKEN, B_DRAIN, NBARS
 };
 // A token tile's scales: x = S·a·(2^exponent of the row), b = log2 s_V.
@@ -74,7 +74,7 @@ struct alignas(16) Unit {
   int pad[2];
 };
 enum { U_TWO = 1, U_BEGINS = 2, U_ENDS = 4 };
-constexpr int OFF_INFO = OFF_BAR + 208, OFF_UNIT = OFF_INFO + NINFO * (int)sizeof(Info), OFF_ALPHA = OFF_UNIT + NUNIT * (int)sizeof(Unit);
+constexpr int OFF_INFO = OFF_BAR + 240, OFF_UNIT = OFF_INFO + NINFO * (int)sizeof(Info), OFF_ALPHA = OFF_UNIT + NUNIT * (int)sizeof(Unit);
 constexpr int OFF_XCH = OFF_ALPHA + NALPHA * ROWS, OFF_MISC = OFF_XCH + TILE * 8;
 struct Misc {
   uint32_t tmem;
@@ -83,7 +83,7 @@ struct Misc {
   int b, h, rt, pad;
 };
 constexpr int SMEM = OFF_MISC + (int)sizeof(Misc);
-static_assert(NBARS * 8 <= 208 && sizeof(Info) == 80 && sizeof(Unit) == 48 && OFF_UNIT % 16 == 0 && OFF_XCH % 8 == 0 && OFF_MISC % 8 == 0, "layout");
+static_assert(NBARS * 8 <= 240 && sizeof(Info) == 80 && sizeof(Unit) == 48 && OFF_UNIT % 16 == 0 && OFF_XCH % 8 == 0 && OFF_MISC % 8 == 0, "layout");
 static_assert(SMEM <= 227 * 1024, "shared memory");
 constexpr int S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float C0 = INV_SQRT_D * LOG2E;
@@ -322,6 +322,16 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {  // of either half
   return (uint32_t)((w & 0x7f80u) == 0x7f80u) | (uint32_t)((w & 0x7f800000u) == 0x7f800000u);
 }
 
+// Whether a phase is over.
+__device__ __forceinline__ bool passed(uint64_t* bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(r)
+               : "r"(saddr(bar)), "r"(parity)
+               : "memory");
+  return r != 0;
+}
+
 template <int TYPE>
 struct Producer {
   const Kv8Prefill& a;
@@ -346,7 +356,14 @@ struct Producer {
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
     return ok;
   }
-  __device__ bool wait_empty(int item) { return item < NBUF ? ok : wait(B_EMPTY + item % NBUF, item / NBUF - 1); }
+  // The MMAs that free a buffer may need copies that nobody has been told of: it does not
+  // wait with any.
+  __device__ bool wait_empty(int item) {
+    if (item < NBUF) return ok;
+    const int bar = B_EMPTY + item % NBUF, phase = item / NBUF - 1;
+    if (npend > 0 && !__all_sync(0xffffffffu, passed(&bars[bar], phase & 1))) flush();
+    return wait(bar, phase);
+  }
 
   __device__ void tell(const Pending& p) {
     if (p.from < p.to) {  // this thread's own pieces
@@ -473,35 +490,36 @@ struct Producer {
     arrive(&bars[B_QFULL]);
   }
 
-  // The page of this warp's block of tile `i`: -1 if the block does not count.
-  __device__ int page_of(const Walk& u, int i) const {
-    if (i >= u.hist_end() || (8 * i + wp) * KV8_BLK >= u.r.H) return -1;
-    const int id = a.cv.page_table[(size_t)u.b * a.cv.max_pages_per_req + 2 * i + (wp >> 2)];
-    if (id >= 0 && id < a.cv.num_pages) return id;
-    if (lane == 0) record_error(a.cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
-    return -1;
-  }
-
   __device__ void history(const Walk& u) {
-    const int end = u.hist_end(), sub = wp % KV8_PAGE_BLOCKS;
+    const CacheView& cv = a.cv;
+    const int end = u.hist_end(), sub = wp % KV8_PAGE_BLOCKS, blocks = u.r.H / KV8_BLK;
+    const int32_t* pages = cv.page_table + (size_t)u.b * cv.max_pages_per_req + (wp >> 2);
+    const uint8_t* mine = kv8_head(cv, 0, u.h) + sub * KV8_BLOCK_BYTES;  // this warp's block in page 0
+    constexpr int NO_BLOCK = INT32_MIN;
     Codes k, v;
     float2 sc = make_float2(0.f, 0.f);
-    int now = page_of(u, u.i0), next = page_of(u, u.i0 + 1);
+    // The entry of the page with this warp's block of tile i, NO_BLOCK if there is none.  It
+    // is looked at a tile later: a load that is looked at at once takes its time.
+    auto entry = [&](int i) { return i < end && 8 * i + wp < blocks ? pages[2 * i] : NO_BLOCK; };
+    auto good = [&](int id) {
+      if (id >= 0 && id < cv.num_pages) return id;
+      if (id != NO_BLOCK && lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+      return -1;
+    };
     auto load_k = [&](int pid) {
-      const uint8_t* base = kv8_head(a.cv, pid < 0 ? 0 : pid, u.h);
-      load_codes<0>(k, base + sub * KV8_BLOCK_BYTES, pid >= 0, lane);
-      if (pid >= 0) sc = __ldcg((const float2*)(base + KV8_OFF_SCALES) + sub);
+      const uint8_t* block = mine + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes);
+      load_codes<0>(k, block, pid >= 0, lane);
+      if (pid >= 0) sc = __ldcg((const float2*)(block - sub * KV8_BLOCK_BYTES + KV8_OFF_SCALES) + sub);
     };
-    auto load_v = [&](int pid) {
-      load_codes<1>(v, kv8_head(a.cv, pid < 0 ? 0 : pid, u.h) + sub * KV8_BLOCK_BYTES, pid >= 0, lane);
-    };
+    auto load_v = [&](int pid) { load_codes<1>(v, mine + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes), pid >= 0, lane); };
+    int now = good(entry(u.i0)), next = entry(u.i0 + 1);
     load_k(now);
     load_v(now);
     load_q16(u);
     const uint32_t base = saddr(smem + OFF_BUF);
 #pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
-      const int after = page_of(u, i + 2), kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
+      const int after = entry(i + 2), kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
       if (!wait_empty(2 * gt)) return;
       const bool bad = now >= 0 && sc.y != sc.y;
       info(u, make_float2(sc.x * C0, now < 0 || bad ? 0.f : log2f(sc.y)), now < 0 ? 0 : bad ? 3 : 1,
@@ -509,6 +527,7 @@ struct Producer {
       store_k<TYPE>(base + kb * BUF, k, wp, lane);
       fence_proxy_async();
       arrive(&bars[B_FULL + kb]);
+      next = good(next);
       load_k(next);
       if (!wait_empty(2 * gt + 1)) return;
       store_v<TYPE>(base + vb * BUF, v, wp, lane);
@@ -601,10 +620,8 @@ __device__ __forceinline__ void scores_mma(uint32_t d, uint32_t q, uint32_t k, u
     for (int ks = 0; ks < 4; ++ks) mma_ss(d, desc(q + 2 * ks, hi), desc(k + 2 * ks, hi), id, half | ks);
 }
 __device__ __forceinline__ void values_mma(uint32_t d, uint32_t p, uint32_t v, uint64_t hi, uint32_t id, uint32_t add) {
-#pragma unroll 1
-  for (int half = 0; half < 2; ++half, p += 32, v += 4 * (2048 >> 4))
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) mma_ts(d, p + 8 * kk, desc(v + kk * (2048 >> 4), hi), id, add | half | kk);
+  for (int kk = 0; kk < 4; ++kk) mma_ts(d, p + 8 * kk, desc(v + kk * (2048 >> 4), hi), id, add | kk);  // 64 tokens
 }
 
 __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
@@ -623,21 +640,27 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
   auto wait = [&](int bar, uint32_t phase) {
     return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
   };
-  auto scores = [&]() -> bool {
-    if (!s.half) {
-      if (!wait(B_FULL + s.buf, s.phase)) return false;
-      s.flags = same(infos[s.tile & (NINFO - 1)].flags);
-      if (s.flags & F_NEWQ) {
-        if (!wait(B_QFULL, qphase)) return false;
-        qphase ^= 1;
-      }
+  auto learn_s = [&]() -> bool {
+    if (s.half) return true;
+    if (!wait(B_FULL + s.buf, s.phase)) return false;
+    s.flags = same(infos[s.tile & (NINFO - 1)].flags);
+    if (s.flags & F_NEWQ) {
+      if (!wait(B_QFULL, qphase)) return false;
+      qphase ^= 1;
     }
-    fence_after();
+    return true;
+  };
+  auto learn_p = [&]() -> bool {
+    if (p.half) return true;
+    if (!wait(B_FULL + p.buf, p.phase)) return false;
+    p.flags = same(infos[p.tile & (NINFO - 1)].flags);
+    return true;
+  };
+  auto scores = [&]() {
     const uint32_t w = s.step & 1, q = qlo + (s.flags & F_TWO ? w * (BUF >> 4) : 0), k = blo + s.buf * (BUF >> 4);
-    const uint32_t d = tmem + S_COL + TILE * w;
     const bool last = !(s.flags & F_TWO) || s.half;  // of the tile's steps
     if (elect()) {
-      scores_mma(d, q, k, hi, s.flags & F_HIST ? idesc(0, 0) : idesc(1, 0));
+      scores_mma(tmem + S_COL + TILE * w, q, k, hi, s.flags & F_HIST ? idesc(0, 0) : idesc(1, 0));
       commit(&bars[B_S + w]);
       if (last) commit(&bars[B_EMPTY + s.buf]);
       if (last && (s.flags & F_ENDQ)) commit(&bars[B_QEMPTY]);
@@ -650,27 +673,20 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
       s.buf += 2;
       if (s.buf >= NBUF) s.buf -= NBUF, s.phase ^= 1;
     }
-    return true;
   };
-  auto values = [&]() -> bool {
-    const uint32_t w = p.step & 1;
-    if (!wait(B_P + w, pphase >> w)) return false;
-    pphase ^= 1u << w;
-    if (!p.half) {
-      if (!wait(B_FULL + p.buf, p.phase)) return false;
-      p.flags = same(infos[p.tile & (NINFO - 1)].flags);
-    }
-    fence_after();
-    const uint32_t v = blo + p.buf * (BUF >> 4), d = tmem + O_COL + TILE * w, add = started >> w & 1;
-    const bool last = !(p.flags & F_TWO) || p.half, end = last && (p.flags & F_ENDU);
+  auto values = [&](int part) {  // tokens 64 part .. + 63
+    const uint32_t w = p.step & 1, v = blo + p.buf * (BUF >> 4) + part * (4 * 2048 >> 4);
+    const bool last = part && (!(p.flags & F_TWO) || p.half), end = last && (p.flags & F_ENDU);
+    const uint32_t add = part | (started >> w & 1);
     started |= 1u << w;
     if (elect()) {
-      values_mma(d, tmem + S_COL + TILE * w, v, hi_mn, p.flags & F_HIST ? idesc(0, 1) : idesc(1, 1), add);
+      values_mma(tmem + O_COL + TILE * w, tmem + S_COL + TILE * w + 32 * part, v, hi_mn, p.flags & F_HIST ? idesc(0, 1) : idesc(1, 1), add);
       if (last) commit(&bars[B_EMPTY + p.buf]);
       if (end && (started & 1)) commit(&bars[B_O]);
       if (end && (started & 2)) commit(&bars[B_O + 1]);
     }
     __syncwarp();
+    if (!part) return;
     if (end) started = 0;
     ++p.step;
     p.half = !last;
@@ -679,14 +695,35 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
       p.buf += 2;
       if (p.buf >= NBUF) p.buf -= NBUF, p.phase ^= 1;
     }
-    return true;
   };
+  // A look at shared memory takes some 250 cycles beside the MMAs, so what a step needs is
+  // looked up before its P is awaited.
   bool ok = true;
-  for (int i = 0; i < 2; ++i)
-    if (ok && s.tile < total) ok = scores();
+  for (int i = 0; i < 2 && ok && s.tile < total; ++i) {
+    ok = learn_s();
+    fence_after();
+    if (ok) scores();
+  }
   while (ok && p.tile < total) {
-    ok = values();
-    if (ok && s.tile < total) ok = scores();
+    const bool more = s.tile < total;
+    const uint32_t w = p.step & 1, phase = pphase >> w;
+    pphase ^= 1u << w;
+    ok = learn_p() && wait(B_P + 2 * w, phase);
+    if (!ok) break;
+    fence_after();
+    values(0);
+    // (not awaited: K may need the V that this step frees)
+    const bool known = more && (s.half || (__all_sync(0xffffffffu, passed(&bars[B_FULL + s.buf], s.phase)) && learn_s()));
+    ok = wait(B_P + 2 * w + 1, phase);
+    if (!ok) break;
+    fence_after();
+    values(1);
+    if (more) {
+      ok = known || learn_s();
+      if (!ok) break;
+      if (!known) fence_after();
+      scores();
+    }
   }
   // all that was issued has ended before the tensor memory is given back
   if (elect()) commit(&bars[B_DRAIN]);
@@ -753,106 +790,121 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A tile for one row, in 32-column pieces of S, which are read twice: for the maximum
-// and for the exponentials (all 128 would not fit into the registers, and a spilled
-// one goes to the L2 here: shared memory has taken the L1).
-// Tokens that the row takes: `seen` first ones, and of those the blocks whose mark says so.
-// EVERY: all of them.
-template <bool EVERY>
-__device__ __forceinline__ void hide(uint32_t (&r)[32], int c, const Info* f, int seen) {
-  if (!EVERY) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (!(f->marks[2 * c + (j >> 4)] & 1) || 32 * c + j >= seen) r[j] = 0xff800000u;  // -infinity
-  }
+// 16 columns of S, and their largest.
+__device__ __forceinline__ void tmem_ld16_max(uint32_t at, uint32_t (&r)[16], float& m) {
+  asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(m)
+               : "r"(at)
+               : "memory");
 }
-// The scales of a tile's blocks in registers, read before S is awaited (from shared
-// memory, which the MMAs and the producers keep busy, each takes some 240 cycles):
-// four blocks at hand, four to come.
-struct Scales {
-  float4 at[2], to[2];  // (factor of the logits, log2 s_V) of two blocks
-  __device__ __forceinline__ void load(const Info* f, float al) {
-    const float4* x = (const float4*)f->cs;
-    at[0] = x[0], at[1] = x[1], to[0] = x[2], to[1] = x[3];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) at[i].x *= al, at[i].z *= al, to[i].x *= al, to[i].z *= al;
-  }
-  __device__ __forceinline__ void turn() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 x = at[i];
-      at[i] = to[i];
-      to[i] = x;
-    }
-  }
-};
-// Largest logit so far, and the same with the value scale.
-__device__ __forceinline__ void largest(const uint32_t (&r)[32], const float4& cs, float& mx, float& tx) {
-  float y[2];
-#pragma unroll
-  for (int hb = 0; hb < 2; ++hb) {
-    auto x = [&](int j) { return __uint_as_float(r[16 * hb + j]); };
-    float m0 = fmaxf(x(0), x(1)), m1 = fmaxf(x(2), x(3));
-#pragma unroll
-    for (int j = 4; j < 16; j += 4) {
-      m0 = max3(m0, x(j), x(j + 1));
-      m1 = max3(m1, x(j + 2), x(j + 3));
-    }
-    y[hb] = fmaxf(m0, m1);
-  }
-  y[0] *= cs.x;
-  y[1] *= cs.z;
-  mx = max3(mx, y[0], y[1]);
-  tx = max3(tx, y[0] + cs.y, y[1] + cs.w);
+__device__ __forceinline__ void tmem_ld16_async(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(at)
+               : "memory");
 }
-template <bool F16, bool EVERY>
-__device__ __forceinline__ void exponentials(const uint32_t (&r)[32], int c, Row& st, uint32_t sa, const Info* f, const float4& cs, int seen) {
-  uint32_t o[16];
-#pragma unroll
-  for (int hb = 0; hb < 2; ++hb) {
-    const int b = 2 * c + hb, mark = EVERY ? 1 : f->marks[b];
-    const float shift = max_nan((hb ? cs.w : cs.y) - st.M, -st.m - FAR), cb = hb ? cs.z : cs.x;
-    const uint64_t cb2 = pair(cb, cb), shift2 = pair(shift, shift);
-    uint64_t sum = 0;  // two zeros
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      float y, z;
-      unpair(fma2(pair(__uint_as_float(r[16 * hb + j]), __uint_as_float(r[16 * hb + j + 1])), cb2, shift2), y, z);
-      y = ex2(y);
-      z = ex2(z);
-      if (!EVERY) {
-        if (!(mark & 1) || 16 * b + j >= seen) y = 0.f;
-        if (!(mark & 1) || 16 * b + j + 1 >= seen) z = 0.f;
-      }
-      sum = add2(sum, pair(y, z));
-      if (!EVERY && (mark & 2)) y = z = NAN;
-      o[8 * hb + j / 2] = pack2<F16>(y, z);
-    }
-    float s0, s1;
-    unpair(sum, s0, s1);
-    st.l = fmaf(s0 + s1, ex2(-shift - st.m), st.l);
-  }
-  tmem_st16(sa + 16 * c, o);
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void after_wait(uint32_t (&r)[16]) {  // uses of r stay behind the wait
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
-// P of the tile to tensor memory, sums into the state.
+// Tokens of a tile that a row takes: `seen` first ones, and of those the blocks whose mark
+// (a byte each) says so.  EVERY: all of them.
+struct Taken {
+  uint32_t marks[2];
+  int seen;
+  __device__ __forceinline__ bool operator()(int b, int j) const { return (marks[b >> 2] >> (8 * (b & 3)) & 1) && 16 * b + j < seen; }
+  __device__ __forceinline__ bool nan(int b) const { return marks[b >> 2] >> (8 * (b & 3)) & 2; }
+};
+
+// P of block b from its S, and its sum into the state.
 template <bool F16, bool EVERY>
-__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, Scales& sc, int seen, bool first) {
-  uint32_t r0[32], r1[32];
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row& st, uint32_t sa, float cb, float lsv, const Taken& taken) {
+  const float shift = max_nan(lsv - st.M, -st.m - FAR);
+  const uint64_t cb2 = pair(cb, cb), shift2 = pair(shift, shift);
+  uint64_t sum = 0;  // two zeros
+  uint32_t o[8];
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    float y, z;
+    unpair(fma2(pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), cb2, shift2), y, z);
+    y = ex2(y);
+    z = ex2(z);
+    if (!EVERY) {
+      if (!taken(b, j)) y = 0.f;
+      if (!taken(b, j + 1)) z = 0.f;
+    }
+    sum = add2(sum, pair(y, z));
+    if (!EVERY && taken.nan(b)) y = z = NAN;
+    o[j / 2] = pack2<F16>(y, z);
+  }
+  float s0, s1;
+  unpair(sum, s0, s1);
+  st.l = fmaf(s0 + s1, ex2(-shift - st.m), st.l);
+  tmem_st8(sa + 8 * b, o);
+}
+
+// Largest of a block's taken logits, where not all are.
+__device__ __forceinline__ float largest(const uint32_t (&r)[16], int b, const Taken& taken) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = fmaxf(m, taken(b, j) ? __uint_as_float(r[j]) : -INFINITY);
+  return m;
+}
+
+// P of the tile to tensor memory, in two halves (said: tells of the first), sums into the
+// state.  S of the second half is read twice, as the registers do not hold all of it (and
+// a spilled one goes to the L2 here: shared memory has taken the L1).
+template <bool F16, bool EVERY, typename Said>
+__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, const Taken& taken, bool first, Said said) {
+  uint32_t r[4][16];
+  float mb[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld16_max(sa + 64 + 16 * i, r[i], mb[4 + i]);
+  const float4* cs = (const float4*)f->cs;
   float mx = NONE, tx = NONE;
-  tmem_ld32(sa, r0);
-  tmem_ld_wait_regs(r0);
-#pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    tmem_ld32(sa + 32 * (c + 1), r1);
-    hide<EVERY>(r0, c, f, seen);
-    largest(r0, sc.at[0], mx, tx);
-    tmem_ld_wait_regs(r1);
-    tmem_ld32(sa + 32 * (c ^ 2), r0);  // the third piece, then the first again
-    hide<EVERY>(r1, c + 1, f, seen);
-    largest(r1, sc.at[1], mx, tx);
-    sc.turn();
-    tmem_ld_wait_regs(r0);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) after_wait(r[i]);
+  if (!EVERY)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mb[4 + i] = largest(r[i], 4 + i, taken);
+  asm volatile("" : "+f"(mb[4]), "+f"(mb[5]), "+f"(mb[6]), "+f"(mb[7])::"memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tmem_ld16_max(sa + 16 * i, r[i], mb[i]);
+  float4 sc[2];
+#pragma unroll
+  for (int i = 2; i < 4; ++i) {
+    const float4 c = cs[i];
+    const float y = mb[2 * i] * (c.x * al), z = mb[2 * i + 1] * (c.z * al);
+    mx = max3(mx, y, z);
+    tx = max3(tx, y + c.y, z + c.w);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sc[i] = cs[i];
+    sc[i].x *= al, sc[i].z *= al;
+  }
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) after_wait(r[i]);
+  if (!EVERY)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mb[i] = largest(r[i], i, taken);
+  asm volatile("" : "+f"(mb[0]), "+f"(mb[1]), "+f"(mb[2]), "+f"(mb[3])::"memory");
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float y = mb[2 * i] * sc[i].x, z = mb[2 * i + 1] * sc[i].z;
+    mx = max3(mx, y, z);
+    tx = max3(tx, y + sc[i].y, z + sc[i].w);
   }
   const float mn = fmaxf(st.m, mx);
   st.l *= ex2(st.m - mn);
@@ -872,16 +924,24 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
       tmem_st16(oa + c, v);
     }
   }
-#pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    tmem_ld32(sa + 32 * (c + 1), r1);
-    exponentials<F16, EVERY>(r0, c, st, sa, f, sc.at[0], seen);
-    tmem_ld_wait_regs(r1);
-    if (c == 0) tmem_ld32(sa + 64, r0);
-    exponentials<F16, EVERY>(r1, c + 1, st, sa, f, sc.at[1], seen);
-    sc.turn();
-    tmem_ld_wait_regs(r0);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    exponentials<F16, EVERY>(r[b], b, st, sa, b & 1 ? sc[b >> 1].z : sc[b >> 1].x, b & 1 ? sc[b >> 1].w : sc[b >> 1].y, taken);
+    tmem_ld16_async(sa + 64 + 16 * b, r[b]);
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sc[i] = cs[2 + i];
+    sc[i].x *= al, sc[i].z *= al;
+  }
+  tmem_st_wait();
+  said();
+  tmem_ld_wait();
+#pragma unroll
+  for (int b = 0; b < 4; ++b) after_wait(r[b]);
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    exponentials<F16, EVERY>(r[b], 4 + b, st, sa, b & 1 ? sc[b >> 1].z : sc[b >> 1].x, b & 1 ? sc[b >> 1].w : sc[b >> 1].y, taken);
   tmem_st_wait();
 }
 
@@ -1007,40 +1067,31 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
     int cnt = 0;
     for (int i = two ? 0 : (wg - g) & 1; i < tiles; i += two ? 1 : 2) {
       const int tile = gt + i;
-      ok = wait(B_INFO + (tile & (NINFO - 1)), tile / NINFO);
-      if (!ok) break;
-      const Info* f = (const Info*)(smem + OFF_INFO) + (tile & (NINFO - 1));
-      Scales sc;
-      bool every;
-      int seen = TILE;
-      if (i < hist) {
-        // the row's exponent is there when Q is, which the first S tells
-        if (cnt > 0) sc.load(f, al);
-        const uint32_t* marks = (const uint32_t*)f->marks;
-        every = marks[0] == ALL_COUNT && marks[1] == ALL_COUNT;
-      } else {
-        sc.load(f, 1.f);
-        seen = line - (i - hist) * TILE;
-        every = __all_sync(0xffffffffu, seen >= TILE);
-      }
+      // S of a tile tells that all about it is there: the MMAs began after the producers had
+      // told of K, which they do last
       ok = wait(B_S + wg, ns);
       if (!ok) break;
       ++ns;
       fence_after();
-      if (i < hist && cnt == 0) {
-        al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
-        sc.load(f, al);
-      }
+      const Info* f = (const Info*)(smem + OFF_INFO) + (tile & (NINFO - 1));
+      auto said = [&]() {
+        fence_before();
+        __syncwarp();
+        if ((tid & 31) == 0) arrive(&bars[B_P + 2 * wg]);
+      };
       if (i < hist) {
-        if (every) weigh<true, true>(st, sa, oa, f, sc, TILE, cnt == 0);
-        else weigh<true, false>(st, sa, oa, f, sc, TILE, cnt == 0);
+        if (cnt == 0) al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
+        const Taken taken = {{((const uint32_t*)f->marks)[0], ((const uint32_t*)f->marks)[1]}, TILE};
+        if (taken.marks[0] == ALL_COUNT && taken.marks[1] == ALL_COUNT) weigh<true, true>(st, sa, oa, f, al, taken, cnt == 0, said);
+        else weigh<true, false>(st, sa, oa, f, al, taken, cnt == 0, said);
       } else {
-        if (every) weigh<false, true>(st, sa, oa, f, sc, TILE, cnt == 0);
-        else weigh<false, false>(st, sa, oa, f, sc, seen, cnt == 0);
+        const Taken taken = {{ALL_COUNT, ALL_COUNT}, line - (i - hist) * TILE};
+        if (__all_sync(0xffffffffu, taken.seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, taken, cnt == 0, said);
+        else weigh<false, false>(st, sa, oa, f, 1.f, taken, cnt == 0, said);
       }
       fence_before();
       __syncwarp();
-      if ((tid & 31) == 0) arrive(&bars[B_P + wg]);
+      if ((tid & 31) == 0) arrive(&bars[B_P + 2 * wg + 1]);
       ++cnt;
     }
     if (ok && cnt > 0) {
@@ -1106,7 +1157,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], PROD_WARPS);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_S + i], 1);
-      mbar_init(&bars[B_P + i], 4);
+      mbar_init(&bars[B_P + 2 * i], 4);
+      mbar_init(&bars[B_P + 2 * i + 1], 4);
       mbar_init(&bars[B_O + i], 1);
     }
     mbar_init(&bars[B_QFULL], PROD);
