@@ -493,17 +493,18 @@ struct Producer {
   __device__ void history(const Walk& u) {
     const CacheView& cv = a.cv;
     const int end = u.hist_end(), sub = wp % KV8_PAGE_BLOCKS, blocks = u.r.H / KV8_BLK;
-    const int32_t* pages = cv.page_table + (size_t)u.b * cv.max_pages_per_req + (wp >> 2);
+    const int32_t* pages = cv.page_table + (size_t)u.b * cv.max_pages_per_req;
+    const int last_page = (u.r.H - 1) / PAGE;
     const uint8_t* mine = kv8_head(cv, 0, u.h) + sub * KV8_BLOCK_BYTES;  // this warp's block in page 0
-    constexpr int NO_BLOCK = INT32_MIN;
     Codes k, v;
     float2 sc = make_float2(0.f, 0.f);
-    // The entry of the page with this warp's block of tile i, NO_BLOCK if there is none.  It
-    // is looked at a tile later: a load that is looked at at once takes its time.
-    auto entry = [&](int i) { return i < end && 8 * i + wp < blocks ? pages[2 * i] : NO_BLOCK; };
-    auto good = [&](int id) {
+    // The entry of the page with this warp's block of tile i (any entry, where there is no such
+    // block).  It is looked at a tile later: what is made of a load at once takes its time.
+    auto entry = [&](int i) { return pages[min(2 * i + (wp >> 2), last_page)]; };
+    auto good = [&](int id, int i) {
+      if (i >= end || 8 * i + wp >= blocks) return -1;
       if (id >= 0 && id < cv.num_pages) return id;
-      if (id != NO_BLOCK && lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+      if (lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
       return -1;
     };
     auto load_k = [&](int pid) {
@@ -512,14 +513,25 @@ struct Producer {
       if (pid >= 0) sc = __ldcg((const float2*)(block - sub * KV8_BLOCK_BYTES + KV8_OFF_SCALES) + sub);
     };
     auto load_v = [&](int pid) { load_codes<1>(v, mine + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes), pid >= 0, lane); };
-    int now = good(entry(u.i0)), next = entry(u.i0 + 1);
+    // The page of tile i into the L2, by one lane for each page: the registers have room for
+    // one tile, the memory takes longer than one.
+    auto fetch = [&](int pid) {
+      if (pid >= 0 && wp % KV8_PAGE_BLOCKS == 0 && lane == 0)
+        bulk_prefetch_l2(cv.pool + (size_t)pid * cv.page_bytes + (size_t)u.h * KV8_HEAD_BYTES, KV8_HEAD_BYTES);
+    };
+    int now = good(entry(u.i0), u.i0), next = entry(u.i0 + 1), far = entry(u.i0 + 2);
     load_k(now);
     load_v(now);
+    next = good(next, u.i0 + 1);
+    fetch(next);
     load_q16(u);
     const uint32_t base = saddr(smem + OFF_BUF);
 #pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
-      const int after = entry(i + 2), kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
+      const int after = far, kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
+      far = entry(i + 3);
+      const int ahead = good(after, i + 2);
+      fetch(ahead);
       if (!wait_empty(2 * gt)) return;
       const bool bad = now >= 0 && sc.y != sc.y;
       info(u, make_float2(sc.x * C0, now < 0 || bad ? 0.f : log2f(sc.y)), now < 0 ? 0 : bad ? 3 : 1,
@@ -527,7 +539,6 @@ struct Producer {
       store_k<TYPE>(base + kb * BUF, k, wp, lane);
       fence_proxy_async();
       arrive(&bars[B_FULL + kb]);
-      next = good(next);
       load_k(next);
       if (!wait_empty(2 * gt + 1)) return;
       store_v<TYPE>(base + vb * BUF, v, wp, lane);
@@ -535,7 +546,7 @@ struct Producer {
       arrive(&bars[B_FULL + vb]);
       load_v(next);
       now = next;
-      next = after;
+      next = ahead;
     }
   }
 
