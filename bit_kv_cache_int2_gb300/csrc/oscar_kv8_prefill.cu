@@ -13,7 +13,7 @@
 // (S of each row tile 128 columns, P over the first half of its S, O 128), Q, K, V
 // in shared memory, 128-byte swizzled.  Warps:
 //   0-7   softmax, four for each row tile, a thread per row
-//   8-15  producers, one for each block of 16 tokens: history codes from global memory through registers to FP16
+//   8-15  producers, four for keys and four for values: history codes from global memory through registers to FP16
 //         tiles (both code types are exact there), BF16 tokens by cp.async as they
 //         are; K and V tiles alternate in a ring of five
 //   16    the MMAs: S of the step after next is issued behind O of this one, so the
@@ -43,10 +43,10 @@ namespace {
 using namespace tcgen05;
 
 constexpr int ROWS = 256, TILE = 128;
-constexpr int PROD_WARPS = 8, PROD = 32 * PROD_WARPS;  // a warp for each 16-token block of a tile
+constexpr int PROD = 256, SIDE = 128;  // producer threads: 128 for K, 128 for V
 constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 17-19 fill the MMA warp's group up
-// Registers a thread: 256·144 + 256·80 + 128·32 = the 640·96 of the launch.
-constexpr int REGS_SOFTMAX = 144, REGS_PROD = 80, REGS_MMA = 32;
+// Registers a thread: 256·136 + 256·88 + 128·32 = the 640·96 of the launch.
+constexpr int REGS_SOFTMAX = 136, REGS_PROD = 88, REGS_MMA = 32;
 constexpr int NBUF = 5, REGION = 16384, BUF = 2 * REGION;  // a tile: two regions of 64 channels, [128 rows][128 B]
 constexpr int NINFO = 4, NALPHA = 3, NUNIT = 8;
 constexpr int OFF_Q = 0, OFF_BUF = 2 * BUF, OFF_BAR = OFF_BUF + NBUF * BUF;
@@ -338,7 +338,7 @@ struct Producer {
   uint8_t* smem;
   uint64_t* bars;
   Misc* misc;
-  int t, wp, lane;  // thread of 256, warp of 8
+  int t, wp, lane, side;  // thread of 256, warp of its side's four; K: 0, V: 1
   bool ok = true;
   int gt = 0, qn = 0, un = 0;  // token tiles, loads of Q, units
   bool told = false;           // this unit is published
@@ -350,7 +350,8 @@ struct Producer {
   int npend = 0;
 
   __device__ Producer(const Kv8Prefill& args, uint8_t* s, int tid)
-      : a(args), smem(s), bars((uint64_t*)(s + OFF_BAR)), misc((Misc*)(s + OFF_MISC)), t(tid - PROD0), wp((tid - PROD0) >> 5), lane(tid & 31) {}
+      : a(args), smem(s), bars((uint64_t*)(s + OFF_BAR)), misc((Misc*)(s + OFF_MISC)), t(tid - PROD0), wp(((tid - PROD0) >> 5) & 3), lane(tid & 31),
+        side((int)__shfl_sync(0xffffffffu, (tid - PROD0) / SIDE, 0)) {}
 
   __device__ bool wait(int bar, int phase) {
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
@@ -368,8 +369,8 @@ struct Producer {
   __device__ void tell(const Pending& p) {
     if (p.from < p.to) {  // this thread's own pieces
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const int tok = 16 * i + (t >> 4), ch = t & 15;
+      for (int i = 0; i < 16; ++i) {
+        const int tok = 8 * i + (t % SIDE >> 4), ch = t & 15;
         uint4* x = (uint4*)(smem + OFF_BUF + p.buf * BUF + (ch >> 3) * REGION + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
         if (tok < p.from || tok >= p.to) continue;
         uint32_t w[4] = {x->x, x->y, x->z, x->w};
@@ -423,15 +424,17 @@ struct Producer {
     x->b = u.b, x->h = u.h, x->t0 = u.t0, x->t1 = u.t1;
     x->c0 = s0 - u.r.w, x->c1 = (u.i1 - u.r.nh) * TILE - u.r.w;
   }
+  // Lanes 0 and 1 of the K warps: blocks 2 wp, 2 wp + 1 of the tile.
   __device__ void info(const Walk& u, float2 cs, int mark, uint32_t flags) {
     if (!told) publish(u);
-    if (lane == 0) {
-      Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
-      f->cs[wp] = cs;
-      f->marks[wp] = (uint8_t)mark;
-      if (wp == 0) f->flags = flags;
-      arrive(&bars[B_INFO + (gt & (NINFO - 1))]);
+    Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
+    if (lane < 2) {
+      f->cs[2 * wp + lane] = cs;
+      f->marks[2 * wp + lane] = (uint8_t)mark;
     }
+    if (t == 0) f->flags = flags;
+    __syncwarp();
+    if (lane == 0) arrive(&bars[B_INFO + (gt & (NINFO - 1))]);
   }
 
   // Rows of the unit, 16 lanes a row: token and head of row i, 16-byte piece t & 15.
@@ -490,61 +493,68 @@ struct Producer {
     arrive(&bars[B_QFULL]);
   }
 
+  // The history's tiles, one side of them.  A warp has blocks 2 wp, 2 wp + 1, its lanes their
+  // codes of the next tile in registers.
+  template <int S>
   __device__ void history(const Walk& u) {
     const CacheView& cv = a.cv;
-    const int end = u.hist_end(), sub = wp % KV8_PAGE_BLOCKS, blocks = u.r.H / KV8_BLK;
+    const int end = u.hist_end(), blocks = u.r.H / KV8_BLK, sub = 2 * wp % KV8_PAGE_BLOCKS;
     const int32_t* pages = cv.page_table + (size_t)u.b * cv.max_pages_per_req;
     const int last_page = (u.r.H - 1) / PAGE;
-    const uint8_t* mine = kv8_head(cv, 0, u.h) + sub * KV8_BLOCK_BYTES;  // this warp's block in page 0
-    Codes k, v;
+    const uint8_t* head = kv8_head(cv, 0, u.h);  // in page 0
+    Codes c[2];
     float2 sc = make_float2(0.f, 0.f);
-    // The entry of the page with this warp's block of tile i (any entry, where there is no such
-    // block).  It is looked at a tile later: what is made of a load at once takes its time.
-    auto entry = [&](int i) { return pages[min(2 * i + (wp >> 2), last_page)]; };
+    // The entry of the page with the warp's blocks of tile i (any entry, where there are none).  It
+    // is looked at a tile later: what is made of a load at once takes its time.
+    auto entry = [&](int i) { return pages[min(2 * i + (wp >> 1), last_page)]; };
     auto good = [&](int id, int i) {
-      if (i >= end || 8 * i + wp >= blocks) return -1;
+      if (i >= end || 8 * i + 2 * wp >= blocks) return -1;
       if (id >= 0 && id < cv.num_pages) return id;
-      if (lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+      if (S == 0 && lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
       return -1;
     };
-    auto load_k = [&](int pid) {
-      const uint8_t* block = mine + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes);
-      load_codes<0>(k, block, pid >= 0, lane);
-      if (pid >= 0) sc = __ldcg((const float2*)(block - sub * KV8_BLOCK_BYTES + KV8_OFF_SCALES) + sub);
+    auto there = [&](int pid, int i, int j) { return pid >= 0 && 8 * i + 2 * wp + j < blocks; };
+    auto load = [&](int pid, int i, int j) {
+      load_codes<S>(c[j], head + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes) + (sub + j) * KV8_BLOCK_BYTES, there(pid, i, j), lane);
     };
-    auto load_v = [&](int pid) { load_codes<1>(v, mine + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes), pid >= 0, lane); };
+    auto scales = [&](int pid, int i) {
+      if (S == 0 && lane < 2 && there(pid, i, lane))
+        sc = __ldcg((const float2*)(head + (size_t)pid * cv.page_bytes + KV8_OFF_SCALES) + sub + lane);
+    };
     // The page of tile i into the L2, by one lane for each page: the registers have room for
     // one tile, the memory takes longer than one.
     auto fetch = [&](int pid) {
-      if (pid >= 0 && wp % KV8_PAGE_BLOCKS == 0 && lane == 0)
-        bulk_prefetch_l2(cv.pool + (size_t)pid * cv.page_bytes + (size_t)u.h * KV8_HEAD_BYTES, KV8_HEAD_BYTES);
+      if (S == 0 && pid >= 0 && !(wp & 1) && lane == 0) bulk_prefetch_l2(head + (size_t)pid * cv.page_bytes, KV8_HEAD_BYTES);
     };
     int now = good(entry(u.i0), u.i0), next = entry(u.i0 + 1), far = entry(u.i0 + 2);
-    load_k(now);
-    load_v(now);
+    load(now, u.i0, 0);
+    load(now, u.i0, 1);
+    scales(now, u.i0);
     next = good(next, u.i0 + 1);
     fetch(next);
     load_q16(u);
     const uint32_t base = saddr(smem + OFF_BUF);
 #pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
-      const int after = far, kb = 2 * gt % NBUF, vb = (2 * gt + 1) % NBUF;
+      const int after = far, item = 2 * gt + S, buf = item % NBUF;
       far = entry(i + 3);
       const int ahead = good(after, i + 2);
       fetch(ahead);
-      if (!wait_empty(2 * gt)) return;
-      const bool bad = now >= 0 && sc.y != sc.y;
-      info(u, make_float2(sc.x * C0, now < 0 || bad ? 0.f : log2f(sc.y)), now < 0 ? 0 : bad ? 3 : 1,
-           F_HIST | (u.two ? F_TWO : 0) | (i == u.i0 ? F_NEWQ : 0) | (i + 1 == end ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0));
-      store_k<TYPE>(base + kb * BUF, k, wp, lane);
+      if (!wait_empty(item)) return;
+      if (S == 0) {
+        const bool on = lane < 2 && there(now, i, lane), bad = on && sc.y != sc.y;
+        info(u, make_float2(sc.x * C0, !on || bad ? 0.f : log2f(sc.y)), !on ? 0 : bad ? 3 : 1,
+             F_HIST | (u.two ? F_TWO : 0) | (i == u.i0 ? F_NEWQ : 0) | (i + 1 == end ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0));
+        scales(next, i + 1);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (S == 0) store_k<TYPE>(base + buf * BUF, c[j], 2 * wp + j, lane);
+        else store_v<TYPE>(base + buf * BUF, c[j], 2 * wp + j, lane);
+        load(next, i + 1, j);
+      }
       fence_proxy_async();
-      arrive(&bars[B_FULL + kb]);
-      load_k(next);
-      if (!wait_empty(2 * gt + 1)) return;
-      store_v<TYPE>(base + vb * BUF, v, wp, lane);
-      fence_proxy_async();
-      arrive(&bars[B_FULL + vb]);
-      load_v(next);
+      arrive(&bars[B_FULL + buf]);
       now = next;
       next = ahead;
     }
@@ -568,31 +578,28 @@ struct Producer {
     const int nsink = u.r.L < SINK ? u.r.L : SINK, all = u.r.w + u.t1;
     for (int i = u.line_begin(); i < u.i1 && ok; ++i, ++gt) {
       const int s0 = (i - u.r.nh) * TILE;
-#pragma unroll 1
-      for (int side = 0; side < 2; ++side) {
-        const int item = 2 * gt + side, buf = item % NBUF;
-        if (!wait_empty(item)) return;
-        if (side == 0)
-          info(u, make_float2(C0, 0.f), 1,
-               (u.two ? F_TWO : 0) | (i == u.line_begin() ? F_NEWQ : 0) | (i + 1 == u.i1 ? F_ENDQ | F_ENDU : 0));
-        const __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
-        const __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
-        const __nv_bfloat16* fresh = (side ? a.v : a.k) + ((size_t)u.b * u.geo.T * cv.Hkv + u.h) * D;
-        const int ch = t & 15;
-        const uint32_t to = saddr(smem + OFF_BUF) + buf * BUF + (ch >> 3) * REGION;
+      const int item = 2 * gt + side, buf = item % NBUF;
+      if (!wait_empty(item)) return;
+      if (side == 0)
+        info(u, make_float2(C0, 0.f), 1,
+             (u.two ? F_TWO : 0) | (i == u.line_begin() ? F_NEWQ : 0) | (i + 1 == u.i1 ? F_ENDQ | F_ENDU : 0));
+      const __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
+      const __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
+      const __nv_bfloat16* fresh = (side ? a.v : a.k) + ((size_t)u.b * u.geo.T * cv.Hkv + u.h) * D;
+      const int ch = t & 15;
+      const uint32_t to = saddr(smem + OFF_BUF) + buf * BUF + (ch >> 3) * REGION;
 #pragma unroll 4
-        for (int j = 0; j < 8; ++j) {
-          const int tok = 16 * j + (t >> 4), s = s0 + tok;
-          const bool on = s < all;
-          const __nv_bfloat16* p = s < nsink   ? sink + (size_t)s * D
-                                   : s < u.r.w ? ring + (size_t)((u.r.H + s - nsink) & (RECENT - 1)) * D
-                                               : fresh + (size_t)(on ? s - u.r.w : 0) * cv.Hkv * D;
-          copy16(to + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4), p + 8 * ch, on);
-        }
-        // tokens that only some of the unit's rows see: chunk tokens behind its first
-        const int from = u.r.w + u.t0 + 1 - s0, cut_to = all - s0 < TILE ? all - s0 : TILE;
-        push(B_FULL + buf, buf, side ? (from > 0 ? from : 0) : 0, side ? cut_to : 0);
+      for (int j = 0; j < 16; ++j) {
+        const int tok = 8 * j + (t % SIDE >> 4), s = s0 + tok;
+        const bool on = s < all;
+        const __nv_bfloat16* p = s < nsink   ? sink + (size_t)s * D
+                                 : s < u.r.w ? ring + (size_t)((u.r.H + s - nsink) & (RECENT - 1)) * D
+                                             : fresh + (size_t)(on ? s - u.r.w : 0) * cv.Hkv * D;
+        copy16(to + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4), p + 8 * ch, on);
       }
+      // tokens that only some of the unit's rows see: chunk tokens behind its first
+      const int from = u.r.w + u.t0 + 1 - s0, cut_to = all - s0 < TILE ? all - s0 : TILE;
+      push(B_FULL + buf, buf, side ? (from > 0 ? from : 0) : 0, side ? cut_to : 0);
     }
     flush();
   }
@@ -601,7 +608,10 @@ struct Producer {
     Walk u(a, misc);
     for (; u.more() && ok; u.next(), ++un) {
       told = false;
-      if (u.i0 < u.hist_end()) history(u);
+      if (u.i0 < u.hist_end()) {
+        if (side == 0) history<0>(u);
+        else history<1>(u);
+      }
       if (ok && u.line_begin() < u.i1) line(u);
     }
     copies_wait<0>();
@@ -1162,10 +1172,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(&bars[B_FULL + i], PROD);
+      mbar_init(&bars[B_FULL + i], SIDE);
       mbar_init(&bars[B_EMPTY + i], 1);
     }
-    for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], PROD_WARPS);
+    for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], SIDE / 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_S + i], 1);
       mbar_init(&bars[B_P + 2 * i], 4);
