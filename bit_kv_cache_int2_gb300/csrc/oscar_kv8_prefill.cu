@@ -78,7 +78,7 @@ constexpr int OFF_INFO = OFF_BAR + 240, OFF_UNIT = OFF_INFO + NINFO * (int)sizeo
 constexpr int OFF_XCH = OFF_ALPHA + NALPHA * ROWS, OFF_MISC = OFF_XCH + TILE * 8;
 struct Misc {
   uint32_t tmem;
-  int abort, bad_v, pad0;
+  int abort, bad_v, tiles;  // tiles: in the part
   long long lo, hi, at;
   int b, h, rt, pad;
 };
@@ -107,6 +107,9 @@ __device__ __forceinline__ long long tiles_sum(int w, long long n, int c) {
   return n * (a / TILE) + f(n + e) - f(e);
 }
 
+// Loading Q and writing the rows takes a unit about as long as so many tiles.
+constexpr int UNIT_COST = 3;
+
 struct Geo {
   int T, c, RT;  // tokens, tokens of a unit, units of a (request, kv head)
   __device__ explicit Geo(const Kv8Prefill& a) : T(a.T), c(ROWS / a.cv.G), RT((int)(((long long)a.T * a.cv.G + ROWS - 1) / ROWS)) {}
@@ -121,9 +124,10 @@ struct Lens {
     nh = (H + TILE - 1) / TILE;
     w = L - H;
   }
-  __device__ long long before(const Geo& g, int rt) const { return (long long)rt * nh + tiles_sum(w, rt, g.c); }
+  // Places in the list: a unit has UNIT_COST empty ones and then its tiles.
+  __device__ long long before(const Geo& g, int rt) const { return (long long)rt * (UNIT_COST + nh) + tiles_sum(w, rt, g.c); }
   __device__ long long per_head(const Geo& g) const {
-    return (long long)g.RT * nh + tiles_sum(w, g.RT - 1, g.c) + ((long long)w + g.T + TILE - 1) / TILE;
+    return (long long)g.RT * (UNIT_COST + nh) + tiles_sum(w, g.RT - 1, g.c) + ((long long)w + g.T + TILE - 1) / TILE;
   }
 };
 
@@ -142,6 +146,7 @@ struct Walk {
     if (more()) {
       r.load(a.cv, b);
       unit();
+      if (i0 >= i1) next();
     }
   }
   __device__ bool more() const { return at < hi; }
@@ -150,20 +155,23 @@ struct Walk {
     t1 = geo.T - t0 < geo.c ? geo.T : t0 + geo.c;
     two = (t1 - t0) * a.cv.G > TILE;
     n = r.nh + (r.w + t1 + TILE - 1) / TILE;
-    i0 = at < lo ? (int)(lo - at) : 0;
-    i1 = hi - at < n ? (int)(hi - at) : n;
+    const long long first = at + UNIT_COST;
+    i0 = first < lo ? (int)(lo - first) : 0;
+    i1 = hi - first < n ? (int)(hi - first) : n;
   }
-  __device__ void next() {
-    at += n;
-    if (++rt == geo.RT) {
-      rt = 0;
-      if (++h == a.cv.Hkv) {
-        h = 0;
-        ++b;
-        if (more()) r.load(a.cv, b);
+  __device__ void next() {  // the next unit with a tile in the part
+    do {
+      at += UNIT_COST + n;
+      if (++rt == geo.RT) {
+        rt = 0;
+        if (++h == a.cv.Hkv) {
+          h = 0;
+          ++b;
+          if (more()) r.load(a.cv, b);
+        }
       }
-    }
-    if (more()) unit();
+      if (more()) unit();
+    } while (more() && i0 >= i1);
   }
   __device__ int hist_end() const { return i1 < r.nh ? i1 : r.nh; }  // tiles i0 .. here are history
   __device__ int line_begin() const { return i0 > r.nh ? i0 : r.nh; }
@@ -204,6 +212,7 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     m->lo = lo;
     m->hi = hi;
     m->at = 0;
+    m->tiles = 0;
     if (!any) a.splits[blockIdx.x] = make_int4(0, 0, 0, -1);
   }
   if (!any || lane > 1) return;
@@ -221,15 +230,20 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     if (r.before(g, mid) <= x) rt = mid; else top = mid - 1;
   }
   const long long begin = pre[b] + h * per + r.before(g, rt);
+  // tiles in front of the part, and in front of its end
+  const long long in_unit = (lane == 0 ? lo : hi) - begin - UNIT_COST;
+  const long long real = begin - UNIT_COST * (((long long)b * cv.Hkv + h) * g.RT + rt) + (in_unit > 0 ? in_unit : 0);
+  const long long real_hi = __shfl_sync(3u, real, 1);
   if (lane == 0) {
+    m->tiles = (int)(real_hi - real);
     m->b = b;
     m->h = h;
     m->rt = rt;
     m->at = begin;
   } else {
     const int t1 = g.T - rt * g.c < g.c ? g.T : (rt + 1) * g.c;
-    const long long end = begin + r.nh + (r.w + t1 + TILE - 1) / TILE;
-    a.splits[blockIdx.x] = make_int4(b, h, rt, begin >= lo && end > hi ? balanced_owner(bl, end - 1) : -1);
+    const long long first = begin + UNIT_COST, end = first + r.nh + (r.w + t1 + TILE - 1) / TILE;
+    a.splits[blockIdx.x] = make_int4(b, h, rt, first >= lo && first < hi && end > hi ? balanced_owner(bl, end - 1) : -1);
   }
 }
 
@@ -651,7 +665,7 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
   const Info* infos = (const Info*)(smem + OFF_INFO);
   const uint32_t tmem = same(misc->tmem), qlo = saddr(smem + OFF_Q) >> 4, blo = saddr(smem + OFF_BUF) >> 4;
   const uint64_t hi = sdesc(0), hi_mn = sdesc_mn(0, REGION);
-  const int total = (int)same((uint32_t)(misc->hi - misc->lo));
+  const int total = (int)same((uint32_t)misc->tiles);
   // of S and of O: tiles done, second row tile's turn, step, ring place and its phase
   struct {
     int tile, half, step, buf, phase;
@@ -661,12 +675,13 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
   auto wait = [&](int bar, uint32_t phase) {
     return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
   };
-  auto learn_s = [&]() -> bool {
+  // What S of the next step needs: waits for it, or (look) only looks.
+  auto learn_s = [&](bool look) -> bool {
     if (s.half) return true;
-    if (!wait(B_FULL + s.buf, s.phase)) return false;
+    if (look ? !__all_sync(0xffffffffu, passed(&bars[B_FULL + s.buf], s.phase)) : !wait(B_FULL + s.buf, s.phase)) return false;
     s.flags = same(infos[s.tile & (NINFO - 1)].flags);
     if (s.flags & F_NEWQ) {
-      if (!wait(B_QFULL, qphase)) return false;
+      if (look ? !__all_sync(0xffffffffu, passed(&bars[B_QFULL], qphase)) : !wait(B_QFULL, qphase)) return false;
       qphase ^= 1;
     }
     return true;
@@ -717,34 +732,34 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
       if (p.buf >= NBUF) p.buf -= NBUF, p.phase ^= 1;
     }
   };
-  // A look at shared memory takes some 250 cycles beside the MMAs, so what a step needs is
-  // looked up before its P is awaited.
+  // S runs up to two steps ahead of O, but waits for K or Q only when there is no O left to
+  // issue: K may need the buffer of a V, and Q's loading may not hold up a unit's end.
+  // A look at shared memory takes some 250 cycles beside the MMAs, so it is taken before
+  // P is awaited where possible.
   bool ok = true;
-  for (int i = 0; i < 2 && ok && s.tile < total; ++i) {
-    ok = learn_s();
-    fence_after();
-    if (ok) scores();
-  }
   while (ok && p.tile < total) {
-    const bool more = s.tile < total;
+    while (s.tile < total && s.step - p.step < 2) {
+      const bool must = s.step == p.step;
+      if (!learn_s(!must)) {
+        ok = !must;
+        break;
+      }
+      fence_after();
+      scores();
+    }
+    if (!ok) break;
     const uint32_t w = p.step & 1, phase = pphase >> w;
     pphase ^= 1u << w;
     ok = learn_p() && wait(B_P + 2 * w, phase);
     if (!ok) break;
     fence_after();
     values(0);
-    // (not awaited: K may need the V that this step frees)
-    const bool known = more && (s.half || (__all_sync(0xffffffffu, passed(&bars[B_FULL + s.buf], s.phase)) && learn_s()));
+    const bool more = s.tile < total && s.step - p.step < 3 && learn_s(true);
     ok = wait(B_P + 2 * w + 1, phase);
     if (!ok) break;
     fence_after();
     values(1);
-    if (more) {
-      ok = known || learn_s();
-      if (!ok) break;
-      if (!known) fence_after();
-      scores();
-    }
+    if (more) scores();
   }
   // all that was issued has ended before the tensor memory is given back
   if (elect()) commit(&bars[B_DRAIN]);
@@ -1070,7 +1085,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
   const int warp = tid >> 5, wg = warp >> 2, row = tid & 127, G = a.cv.G;
   const uint32_t tmem = misc->tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t sa = tmem + S_COL + TILE * wg, oa = tmem + O_COL + TILE * wg;
-  const int total = (int)(misc->hi - misc->lo);
+  const int total = misc->tiles;
   auto wait = [&](int bar, int phase) {
     return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
   };
