@@ -119,12 +119,13 @@ struct Kv8Prefill {
   int4* splits;                    // scratch [grid]: the unit that begins in a CTA's part and ends in a later one's
   float* part;                     // scratch [grid][2][256][PART_STRIDE]: m, l, M, o (oscar_kv8_prefill.cu)
   int B, T, grid, wait_polls;
+  int lg, units;  // log2 of G; units of 256 rows of a (request, kv head) (set by launch_kv8_prefill)
 };
 constexpr int KV8_PREFILL_MAX_GRID = 160;  // CTAs (one per SM) that the scratch has records for
 struct Kv8PrefillScratch {
   size_t off_part, total;
 };
-cudaError_t launch_kv8_prefill(const Kv8Prefill& a, int type, cudaStream_t st, Profiler* prof);
+cudaError_t launch_kv8_prefill(Kv8Prefill a, int type, cudaStream_t st, Profiler* prof);
 Kv8PrefillScratch kv8_prefill_scratch(int grid);
 
 // The largest number of 16 KB units a request may have: the work list counts

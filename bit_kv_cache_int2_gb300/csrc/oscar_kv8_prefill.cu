@@ -16,6 +16,7 @@
 //   8-15  producers, four for keys and four for values: history codes from global memory through registers to FP16
 //         tiles (both code types are exact there), BF16 tokens by cp.async as they
 //         are; K and V tiles alternate in a ring of five
+//   17    goes ahead of them: what a tile is, its scales, pages into the L2
 //   16    the MMAs: S of the step after next is issued behind O of this one, so the
 //         tensor cores work on one row tile while the other's softmax runs
 // Steps (a row tile and a token tile) go to the two softmax groups in turn.  A unit
@@ -44,8 +45,8 @@ using namespace tcgen05;
 
 constexpr int ROWS = 256, TILE = 128;
 constexpr int PROD = 256, SIDE = 128;  // producer threads: 128 for K, 128 for V
-constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 17-19 fill the MMA warp's group up
-// Registers a thread: 256·136 + 256·88 + 128·32 = the 640·96 of the launch.
+constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 18, 19 fill the group up
+// Registers a thread: 256·136 + 256·80 + 128·40, within the 640·96 of the launch.
 constexpr int REGS_SOFTMAX = 136, REGS_PROD = 88, REGS_MMA = 32;
 constexpr int NBUF = 5, REGION = 16384, BUF = 2 * REGION;  // a tile: two regions of 64 channels, [128 rows][128 B]
 constexpr int NINFO = 4, NALPHA = 3, NUNIT = 8;
@@ -94,26 +95,32 @@ constexpr uint32_t idesc(int type, int mn) {
          ((uint32_t)(TILE >> 4) << 24);
 }
 
+extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ uint64_t* barrier(int i) { return (uint64_t*)(smem + OFF_BAR) + i; }
+__device__ __forceinline__ Misc* the_misc() { return (Misc*)(smem + OFF_MISC); }
+
 // ---------------------------------------------------------------- the work list
-// Sum over r = 1 .. n of ceil((w + r c) / 128); c is 32, 64, 128 or 256.
-__device__ __forceinline__ long long tiles_sum(int w, long long n, int c) {
-  const int a = w + TILE - 1;
-  if (c >= TILE) return n * (a / TILE) + (c / TILE) * (n * (n + 1) / 2);
-  const int p = TILE / c, e = a % TILE / c;
-  auto f = [&](long long x) {  // sum of floor(r / p) over r = 1 .. x
-    const long long q = x / p;
-    return p * (q * (q - 1) / 2) + q * (x % p + 1);
-  };
-  return n * (a / TILE) + f(n + e) - f(e);
+// (64-bit divisions take hundreds of cycles, and every CTA begins with these sums.)
+__device__ __forceinline__ long long quotient(long long a, long long b) {  // a >= 0, b > 0
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
+// Sum over r = 1 .. n of ceil((w + r c) / 128), c = 2^lc one of 32, 64, 128, 256.
+__device__ __forceinline__ long long tiles_sum(int w, long long n, int lc) {
+  const int a = w + TILE - 1;
+  if (lc >= 7) return n * (a >> 7) + ((n * (n + 1) / 2) << (lc - 7));
+  const int lp = 7 - lc, e = (a & (TILE - 1)) >> lc;
+  auto f = [&](long long x) {  // sum of floor(r / 2^lp) over r = 1 .. x
+    const long long q = x >> lp;
+    return (q * (q - 1) / 2 << lp) + q * ((x & ((1 << lp) - 1)) + 1);
+  };
+  return n * (a >> 7) + f(n + e) - f(e);
+}
+// Where part i of n begins in a list of W, and whose part place x is in.
+__device__ __forceinline__ long long part_begin(long long W, int n, int i) { return quotient(i * W, n); }
+__device__ __forceinline__ int part_of(long long W, int n, long long x) { return (int)(quotient((x + 1) * n + W - 1, W) - 1); }
 
 // Loading Q and writing the rows takes a unit about as long as so many tiles.
 constexpr int UNIT_COST = 3;
-
-struct Geo {
-  int T, c, RT;  // tokens, tokens of a unit, units of a (request, kv head)
-  __device__ explicit Geo(const Kv8Prefill& a) : T(a.T), c(ROWS / a.cv.G), RT((int)(((long long)a.T * a.cv.G + ROWS - 1) / ROWS)) {}
-};
 
 struct Lens {
   int L, H, nh, w;  // tokens, history; history tiles; BF16 tokens in the cache
@@ -125,44 +132,43 @@ struct Lens {
     w = L - H;
   }
   // Places in the list: a unit has UNIT_COST empty ones and then its tiles.
-  __device__ long long before(const Geo& g, int rt) const { return (long long)rt * (UNIT_COST + nh) + tiles_sum(w, rt, g.c); }
-  __device__ long long per_head(const Geo& g) const {
-    return (long long)g.RT * (UNIT_COST + nh) + tiles_sum(w, g.RT - 1, g.c) + ((long long)w + g.T + TILE - 1) / TILE;
+  __device__ long long before(const Kv8Prefill& a, int rt) const { return (long long)rt * (UNIT_COST + nh) + tiles_sum(w, rt, 8 - a.lg); }
+  __device__ long long per_head(const Kv8Prefill& a) const {
+    return (long long)a.units * (UNIT_COST + nh) + tiles_sum(w, a.units - 1, 8 - a.lg) + ((long long)w + a.T + TILE - 1) / TILE;
   }
 };
 
 // The units of a CTA's part of the list, one after the other.
 struct Walk {
   const Kv8Prefill& a;
-  Geo geo;
   Lens r;
-  long long lo, hi, at;  // the part; where the unit begins
+  int at, len;     // where the unit begins, from the part's begin; the part's length
   int b, h, rt;
   int n, i0, i1;   // the unit's tiles, and those of them in the part
   int t0, t1;      // its tokens
   bool two;        // two row tiles
   __device__ Walk(const Kv8Prefill& args, const Misc* m)
-      : a(args), geo(args), lo(m->lo), hi(m->hi), at(m->at), b(m->b), h(m->h), rt(m->rt) {
+      : a(args), at((int)(m->at - m->lo)), len((int)(m->hi - m->lo)), b(m->b), h(m->h), rt(m->rt) {
     if (more()) {
       r.load(a.cv, b);
       unit();
       if (i0 >= i1) next();
     }
   }
-  __device__ bool more() const { return at < hi; }
+  __device__ bool more() const { return at < len; }
   __device__ void unit() {
-    t0 = rt * geo.c;
-    t1 = geo.T - t0 < geo.c ? geo.T : t0 + geo.c;
-    two = (t1 - t0) * a.cv.G > TILE;
+    t0 = rt << (8 - a.lg);
+    t1 = min(t0 + (ROWS >> a.lg), a.T);
+    two = ((t1 - t0) << a.lg) > TILE;
     n = r.nh + (r.w + t1 + TILE - 1) / TILE;
-    const long long first = at + UNIT_COST;
-    i0 = first < lo ? (int)(lo - first) : 0;
-    i1 = hi - first < n ? (int)(hi - first) : n;
+    const int first = at + UNIT_COST;
+    i0 = max(-first, 0);
+    i1 = min(len - first, n);
   }
   __device__ void next() {  // the next unit with a tile in the part
     do {
       at += UNIT_COST + n;
-      if (++rt == geo.RT) {
+      if (++rt == a.units) {
         rt = 0;
         if (++h == a.cv.Hkv) {
           h = 0;
@@ -181,7 +187,6 @@ struct Walk {
 // one's: request, head, unit and the CTA with its last tile, -1 if there is none.
 // pre: [B] in shared memory.
 __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
-  const Geo g(a);
   const CacheView& cv = a.cv;
   long long W = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -191,7 +196,7 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
       Lens r;
       r.load(cv, b);
       if (!r.ok && blockIdx.x == 0) record_error(cv.err, OSCAR_ERR_STATE);
-      x = r.per_head(g) * cv.Hkv;
+      x = r.per_head(a) * cv.Hkv;
     }
     long long inc = x;
 #pragma unroll
@@ -203,11 +208,9 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     W += __shfl_sync(0xffffffffu, inc, 31);
   }
   __syncwarp();
-  Balanced bl;
-  bl.W = W;
-  bl.n = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
-  const bool any = (int)blockIdx.x < bl.n;
-  const long long lo = any ? balanced_lo(bl, blockIdx.x) : 0, hi = any ? balanced_lo(bl, blockIdx.x + 1) : 0;
+  const int parts = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
+  const bool any = (int)blockIdx.x < parts;
+  const long long lo = any ? part_begin(W, parts, blockIdx.x) : 0, hi = any ? part_begin(W, parts, blockIdx.x + 1) : 0;
   if (lane == 0) {
     m->lo = lo;
     m->hi = hi;
@@ -221,18 +224,18 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
   const int b = balanced_request(pre, a.B, at);
   Lens r;
   r.load(cv, b);
-  const long long per = r.per_head(g), in = at - pre[b];
-  const int h = (int)(in / per);
+  const long long per = r.per_head(a), in = at - pre[b];
+  const int h = (int)quotient(in, per);
   const long long x = in - h * per;
-  int rt = 0, top = g.RT - 1;
+  int rt = 0, top = a.units - 1;
   while (rt < top) {  // the last unit that begins at or before x
     const int mid = (rt + top + 1) >> 1;
-    if (r.before(g, mid) <= x) rt = mid; else top = mid - 1;
+    if (r.before(a, mid) <= x) rt = mid; else top = mid - 1;
   }
-  const long long begin = pre[b] + h * per + r.before(g, rt);
+  const long long begin = pre[b] + h * per + r.before(a, rt);
   // tiles in front of the part, and in front of its end
   const long long in_unit = (lane == 0 ? lo : hi) - begin - UNIT_COST;
-  const long long real = begin - UNIT_COST * (((long long)b * cv.Hkv + h) * g.RT + rt) + (in_unit > 0 ? in_unit : 0);
+  const long long real = begin - UNIT_COST * (((long long)b * cv.Hkv + h) * a.units + rt) + (in_unit > 0 ? in_unit : 0);
   const long long real_hi = __shfl_sync(3u, real, 1);
   if (lane == 0) {
     m->tiles = (int)(real_hi - real);
@@ -241,9 +244,9 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     m->rt = rt;
     m->at = begin;
   } else {
-    const int t1 = g.T - rt * g.c < g.c ? g.T : (rt + 1) * g.c;
+    const int t1 = min((rt + 1) << (8 - a.lg), a.T);
     const long long first = begin + UNIT_COST, end = first + r.nh + (r.w + t1 + TILE - 1) / TILE;
-    a.splits[blockIdx.x] = make_int4(b, h, rt, first >= lo && first < hi && end > hi ? balanced_owner(bl, end - 1) : -1);
+    a.splits[blockIdx.x] = make_int4(b, h, rt, first >= lo && first < hi && end > hi ? part_of(W, parts, end - 1) : -1);
   }
 }
 
@@ -336,6 +339,44 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {  // of either half
   return (uint32_t)((w & 0x7f80u) == 0x7f80u) | (uint32_t)((w & 0x7f800000u) == 0x7f800000u);
 }
 
+// Where a row's 16-byte piece t & 15 stands in Q.
+__device__ __forceinline__ uint32_t q_place(uint32_t q, int t, int row) {
+  const int ch = t & 15;
+  return q + (row >> 7) * BUF + (ch >> 3) * REGION + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4);
+}
+
+// Q, copied as it is, to FP16 in its place, by 256 threads with the pieces that each copied: a
+// row times the power of two that takes its largest finite value to [2^14, 2^15) (not
+// beyond 2^125).  What is lost lies 2^38 below it.  (A call of its own: inlined, it takes
+// registers from the loop behind it.)
+__device__ __forceinline__ void convert_q(uint32_t q, int8_t* al, int t, int rows) {
+#pragma unroll 1
+  for (int row = t >> 4; row < rows; row += 16) {
+    const uint32_t at = q_place(q, t, row);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    uint32_t mx = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = w[j] & 0x7fffu, hi = w[j] >> 16 & 0x7fffu;
+      mx = max(mx, lo < 0x7f80u ? lo : 0u);
+      mx = max(mx, hi < 0x7f80u ? hi : 0u);
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const int e = max((int)(mx >> 7), 16);
+    const float f = pow2i(141 - e);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;\n"
+          : "=r"(o[j])
+          : "f"(__uint_as_float(w[j] & 0xffff0000u) * f), "f"(__uint_as_float(w[j] << 16) * f));
+    st16(at, o[0], o[1], o[2], o[3]);
+    if ((t & 15) == 0) al[row] = (int8_t)(e - 141);
+  }
+}
+
 // Whether a phase is over.
 __device__ __forceinline__ bool passed(uint64_t* bar, uint32_t parity) {
   uint32_t r;
@@ -349,37 +390,41 @@ __device__ __forceinline__ bool passed(uint64_t* bar, uint32_t parity) {
 template <int TYPE>
 struct Producer {
   const Kv8Prefill& a;
-  uint8_t* smem;
-  uint64_t* bars;
-  Misc* misc;
   int t, wp, lane, side;  // thread of 256, warp of its side's four; K: 0, V: 1
   bool ok = true;
-  int gt = 0, qn = 0, un = 0;  // token tiles, loads of Q, units
-  bool told = false;           // this unit is published
-  // Copies under way whose barrier has not been told: at most two.  cut: tokens
-  // from, to of a V tile whose values are zeroed where they are not finite.
+  int gt = 0, qn = 0;  // token tiles, loads of Q
+  // Copies under way whose barrier has not been told: at most two.  from, to: tokens of a V
+  // tile whose values are zeroed where they are not finite.
   struct Pending {
     int bar, buf, from, to;
-  } pend[2];
-  int npend = 0;
+  };
+  struct Copies {
+    Pending p[2];
+    int n = 0;
+  };
 
-  __device__ Producer(const Kv8Prefill& args, uint8_t* s, int tid)
-      : a(args), smem(s), bars((uint64_t*)(s + OFF_BAR)), misc((Misc*)(s + OFF_MISC)), t(tid - PROD0), wp(((tid - PROD0) >> 5) & 3), lane(tid & 31),
+  __device__ Producer(const Kv8Prefill& args, int tid)
+      : a(args), t(tid - PROD0), wp(((tid - PROD0) >> 5) & 3), lane(tid & 31),
         side((int)__shfl_sync(0xffffffffu, (tid - PROD0) / SIDE, 0)) {}
 
   __device__ bool wait(int bar, int phase) {
-    if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
+    if (ok) ok = __all_sync(0xffffffffu, wait_bar(barrier(bar), phase & 1, &the_misc()->abort, a.wait_polls));
     return ok;
   }
+  __device__ bool wait_empty(int item) { return item < NBUF ? ok : wait(B_EMPTY + item % NBUF, item / NBUF - 1); }
   // The MMAs that free a buffer may need copies that nobody has been told of: it does not
   // wait with any.
-  __device__ bool wait_empty(int item) {
-    if (item < NBUF) return ok;
-    const int bar = B_EMPTY + item % NBUF, phase = item / NBUF - 1;
-    if (npend > 0 && !__all_sync(0xffffffffu, passed(&bars[bar], phase & 1))) flush();
-    return wait(bar, phase);
+  __device__ bool wait_empty(int item, Copies& c) {
+    if (c.n > 0 && item >= NBUF && !__all_sync(0xffffffffu, passed(barrier(B_EMPTY + item % NBUF), (item / NBUF - 1) & 1))) flush(c);
+    return wait_empty(item);
   }
 
+  // A full buffer is told by the 128 threads of its side and once more: K by the scout, with
+  // what the tile is, V by its first thread.
+  __device__ void told(int bar) {
+    arrive(barrier(bar));
+    if (t == SIDE && bar < B_FULL + NBUF) arrive(barrier(bar));
+  }
   __device__ void tell(const Pending& p) {
     if (p.from < p.to) {  // this thread's own pieces
 #pragma unroll 1
@@ -397,116 +442,49 @@ struct Producer {
         }
         if (bad) {
           *x = make_uint4(w[0], w[1], w[2], w[3]);
-          *(volatile int*)&misc->bad_v = 1;
+          *(volatile int*)&the_misc()->bad_v = 1;
         }
       }
     }
     fence_proxy_async();
-    arrive(&bars[p.bar]);
+    told(p.bar);
   }
-  __device__ void push(int bar, int buf, int from, int to) {
+  __device__ void push(Copies& c, const Pending& p) {
     copies_commit();
-    if (npend == 2) {
+    if (c.n == 2) {
       copies_wait<2>();
-      tell(pend[0]);
-      pend[0] = pend[1];
-      npend = 1;
+      tell(c.p[0]);
+      c.p[0] = c.p[1];
+      c.n = 1;
     }
-    const Pending p = {bar, buf, from, to};
-    if (npend == 0) pend[0] = p; else pend[1] = p;
-    ++npend;
+    if (c.n == 0) c.p[0] = p; else c.p[1] = p;
+    ++c.n;
   }
-  __device__ void flush() {
+  __device__ void flush(Copies& c) {
     copies_wait<0>();
-    if (npend > 0) tell(pend[0]);
-    if (npend > 1) tell(pend[1]);
-    npend = 0;
-  }
-
-  // With the unit's first tile.  NUNIT: the place's last unit lies six tiles or more behind
-  // the last tile whose O is done, so both softmax groups have left it.
-  __device__ void publish(const Walk& u) {
-    told = true;
-    if (t != 0) return;
-    Unit* x = (Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
-    x->tiles = u.i1 - u.i0;
-    x->hist = max(u.hist_end() - u.i0, 0);
-    const int s0 = (u.line_begin() - u.r.nh) * TILE;
-    x->line = u.r.w + u.t0 + 1 - s0;
-    const bool begins = u.i0 == 0, ends = u.i1 == u.n;
-    x->flags = (u.two ? U_TWO : 0) | (begins ? U_BEGINS : 0) | (ends ? U_ENDS : 0);
-    x->b = u.b, x->h = u.h, x->t0 = u.t0, x->t1 = u.t1;
-    x->c0 = s0 - u.r.w, x->c1 = (u.i1 - u.r.nh) * TILE - u.r.w;
-  }
-  // Lanes 0 and 1 of the K warps: blocks 2 wp, 2 wp + 1 of the tile.
-  __device__ void info(const Walk& u, float2 cs, int mark, uint32_t flags) {
-    if (!told) publish(u);
-    Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
-    if (lane < 2) {
-      f->cs[2 * wp + lane] = cs;
-      f->marks[2 * wp + lane] = (uint8_t)mark;
-    }
-    if (t == 0) f->flags = flags;
-    __syncwarp();
-    if (lane == 0) arrive(&bars[B_INFO + (gt & (NINFO - 1))]);
+    if (c.n > 0) tell(c.p[0]);
+    if (c.n > 1) tell(c.p[1]);
+    c.n = 0;
   }
 
   // Rows of the unit, 16 lanes a row: token and head of row i, 16-byte piece t & 15.
   __device__ const uint4* q_piece(const Walk& u, int row, bool& on) const {
-    const int G = a.cv.G, tok = u.t0 + row / G;
+    const int G = a.cv.G, tok = u.t0 + (row >> a.lg);
     on = tok < u.t1;
-    return (const uint4*)(a.q + (((size_t)u.b * u.geo.T + (on ? tok : u.t0)) * a.cv.Hq + u.h * G + (on ? row % G : 0)) * D) + (t & 15);
+    return (const uint4*)(a.q + (((size_t)u.b * a.T + (on ? tok : u.t0)) * a.cv.Hq + u.h * G + (on ? row & (G - 1) : 0)) * D) + (t & 15);
   }
-  __device__ uint32_t q_place(int row) const {
-    const int ch = t & 15;
-    return saddr(smem + OFF_Q) + (row >> 7) * BUF + (ch >> 3) * REGION + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4);
-  }
-
-  // Q in FP16, each row times the power of two that takes its largest finite value to
-  // [2^14, 2^15) (not beyond 2^125): what is lost lies 2^38 below it.
-  __device__ void load_q16(const Walk& u) {
-    if (qn > 0 && !wait(B_QEMPTY, qn - 1)) return;
-    int8_t* al = (int8_t*)(smem + OFF_ALPHA) + qn % NALPHA * ROWS;
+  // The unit's rows of Q on their way to their places, as they are.
+  __device__ bool copy_q(const Walk& u) {
+    if (qn > 0 && !wait(B_QEMPTY, qn - 1)) return false;
     const int rows = u.two ? ROWS : TILE;
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 64) {
-      uint4 x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bool on;
-        const uint4* p = q_piece(u, r0 + 16 * i + (t >> 4), on);
-        x[i] = on ? *p : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + 16 * i + (t >> 4);
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = w[j] & 0x7fffu, hi = w[j] >> 16 & 0x7fffu;
-          mx = max(mx, lo < 0x7f80u ? lo : 0u);
-          mx = max(mx, hi < 0x7f80u ? hi : 0u);
-        }
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const int e = max((int)(mx >> 7), 16);
-        const float f = pow2i(141 - e);
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;\n"
-              : "=r"(o[j])
-              : "f"(__uint_as_float(w[j] & 0xffff0000u) * f), "f"(__uint_as_float(w[j] << 16) * f));
-        st16(q_place(row), o[0], o[1], o[2], o[3]);
-        if ((t & 15) == 0) al[row] = (int8_t)(e - 141);
-      }
+#pragma unroll 4
+    for (int row = t >> 4; row < rows; row += 16) {
+      bool on;
+      const uint4* p = q_piece(u, row, on);
+      copy16(q_place(saddr(smem + OFF_Q), t, row), p, on);
     }
-    ++qn;
-    fence_proxy_async();
-    arrive(&bars[B_QFULL]);
+    return true;
   }
-
   // The history's tiles, one side of them.  A warp has blocks 2 wp, 2 wp + 1, its lanes their
   // codes of the next tile in registers.
   template <int S>
@@ -517,50 +495,35 @@ struct Producer {
     const int last_page = (u.r.H - 1) / PAGE;
     const uint8_t* head = kv8_head(cv, 0, u.h);  // in page 0
     Codes c[2];
-    float2 sc = make_float2(0.f, 0.f);
     // The entry of the page with the warp's blocks of tile i (any entry, where there are none).  It
     // is looked at a tile later: what is made of a load at once takes its time.
     auto entry = [&](int i) { return pages[min(2 * i + (wp >> 1), last_page)]; };
     auto good = [&](int id, int i) {
       if (i >= end || 8 * i + 2 * wp >= blocks) return -1;
-      if (id >= 0 && id < cv.num_pages) return id;
-      if (S == 0 && lane == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
-      return -1;
+      return id >= 0 && id < cv.num_pages ? id : -1;
     };
     auto there = [&](int pid, int i, int j) { return pid >= 0 && 8 * i + 2 * wp + j < blocks; };
     auto load = [&](int pid, int i, int j) {
       load_codes<S>(c[j], head + (pid < 0 ? 0 : (size_t)pid * cv.page_bytes) + (sub + j) * KV8_BLOCK_BYTES, there(pid, i, j), lane);
     };
-    auto scales = [&](int pid, int i) {
-      if (S == 0 && lane < 2 && there(pid, i, lane))
-        sc = __ldcg((const float2*)(head + (size_t)pid * cv.page_bytes + KV8_OFF_SCALES) + sub + lane);
-    };
-    // The page of tile i into the L2, by one lane for each page: the registers have room for
-    // one tile, the memory takes longer than one.
-    auto fetch = [&](int pid) {
-      if (S == 0 && pid >= 0 && !(wp & 1) && lane == 0) bulk_prefetch_l2(head + (size_t)pid * cv.page_bytes, KV8_HEAD_BYTES);
-    };
     int now = good(entry(u.i0), u.i0), next = entry(u.i0 + 1), far = entry(u.i0 + 2);
+    if (!copy_q(u)) return;
+    copies_commit();
     load(now, u.i0, 0);
     load(now, u.i0, 1);
-    scales(now, u.i0);
     next = good(next, u.i0 + 1);
-    fetch(next);
-    load_q16(u);
+    copies_wait<0>();
+    convert_q(saddr(smem + OFF_Q), (int8_t*)(smem + OFF_ALPHA) + qn % NALPHA * ROWS, t, u.two ? ROWS : TILE);
+    ++qn;
+    fence_proxy_async();
+    arrive(barrier(B_QFULL));
     const uint32_t base = saddr(smem + OFF_BUF);
 #pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
       const int after = far, item = 2 * gt + S, buf = item % NBUF;
       far = entry(i + 3);
       const int ahead = good(after, i + 2);
-      fetch(ahead);
       if (!wait_empty(item)) return;
-      if (S == 0) {
-        const bool on = lane < 2 && there(now, i, lane), bad = on && sc.y != sc.y;
-        info(u, make_float2(sc.x * C0, !on || bad ? 0.f : log2f(sc.y)), !on ? 0 : bad ? 3 : 1,
-             F_HIST | (u.two ? F_TWO : 0) | (i == u.i0 ? F_NEWQ : 0) | (i + 1 == end ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0));
-        scales(next, i + 1);
-      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (S == 0) store_k<TYPE>(base + buf * BUF, c[j], 2 * wp + j, lane);
@@ -568,7 +531,7 @@ struct Producer {
         load(next, i + 1, j);
       }
       fence_proxy_async();
-      arrive(&bars[B_FULL + buf]);
+      told(B_FULL + buf);
       now = next;
       next = ahead;
     }
@@ -578,28 +541,19 @@ struct Producer {
   // (which begins at ring slot H mod 256) or in the chunk.
   __device__ void line(const Walk& u) {
     const CacheView& cv = a.cv;
-    if (qn > 0 && !wait(B_QEMPTY, qn - 1)) return;
-    const int rows = u.two ? ROWS : TILE;
-#pragma unroll 4
-    for (int row = t >> 4; row < rows; row += 16) {
-      bool on;
-      const uint4* p = q_piece(u, row, on);
-      copy16(q_place(row), p, on);
-    }
+    if (!copy_q(u)) return;
     ++qn;
-    push(B_QFULL, 0, 0, 0);
+    Copies copies;
+    push(copies, {B_QFULL, 0, 0, 0});
     const size_t head = (size_t)u.b * cv.Hkv + u.h;
     const int nsink = u.r.L < SINK ? u.r.L : SINK, all = u.r.w + u.t1;
     for (int i = u.line_begin(); i < u.i1 && ok; ++i, ++gt) {
       const int s0 = (i - u.r.nh) * TILE;
       const int item = 2 * gt + side, buf = item % NBUF;
-      if (!wait_empty(item)) return;
-      if (side == 0)
-        info(u, make_float2(C0, 0.f), 1,
-             (u.two ? F_TWO : 0) | (i == u.line_begin() ? F_NEWQ : 0) | (i + 1 == u.i1 ? F_ENDQ | F_ENDU : 0));
+      if (!wait_empty(item, copies)) return;
       const __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
       const __nv_bfloat16* ring = (side ? cv.ring_v : cv.ring_k) + head * RECENT * D;
-      const __nv_bfloat16* fresh = (side ? a.v : a.k) + ((size_t)u.b * u.geo.T * cv.Hkv + u.h) * D;
+      const __nv_bfloat16* fresh = (side ? a.v : a.k) + ((size_t)u.b * a.T * cv.Hkv + u.h) * D;
       const int ch = t & 15;
       const uint32_t to = saddr(smem + OFF_BUF) + buf * BUF + (ch >> 3) * REGION;
 #pragma unroll 4
@@ -613,15 +567,14 @@ struct Producer {
       }
       // tokens that only some of the unit's rows see: chunk tokens behind its first
       const int from = u.r.w + u.t0 + 1 - s0, cut_to = all - s0 < TILE ? all - s0 : TILE;
-      push(B_FULL + buf, buf, side ? (from > 0 ? from : 0) : 0, side ? cut_to : 0);
+      push(copies, {B_FULL + buf, buf, side ? (from > 0 ? from : 0) : 0, side ? cut_to : 0});
     }
-    flush();
+    flush(copies);
   }
 
   __device__ void run() {
-    Walk u(a, misc);
-    for (; u.more() && ok; u.next(), ++un) {
-      told = false;
+    Walk u(a, the_misc());
+    for (; u.more() && ok; u.next()) {
       if (u.i0 < u.hist_end()) {
         if (side == 0) history<0>(u);
         else history<1>(u);
@@ -631,6 +584,74 @@ struct Producer {
     copies_wait<0>();
   }
 };
+
+// One warp goes ahead of the producers: it says what each tile is, makes the scales from the
+// history's, reports bad pages and brings pages into the L2 (the producers' registers
+// have room for one tile, the memory takes longer than one).
+__device__ void scout(const Kv8Prefill& a, int lane) {
+  const CacheView& cv = a.cv;
+  int gt = 0, un = 0;
+  for (Walk u(a, the_misc()); u.more(); u.next(), ++un) {
+    const int end = u.hist_end(), blocks = u.r.H / KV8_BLK, last_page = max(u.r.H - 1, 0) / PAGE;
+    const int32_t* pages = cv.page_table + (size_t)u.b * cv.max_pages_per_req;
+    // lanes 0 - 7: the blocks of a tile
+    auto entry = [&](int i) { return i < end ? pages[min(2 * i + (lane >> 2 & 1), last_page)] : -1; };
+    auto good = [&](int id, int i) {
+      if (i >= end || lane >= 8 || 8 * i + lane >= blocks) return -1;
+      if (id >= 0 && id < cv.num_pages) return id;
+      if ((lane & 3) == 0) record_error(cv.err, id < 0 ? OSCAR_ERR_NO_PAGE : OSCAR_ERR_RANGE);
+      return -1;
+    };
+    auto page = [&](int id) { return kv8_head(cv, id, u.h); };
+    auto scale = [&](int id) {
+      return id >= 0 ? __ldcg((const float2*)(page(id) + KV8_OFF_SCALES) + (lane & 3)) : make_float2(0.f, 0.f);
+    };
+    auto fetch = [&](int id) {
+      if (id >= 0 && (lane & 3) == 0) bulk_prefetch_l2(page(id), KV8_HEAD_BYTES);
+    };
+    int now = good(entry(u.i0), u.i0), next = good(entry(u.i0 + 1), u.i0 + 1), far = entry(u.i0 + 2);
+    float2 sc = scale(now);
+    fetch(next);
+#pragma unroll 1
+    for (int i = u.i0; i < u.i1; ++i, ++gt) {
+      const int item = 2 * gt, buf = item % NBUF;
+      if (item >= NBUF &&
+          !__all_sync(0xffffffffu, wait_bar(barrier(B_EMPTY + buf), (item / NBUF - 1) & 1, &the_misc()->abort, a.wait_polls)))
+        return;
+      if (i == u.i0 && lane == 0) {
+        // NUNIT: the place's last unit lies six tiles or more behind the last tile whose O is
+        // done, so both softmax groups have left it
+        Unit* x = (Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
+        x->tiles = u.i1 - u.i0;
+        x->hist = max(end - u.i0, 0);
+        const int s0 = (u.line_begin() - u.r.nh) * TILE;
+        x->line = u.r.w + u.t0 + 1 - s0;
+        x->flags = (u.two ? U_TWO : 0) | (u.i0 == 0 ? U_BEGINS : 0) | (u.i1 == u.n ? U_ENDS : 0);
+        x->b = u.b, x->h = u.h, x->t0 = u.t0, x->t1 = u.t1;
+        x->c0 = s0 - u.r.w, x->c1 = (u.i1 - u.r.nh) * TILE - u.r.w;
+      }
+      Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
+      const bool hist = i < end, bad = now >= 0 && sc.y != sc.y;
+      if (lane < 8) {
+        f->cs[lane] = !hist ? make_float2(C0, 0.f) : make_float2(sc.x * C0, now < 0 || bad ? 0.f : log2f(sc.y));
+        f->marks[lane] = (uint8_t)(!hist ? 1 : now < 0 ? 0 : bad ? 3 : 1);
+      }
+      if (lane == 0)
+        f->flags = (hist ? F_HIST : 0) | (u.two ? F_TWO : 0) | (i == u.i0 || i == end ? F_NEWQ : 0) |
+                   (i + 1 == end || i + 1 == u.i1 ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0);
+      __syncwarp();
+      if (lane == 0) {
+        arrive(barrier(B_INFO + (gt & (NINFO - 1))));
+        arrive(barrier(B_FULL + buf));
+      }
+      now = next;
+      sc = scale(now);
+      next = good(far, i + 2);
+      fetch(next);
+      far = entry(i + 3);
+    }
+  }
+}
 
 
 // -------------------------------------------------------------------- MMA issue
@@ -659,9 +680,8 @@ __device__ __forceinline__ void values_mma(uint32_t d, uint32_t p, uint32_t v, u
   for (int kk = 0; kk < 4; ++kk) mma_ts(d, p + 8 * kk, desc(v + kk * (2048 >> 4), hi), id, add | kk);  // 64 tokens
 }
 
-__device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
-  uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
-  Misc* misc = (Misc*)(smem + OFF_MISC);
+__device__ void issue(const Kv8Prefill& a) {
+  Misc* misc = the_misc();
   const Info* infos = (const Info*)(smem + OFF_INFO);
   const uint32_t tmem = same(misc->tmem), qlo = saddr(smem + OFF_Q) >> 4, blo = saddr(smem + OFF_BUF) >> 4;
   const uint64_t hi = sdesc(0), hi_mn = sdesc_mn(0, REGION);
@@ -673,15 +693,15 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
   } s = {0, 0, 0, 0, 0, 0}, p = {0, 0, 0, 1, 0, 0};
   uint32_t started = 0, pphase = 0, qphase = 0;
   auto wait = [&](int bar, uint32_t phase) {
-    return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
+    return (bool)__all_sync(0xffffffffu, wait_bar(barrier(bar), phase & 1, &misc->abort, a.wait_polls));
   };
   // What S of the next step needs: waits for it, or (look) only looks.
   auto learn_s = [&](bool look) -> bool {
     if (s.half) return true;
-    if (look ? !__all_sync(0xffffffffu, passed(&bars[B_FULL + s.buf], s.phase)) : !wait(B_FULL + s.buf, s.phase)) return false;
+    if (look ? !__all_sync(0xffffffffu, passed(barrier(B_FULL + s.buf), s.phase)) : !wait(B_FULL + s.buf, s.phase)) return false;
     s.flags = same(infos[s.tile & (NINFO - 1)].flags);
     if (s.flags & F_NEWQ) {
-      if (look ? !__all_sync(0xffffffffu, passed(&bars[B_QFULL], qphase)) : !wait(B_QFULL, qphase)) return false;
+      if (look ? !__all_sync(0xffffffffu, passed(barrier(B_QFULL), qphase)) : !wait(B_QFULL, qphase)) return false;
       qphase ^= 1;
     }
     return true;
@@ -697,9 +717,9 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
     const bool last = !(s.flags & F_TWO) || s.half;  // of the tile's steps
     if (elect()) {
       scores_mma(tmem + S_COL + TILE * w, q, k, hi, s.flags & F_HIST ? idesc(0, 0) : idesc(1, 0));
-      commit(&bars[B_S + w]);
-      if (last) commit(&bars[B_EMPTY + s.buf]);
-      if (last && (s.flags & F_ENDQ)) commit(&bars[B_QEMPTY]);
+      commit(barrier(B_S + w));
+      if (last) commit(barrier(B_EMPTY + s.buf));
+      if (last && (s.flags & F_ENDQ)) commit(barrier(B_QEMPTY));
     }
     __syncwarp();
     ++s.step;
@@ -717,9 +737,9 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
     started |= 1u << w;
     if (elect()) {
       values_mma(tmem + O_COL + TILE * w, tmem + S_COL + TILE * w + 32 * part, v, hi_mn, p.flags & F_HIST ? idesc(0, 1) : idesc(1, 1), add);
-      if (last) commit(&bars[B_EMPTY + p.buf]);
-      if (end && (started & 1)) commit(&bars[B_O]);
-      if (end && (started & 2)) commit(&bars[B_O + 1]);
+      if (last) commit(barrier(B_EMPTY + p.buf));
+      if (end && (started & 1)) commit(barrier(B_O));
+      if (end && (started & 2)) commit(barrier(B_O + 1));
     }
     __syncwarp();
     if (!part) return;
@@ -762,9 +782,9 @@ __device__ void issue(const Kv8Prefill& a, uint8_t* smem) {
     if (more) scores();
   }
   // all that was issued has ended before the tensor memory is given back
-  if (elect()) commit(&bars[B_DRAIN]);
+  if (elect()) commit(barrier(B_DRAIN));
   __syncwarp();
-  mbar_wait(&bars[B_DRAIN], 0);
+  mbar_wait(barrier(B_DRAIN), 0);
 }
 
 // ---------------------------------------------------------------------- softmax
@@ -981,6 +1001,17 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
   tmem_st_wait();
 }
 
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8], bool wide) {
+  if (wide) {  // aligned to 32 bytes
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    ((uint4*)p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    ((uint4*)p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // Adds the values that are not finite of the chunk tokens j0 .. j1 - 1 to a row's channels c0 .. c0 + 31
 // (they were left out of the product: other rows do not see them).
 __device__ __noinline__ void add_bad(const Kv8Prefill& a, int b, int h, int j0, int j1, int c0, float* o) {
@@ -993,19 +1024,27 @@ __device__ __noinline__ void add_bad(const Kv8Prefill& a, int b, int h, int j0, 
   }
 }
 
-__device__ float* record(const Kv8Prefill& a, int cta, int slot, int row) {
-  return a.part + ((size_t)(2 * cta + slot) * ROWS + row) * PART_STRIDE;
-}
+// The record of a unit that is not whole in a part: O by groups of four channels, [32][256]
+// rows (neighbouring lanes have neighbouring rows), then each row's log2 of the sum of
+// exponentials and its M.
+struct Record {
+  float* p;
+  __device__ Record(const Kv8Prefill& a, int cta, int slot) : p(a.part + (size_t)(2 * cta + slot) * ROWS * PART_STRIDE) {}
+  __device__ float4* o(int group, int row) const { return (float4*)p + group * ROWS + row; }
+  __device__ float& lg(int row) const { return p[ROWS * D + row]; }
+  __device__ float& M(int row) const { return p[ROWS * D + ROWS + row]; }
+};
 
 // A row of a unit (lg: its log2 of the sum of exponentials), or its record where the
 // unit is not whole here.  O = g0·[oa] + g1·[ob].
 __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, int row, float lg, float M, uint32_t oa, float g0,
                                           uint32_t ob, float g1, bool bad_v) {
-  const int G = a.cv.G, tok = u->t0 + row / G;
+  const int G = a.cv.G, tok = u->t0 + (row >> a.lg);
   const bool on = tok < u->t1, whole = (u->flags & (U_BEGINS | U_ENDS)) == (U_BEGINS | U_ENDS);
-  const size_t at = ((size_t)u->b * a.T + (on ? tok : u->t0)) * a.cv.Hq + u->h * G + row % G;
-  float* rec = record(a, blockIdx.x, u->flags & U_BEGINS ? 1 : 0, row);
-  const float f = !whole ? 1.f : lg == -INFINITY ? 0.f : ex2(M - lg);  // nothing seen: zeros, and -infinity as the lse
+  const size_t at = ((size_t)u->b * a.T + (on ? tok : u->t0)) * a.cv.Hq + u->h * G + (row & (G - 1));
+  const Record rec(a, blockIdx.x, u->flags & U_BEGINS ? 1 : 0);
+  const bool wide = ((uintptr_t)a.out & 31) == 0;
+  const float f = lg == -INFINITY ? 0.f : ex2(M - lg);  // nothing seen: zeros, and -infinity as the lse
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
@@ -1033,23 +1072,21 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, in
     if (on && !whole) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
-        *(float4*)(rec + PART_O + c + j) = make_float4(o[j] * f, o[j + 1] * f, o[j + 2] * f, o[j + 3] * f);
+        *rec.o((c + j) >> 2, row) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
     } else if (on) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint4 x;
-        x.x = pack2<false>(o[j] * f, o[j + 1] * f);
-        x.y = pack2<false>(o[j + 2] * f, o[j + 3] * f);
-        x.z = pack2<false>(o[j + 4] * f, o[j + 5] * f);
-        x.w = pack2<false>(o[j + 6] * f, o[j + 7] * f);
-        *(uint4*)(a.out + at * D + c + j) = x;
+      for (int j = 0; j < 32; j += 16) {
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = pack2<false>(o[j + 2 * i] * f, o[j + 2 * i + 1] * f);
+        store32(a.out + at * D + c + j, x, wide);
       }
     }
     __syncwarp();
   }
   if (on && !whole) {
-    rec[0] = lg;
-    rec[1] = M;
+    rec.lg(row) = lg;
+    rec.M(row) = M;
   } else if (on && a.lse) {
     a.lse[at] = lg * LN2;
   }
@@ -1061,10 +1098,10 @@ __device__ __noinline__ void abandon(const Kv8Prefill& a, const Misc* m, int un,
   const int G = a.cv.G;
   int i = 0;
   for (Walk u(a, m); u.more(); u.next(), ++i) {
-    const int urow = (u.two ? TILE * wg : 0) + row, tok = u.t0 + urow / G;
+    const int urow = (u.two ? TILE * wg : 0) + row, tok = u.t0 + (urow >> a.lg);
     if (i < un || (!u.two && wg == 1) || tok >= u.t1) continue;
     if (u.i0 > 0 || u.i1 < u.n) {
-      record(a, blockIdx.x, u.i0 == 0 ? 1 : 0, urow)[0] = NAN;
+      Record(a, blockIdx.x, u.i0 == 0 ? 1 : 0).lg(urow) = NAN;
       continue;
     }
     const size_t at = ((size_t)u.b * a.T + tok) * a.cv.Hq + u.h * G + urow % G;
@@ -1079,15 +1116,14 @@ __device__ __forceinline__ float add_logs(float a, float b) {
   return m == -INFINITY ? (a == b ? m : NAN) : m + log2f(ex2(a - m) + ex2(b - m));
 }
 
-__device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
-  uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
-  Misc* misc = (Misc*)(smem + OFF_MISC);
-  const int warp = tid >> 5, wg = warp >> 2, row = tid & 127, G = a.cv.G;
+__device__ void softmax(const Kv8Prefill& a, int tid) {
+  Misc* misc = the_misc();
+  const int warp = tid >> 5, wg = warp >> 2, row = tid & 127;
   const uint32_t tmem = misc->tmem + ((uint32_t)(32 * (warp & 3)) << 16);
   const uint32_t sa = tmem + S_COL + TILE * wg, oa = tmem + O_COL + TILE * wg;
   const int total = misc->tiles;
   auto wait = [&](int bar, int phase) {
-    return (bool)__all_sync(0xffffffffu, wait_bar(&bars[bar], phase & 1, &misc->abort, a.wait_polls));
+    return (bool)__all_sync(0xffffffffu, wait_bar(barrier(bar), phase & 1, &misc->abort, a.wait_polls));
   };
   bool ok = true;
   // token tiles and steps done; this group's S and O so far; exchanges; units, loads of Q
@@ -1097,7 +1133,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
     if (!ok) break;
     const Unit* u = (const Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
     const int tiles = u->tiles, hist = u->hist, two = u->flags & U_TWO;
-    const int urow = (two ? TILE * wg : 0) + row, line = u->line + urow / G;
+    const int urow = (two ? TILE * wg : 0) + row, line = u->line + (urow >> a.lg);
     Row st = {NONE, 0.f, NONE};
     float al = 0.f;
     int cnt = 0;
@@ -1113,7 +1149,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
       auto said = [&]() {
         fence_before();
         __syncwarp();
-        if ((tid & 31) == 0) arrive(&bars[B_P + 2 * wg]);
+        if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg));
       };
       if (i < hist) {
         if (cnt == 0) al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
@@ -1127,7 +1163,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
       }
       fence_before();
       __syncwarp();
-      if ((tid & 31) == 0) arrive(&bars[B_P + 2 * wg + 1]);
+      if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg + 1));
       ++cnt;
     }
     if (ok && cnt > 0) {
@@ -1146,7 +1182,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
         *other = make_float2(lg, cnt > 0 ? st.M : -INFINITY);
         fence_before();
         __syncwarp();
-        if ((tid & 31) == 0) arrive(&bars[B_OTHER]);
+        if ((tid & 31) == 0) arrive(barrier(B_OTHER));
         ok = wait(B_TAKEN, nx);
         if (!ok) break;
       } else {
@@ -1160,7 +1196,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
                   one ? ex2(x.y - M) : 0.f, bad_v);
         fence_before();
         __syncwarp();
-        if ((tid & 31) == 0) arrive(&bars[B_TAKEN]);
+        if ((tid & 31) == 0) arrive(barrier(B_TAKEN));
       }
       ++nx;
     }
@@ -1174,9 +1210,7 @@ __device__ void softmax(const Kv8Prefill& a, uint8_t* smem, int tid) {
 
 template <int TYPE>
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Kv8Prefill a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* bars = (uint64_t*)(smem + OFF_BAR);
-  Misc* misc = (Misc*)(smem + OFF_MISC);
+  Misc* misc = the_misc();
   const int tid = threadIdx.x, warp = (int)same(tid >> 5);
   if (saddr(smem) & 1023) {  // the swizzled tiles begin on 1024 bytes; there is no room to move them
     if (tid == 0) {
@@ -1187,21 +1221,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
   if (tid == 0) {
     for (int i = 0; i < NBUF; ++i) {
-      mbar_init(&bars[B_FULL + i], SIDE);
-      mbar_init(&bars[B_EMPTY + i], 1);
+      mbar_init(barrier(B_FULL + i), SIDE + 1);
+      mbar_init(barrier(B_EMPTY + i), 1);
     }
-    for (int i = 0; i < NINFO; ++i) mbar_init(&bars[B_INFO + i], SIDE / 32);
+    for (int i = 0; i < NINFO; ++i) mbar_init(barrier(B_INFO + i), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[B_S + i], 1);
-      mbar_init(&bars[B_P + 2 * i], 4);
-      mbar_init(&bars[B_P + 2 * i + 1], 4);
-      mbar_init(&bars[B_O + i], 1);
+      mbar_init(barrier(B_S + i), 1);
+      mbar_init(barrier(B_P + 2 * i), 4);
+      mbar_init(barrier(B_P + 2 * i + 1), 4);
+      mbar_init(barrier(B_O + i), 1);
     }
-    mbar_init(&bars[B_QFULL], PROD);
-    mbar_init(&bars[B_QEMPTY], 1);
-    mbar_init(&bars[B_OTHER], 4);
-    mbar_init(&bars[B_TAKEN], 4);
-    mbar_init(&bars[B_DRAIN], 1);
+    mbar_init(barrier(B_QFULL), PROD);
+    mbar_init(barrier(B_QEMPTY), 1);
+    mbar_init(barrier(B_OTHER), 4);
+    mbar_init(barrier(B_TAKEN), 4);
+    mbar_init(barrier(B_DRAIN), 1);
     misc->abort = misc->bad_v = 0;
   }
   if (warp == MMA_WARP) {
@@ -1219,13 +1253,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const uint32_t tmem = misc->tmem;
   if (warp >= MMA_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_MMA));
-    if (warp == MMA_WARP) issue(a, smem);
+    if (warp == MMA_WARP) issue(a);
+    if (warp == MMA_WARP + 1) scout(a, tid & 31);
   } else if (tid >= PROD0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_PROD));
-    Producer<TYPE>(a, smem, tid).run();
+    Producer<TYPE>(a, tid).run();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(REGS_SOFTMAX));
-    softmax(a, smem, tid);
+    softmax(a, tid);
   }
   fence_before();
   __syncthreads();
@@ -1236,44 +1271,48 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
 }
 
-// Joins the records of the unit that begins in part blockIdx.x; a warp per row, a lane
-// per four channels.
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Kv8Prefill a) {
+// Joins the records of the unit that begins in part blockIdx.x, 16 rows a CTA; a thread has
+// four channels of a row.
+constexpr int JOIN_ROWS = 16;
+__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Prefill a) {
+  __shared__ float s[KV8_PREFILL_MAX_GRID][JOIN_ROWS];
   pdl_wait();
   pdl_launch_dependents();
   const int4 d = a.splits[blockIdx.x];
   if (d.w < 0) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), G = a.cv.G;
+  const int r16 = threadIdx.x % JOIN_ROWS, group = threadIdx.x / JOIN_ROWS, row = blockIdx.y * JOIN_ROWS + r16, G = a.cv.G;
   const int tok = d.z * (ROWS / G) + row / G;
-  if (tok >= a.T) return;
+  if (d.z * (ROWS / G) + (int)blockIdx.y * JOIN_ROWS / G >= a.T) return;  // none of the CTA's rows
   const int first = blockIdx.x, n = d.w - first + 1;
+  const bool on = tok < a.T;
+  for (int k = group; k < n; k += 32) s[k][r16] = on ? Record(a, first + k, k == 0).lg(row) : -INFINITY;
+  __syncthreads();
   float m = -INFINITY, L = 0.f;
   bool nan = false;
-  for (int k = lane; k < n; k += 32) {
-    const float x = record(a, first + k, k == 0, row)[0];
-    m = fmaxf(m, x);
-    nan |= x != x;
-  }
-  for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  nan = __any_sync(0xffffffffu, nan);
-  const bool none = m == -INFINITY && !nan;  // nothing seen
-  for (int k = lane; k < n; k += 32) L += ex2(record(a, first + k, k == 0, row)[0] - m);
-  for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-  const float lg = nan ? NAN : none ? -INFINITY : m + log2f(L);
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
   for (int k = 0; k < n; ++k) {
-    const float* r = record(a, first + k, k == 0, row);
-    const float f = none ? 0.f : ex2(r[1] - lg);
-    const float4 x = *(const float4*)(r + PART_O + 4 * lane);
+    m = fmaxf(m, s[k][r16]);
+    nan |= s[k][r16] != s[k][r16];
+  }
+  const bool none = m == -INFINITY;  // nothing seen
+  for (int k = 0; k < n; ++k) L += none ? 0.f : ex2(s[k][r16] - m);
+  const float lg = nan ? NAN : none ? -INFINITY : m + log2f(L);
+  __syncthreads();
+  for (int k = group; k < n; k += 32) s[k][r16] = none && !nan ? 0.f : on ? ex2(Record(a, first + k, k == 0).M(row) - lg) : 0.f;
+  __syncthreads();
+  if (!on) return;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float f = s[k][r16];
+    const float4 x = *Record(a, first + k, k == 0).o(group, row);
     o[0] = fmaf(x.x, f, o[0]);
     o[1] = fmaf(x.y, f, o[1]);
     o[2] = fmaf(x.z, f, o[2]);
     o[3] = fmaf(x.w, f, o[3]);
   }
   const size_t at = ((size_t)d.x * a.T + tok) * a.cv.Hq + d.y * G + row % G;
-  *(uint2*)(a.out + at * D + 4 * lane) = make_uint2(pack2<false>(o[0], o[1]), pack2<false>(o[2], o[3]));
-  if (lane == 0 && a.lse) a.lse[at] = lg * LN2;
+  *(uint2*)(a.out + at * D + 4 * group) = make_uint2(pack2<false>(o[0], o[1]), pack2<false>(o[2], o[3]));
+  if (group == 0 && a.lse) a.lse[at] = lg * LN2;
 }
 
 template <int TYPE>
@@ -1292,13 +1331,16 @@ Kv8PrefillScratch kv8_prefill_scratch(int grid) {
   return s;
 }
 
-cudaError_t launch_kv8_prefill(const Kv8Prefill& a, int type, cudaStream_t st, Profiler* prof) {
+cudaError_t launch_kv8_prefill(Kv8Prefill a, int type, cudaStream_t st, Profiler* prof) {
+  a.lg = 0;
+  while (1 << a.lg < a.cv.G) ++a.lg;
+  a.units = (int)((((long long)a.T << a.lg) + ROWS - 1) / ROWS);
   prof_begin(prof, OSCAR_KERNEL_PREFILL_ATTN, st);
   cudaError_t e = type == OSCAR_KV8_E4M3 ? launch_attend<OSCAR_KV8_E4M3>(a, st) : launch_attend<OSCAR_KV8_INT8>(a, st);
   prof_end(prof, OSCAR_KERNEL_PREFILL_ATTN, st);
   if (e != cudaSuccess) return e;
   prof_begin(prof, OSCAR_KERNEL_PREFILL_MERGE, st);
-  e = launch_pdl(join_kernel, dim3(a.grid, ROWS / 8), dim3(256), 0, st, a);
+  e = launch_pdl(join_kernel, dim3(a.grid, ROWS / JOIN_ROWS), dim3(32 * JOIN_ROWS), 0, st, a);
   prof_end(prof, OSCAR_KERNEL_PREFILL_MERGE, st);
   return e;
 }

@@ -137,8 +137,9 @@ typedef enum {
                                   else up to 4 per CTA of at least 28 pages, balanced at run time */
   OSCAR_OPT_PREFILL_IMPL = 3, /* an oscar_prefill_impl value (default OSCAR_PREFILL_TCGEN05) */
   OSCAR_OPT_WAIT_POLLS = 4,    /* iteration budget of the first wait for each history page of the
-                                  mma.sync and CUDA-core decode kernels, and for each piece of the
-                                  cache in oscar_decode_kv8 (default 4194304 polls).
+                                  mma.sync and CUDA-core decode kernels, for each piece of the cache in
+                                  oscar_decode_kv8 and for each wait of oscar_prefill_kv8 (default
+                                  4194304 polls).
                                   A wait that runs out records OSCAR_ERR_TIMEOUT; the kernel then
                                   waits, with the full budget, for the copies it has in flight and
                                   leaves.  0 makes every such wait give up at once: a way to
