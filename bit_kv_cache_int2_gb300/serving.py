@@ -18,7 +18,9 @@ into a batch:
   (about 3.6x the INT2 bytes at 8-bit accuracy), there optionally with a budget:
   a request whose history exceeds it by 256 tokens loses the blocks that got the
   least attention (``oscar_evict_kv8``), and pages it no longer needs go back to
-  the pool;
+  the pool; with 8-bit history the tokens may also come as a layer's projections,
+  which ``oscar_rope`` turns into queries, keys and values: the prefix is then a
+  prompt that is attended in chunks as it is cached (``oscar_prefill_kv8``);
 * a finished request returns its pages; the last active request moves into
   its slot so the batch stays dense.
 
@@ -183,10 +185,18 @@ class DeviceBackend:
 
     budget (8-bit history only): history tokens a request may keep; the block
     weights decay by `decay` a step.  on_evict(active), if given, runs right
-    before an eviction."""
+    before an eviction.
+
+    rope (8-bit history only): dict(table=oscar.make_rope(..)) and, for heads
+    that are normalised, gamma_q, gamma_k and eps.  Then draw(req) -> the rows of
+    the request's projections, bf16 [prefix + gen][Hq + 2 Hkv][128]: the prefix
+    is a prompt, attended and cached in chunks of prompt_chunk tokens
+    (on_prompt(req, first, out), if given, gets each chunk's attention
+    [T][Hq][128] before the chunk is cached), and a step turns every slot's next
+    row by its position, which an eviction does not change."""
 
     def __init__(self, fmt, ctx, cfg, cache, draw, on_step=None, time_steps=False, max_gen=64, budget=None,
-                 decay=1.0, on_evict=None):
+                 decay=1.0, on_evict=None, rope=None, prompt_chunk=512, on_prompt=None):
         import torch
 
         if fmt not in ("int2", "bf16", *KV8_KINDS):
@@ -194,7 +204,10 @@ class DeviceBackend:
         self.kind = KV8_KINDS.get(fmt)
         if budget is not None and (self.kind is None or budget < 0):
             raise ValueError("a budget needs 8-bit history and is not negative")
+        if rope is not None and (self.kind is None or prompt_chunk < 1):
+            raise ValueError("projections need 8-bit history and chunks of a token or more")
         self.budget, self.on_evict = budget, on_evict
+        self.rope, self.prompt_chunk, self.on_prompt = rope, prompt_chunk, on_prompt
         self.lens = {}  # slot -> [tokens, history tokens] (8-bit history; the device follows the same rule)
         self.kept = {}  # slot -> pages the request holds
         self.weights = None
@@ -206,6 +219,9 @@ class DeviceBackend:
         self.dev = dev
         self.out = torch.empty(B, Hq, 128, dtype=torch.bfloat16, device=dev)
         self.scratch = oscar.alloc_scratch(cfg, dev) if self.kind is None else oscar.alloc_scratch_kv8(cfg, dev)
+        if rope is not None:
+            self.chunk_scratch = oscar.alloc_scratch_kv8(cfg, dev, prefill=True)
+            self.place = torch.zeros(B, dtype=torch.int32, device=dev)  # position of each slot's next token
         self.gen_cap = 0
         self._grow(max_gen)
         self.pos = torch.zeros(B, dtype=torch.long, device=dev)  # next token of each slot
@@ -226,13 +242,16 @@ class DeviceBackend:
         import torch
 
         B, Hq, Hkv = self.cfg.max_batch, self.cfg.num_q_heads, self.cfg.num_kv_heads
-        bufs = (torch.zeros(B, gen, Hkv, 128, dtype=torch.bfloat16, device=self.dev),
-                torch.zeros(B, gen, Hkv, 128, dtype=torch.bfloat16, device=self.dev),
-                torch.zeros(B, gen, Hq, 128, dtype=torch.bfloat16, device=self.dev))
+        heads = (Hkv, Hkv, Hq) if self.rope is None else (Hq + 2 * Hkv,)
+        bufs = [torch.zeros(B, gen, H, 128, dtype=torch.bfloat16, device=self.dev) for H in heads]
         if self.gen_cap:
-            for new, old in zip(bufs, (self.kbuf, self.vbuf, self.qbuf)):
+            for new, old in zip(bufs, self.held):
                 new[:, :self.gen_cap] = old
-        self.kbuf, self.vbuf, self.qbuf = bufs
+        self.held = bufs
+        if self.rope is None:
+            self.kbuf, self.vbuf, self.qbuf = bufs
+        else:
+            self.rows, = bufs
         self.gen_cap = gen
 
     def _view(self, slot):
@@ -246,11 +265,16 @@ class DeviceBackend:
 
         if req.gen > self.gen_cap:
             self._grow(req.gen)
-        K, V, Q = self.draw(req)
         P, n = req.prefix, req.gen
-        self.kbuf[slot, :n] = K[:, P:P + n].permute(1, 0, 2)
-        self.vbuf[slot, :n] = V[:, P:P + n].permute(1, 0, 2)
-        self.qbuf[slot, :n] = Q[:n]
+        if self.rope is not None:
+            rows = self.draw(req)
+            self.rows[slot, :n] = rows[P:P + n]
+            self.place[slot] = 0
+        else:
+            K, V, Q = self.draw(req)
+            self.kbuf[slot, :n] = K[:, P:P + n].permute(1, 0, 2)
+            self.vbuf[slot, :n] = V[:, P:P + n].permute(1, 0, 2)
+            self.qbuf[slot, :n] = Q[:n]
         self.pos[slot] = 0
         row = self.cache["page_table"][slot]
         row.fill_(-1)
@@ -266,14 +290,17 @@ class DeviceBackend:
         self.kept[slot] = len(req.pages)
         if P:
             view = self._view(slot)
-            by_token = self.kind is not None  # [1][P][Hkv][128]; else [1][Hkv][P][128]
-            Kp = (K[:, :P].transpose(0, 1) if by_token else K[:, :P]).unsqueeze(0).contiguous()
-            Vp = (V[:, :P].transpose(0, 1) if by_token else V[:, :P]).unsqueeze(0).contiguous()
+            if self.rope is None:
+                by_token = self.kind is not None  # [1][P][Hkv][128]; else [1][Hkv][P][128]
+                Kp = (K[:, :P].transpose(0, 1) if by_token else K[:, :P]).unsqueeze(0).contiguous()
+                Vp = (V[:, :P].transpose(0, 1) if by_token else V[:, :P]).unsqueeze(0).contiguous()
             if self.import_events is not None:
                 ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
                 ev[0].record()
-            if self.kind is not None:
-                w = self.weights[slot:slot + 1] if self.weights is not None else None
+            w = self.weights[slot:slot + 1] if self.weights is not None else None
+            if self.rope is not None:
+                self._prompt(slot, req, rows, view, w)
+            elif self.kind is not None:
                 oscar.oscar_append_kv8(self.ctx, view, self.kind, Kp, Vp, P, 1, weights=w)
             elif self.fmt == "int2":
                 oscar.oscar_import_tokens(self.ctx, 0, view, Kp, Vp, 1, P)
@@ -283,11 +310,50 @@ class DeviceBackend:
                 ev[1].record()
                 self.import_events.append(ev)
 
+    def _turn(self, rows, place, T, batch):
+        """Queries, keys and values [batch][T][..][128] of projection rows; the first token of each is at `place`."""
+        import torch
+
+        Hq, Hkv, r = self.cfg.num_q_heads, self.cfg.num_kv_heads, self.rope
+        q, k, v = (torch.empty(batch, T, H, 128, dtype=torch.bfloat16, device=self.dev) for H in (Hq, Hkv, Hkv))
+        oscar.oscar_rope(self.ctx, r["table"], rows, place, T, q, k, v, batch, r.get("gamma_q"), r.get("gamma_k"),
+                         r.get("eps", 1e-6))
+        return q, k, v
+
+    def _prompt(self, slot, req, rows, view, weights):
+        """Caches the request's prompt, each chunk after its attention."""
+        import torch
+
+        place = self.place[slot:slot + 1]
+        for at in range(0, req.prefix, self.prompt_chunk):
+            T = min(self.prompt_chunk, req.prefix - at)
+            q, k, v = self._turn(rows[at:at + T].unsqueeze(0), place, T, 1)
+            out = torch.empty_like(q)
+            oscar.oscar_prefill_kv8(self.ctx, view, self.kind, q, k, v, T, out, None, self.chunk_scratch, 1)
+            if self.on_prompt is not None:
+                self.on_prompt(req, at, out[0])
+            oscar.oscar_append_kv8(self.ctx, view, self.kind, k, v, T, 1, weights=weights)
+            place += T
+
+    def export(self, slot):
+        """The cached keys and values of a slot (8-bit history), bf16 [Hkv][n][128] in cache
+        order, as the imports of the other caches take them."""
+        import torch
+
+        if self.kind is None:
+            raise ValueError("only a cache with 8-bit history is read back")
+        n = self.lens[slot][0]
+        K, V = (torch.empty(self.cfg.num_kv_heads, n, 128, dtype=torch.bfloat16, device=self.dev) for _ in range(2))
+        oscar.oscar_read_kv8(self.ctx, self._view(slot), self.kind, 0, n, K, V, 1)
+        return K, V
+
     def move(self, src, dst):
         for key in ("page_table", "sink_k", "sink_v", "ring_k", "ring_v", "seq_lens", "hist_lens"):
             self.cache[key][dst].copy_(self.cache[key][src])
-        for buf in (self.kbuf, self.vbuf, self.qbuf, self.pos):
+        for buf in (*self.held, self.pos):
             buf[dst].copy_(buf[src])
+        if self.rope is not None:
+            self.place[dst].copy_(self.place[src])
         if self.weights is not None:
             self.weights[dst].copy_(self.weights[src])
         self.lens[dst] = self.lens.pop(src)
@@ -298,9 +364,14 @@ class DeviceBackend:
 
         n = len(active)
         sl, ps = self.slots[:n], self.pos[:n]
-        k = self.kbuf[sl, ps]
-        v = self.vbuf[sl, ps]
-        q = self.qbuf[sl, ps]
+        if self.rope is not None:
+            q, k, v = self._turn(self.rows[sl, ps].unsqueeze(1), self.place[:n], 1, n)
+            q = q[:, 0]
+            self.place[:n] += 1
+        else:
+            k = self.kbuf[sl, ps]
+            v = self.vbuf[sl, ps]
+            q = self.qbuf[sl, ps]
         if self.step_events is not None:
             ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
             ev[0].record()

@@ -577,10 +577,125 @@ def test_a_layers_calls_together(kind):
         p.close()
 
 
+@pytest.mark.parametrize("fmt,budget,chunk", [("e4m3", None, 300), ("int8", 320, 77)])
+def test_serving_from_projections(fmt, budget, chunk):
+    """Prompts in chunks and steps from a layer's projections, with requests that move between slots and are
+    evicted from: every output within rounding of the oracle, which is given the GPU's own turned queries and
+    keys; a slot's cache moves to the INT2 format."""
+    from bit_kv_cache_int2_gb300 import serving
+
+    Hkv, G, max_batch, pool_pages = 2, 2, 3, 40
+    kind = serving.KV8_KINDS[fmt]
+    rng = np.random.default_rng(5)
+    reqs = [serving.Request(rid=i, prefix=int(n), gen=int(g)) for i, (n, g) in
+            enumerate(zip(rng.integers(0, 900, 5), rng.integers(5, 280, 5)))]
+    reqs[1].prefix = 0
+
+    def need(prefix, gen):
+        return serving.pages_needed_kv8(prefix, gen, budget=budget)
+
+    mpr = max(need(r.prefix, r.gen) for r in reqs)
+    cfg = oscar.make_config(1, Hkv * G, Hkv, max_batch=max_batch, max_pages_per_req=mpr, num_pages=pool_pages)
+    ctx = oscar.oscar_create(cfg)
+    cache = oscar.alloc_cache(cfg, kv8=True)
+    gam = [(1 + 0.2 * torch.randn(128, generator=torch.Generator().manual_seed(i))).bfloat16().cuda() for i in range(2)]
+    table, w = oscar.make_rope(oscar.ROPE_HALF, 128, 1e4), R.speeds(128, 1e4)
+    streams, held, seen = {}, {}, dict(chunks=0, steps=0, evictions=0, exports=0)
+
+    class View:  # what check_chunk and check_decode look at
+        def __init__(self, rids):
+            self.Hkv, self.G, self.B, self.req = Hkv, G, len(rids), [held[i] for i in rids]
+
+    def draw(req):
+        n = req.prefix + req.gen
+        x = torch.randn(1, n, Hkv * (G + 2), 128, generator=torch.Generator().manual_seed(req.rid)).bfloat16()
+        q, k, v = (torch.empty(n, H, 128, dtype=torch.bfloat16, device="cuda") for H in (Hkv * G, Hkv, Hkv))
+        oscar.oscar_rope(ctx, table, x.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"), n, q, k, v, 1, *gam, eps=1e-6)
+        ref = R.rope(x[0, :, :Hkv * G].double().numpy(), np.arange(n), w, False, gam[0].double().cpu().numpy(), 1e-6)
+        assert np.abs(q.double().cpu().numpy() - ref).max() <= 2.0 ** -7 * np.abs(ref).max()
+        streams[req.rid] = tuple(t.cpu() for t in (q, k, v))
+        held[req.rid] = K8.Request(Hkv, kind)
+        return x[0].cuda()
+
+    def push(rid, t):
+        held[rid].append(*(x[t].double().numpy() for x in streams[rid][1:]))
+
+    def on_prompt(req, first, out):
+        T = len(out)
+        q, k, v = (x[None, first:first + T] for x in streams[req.rid])
+        # the chunk's lse is not asked for here: the oracle's own stands in
+        ref = held[req.rid].chunk(q[0].double().numpy().reshape(T, Hkv, G, 128), k[0].double().numpy(), v[0].double().numpy())
+        check_chunk(View([req.rid]), q, k, v, out[None], torch.from_numpy(ref[1]))
+        for t in range(T):
+            push(req.rid, first + t)
+        seen["chunks"] += 1
+
+    def on_step(active, q, out):
+        for r in active:
+            push(r.rid, r.prefix + r.done)
+        qs = torch.stack([streams[r.rid][0][r.prefix + r.done] for r in active])
+        assert torch.equal(q.cpu(), qs)
+        if seen["steps"] % 16 == 0 or budget is not None:
+            view = View([r.rid for r in active])
+            lse = np.stack([x.attend(y.double().numpy().reshape(Hkv, G, 128))[1] for x, y in zip(view.req, qs)])
+            check_decode(view, qs, out, torch.from_numpy(lse))
+        seen["steps"] += 1
+
+    def on_evict(active):
+        wts = backend.weights.cpu().numpy()
+        for b, r in enumerate(active):
+            held[r.rid].evict(budget, wts[b, :, 16:])
+        seen["evictions"] += 1
+
+    class Backend(serving.DeviceBackend):
+        def step(self, active):
+            super().step(active)
+            if sched.steps % 100 == 2:  # a slot's cache as it is, and into an INT2 cache
+                slot = len(active) - 1
+                K, V = self.export(slot)
+                r = held[active[slot].rid]
+                assert K.shape == V.shape == (Hkv, r.L, 128)
+                for h in range(Hkv):
+                    for got, want in zip((K, V), r.tokens(h)):
+                        assert torch.equal(got[h].cpu(), torch.from_numpy(want).float().bfloat16())
+                pages = max(1, serving.pages_needed(r.L, 0))
+                cfg2 = oscar.make_config(1, Hkv * G, Hkv, max_batch=1, max_pages_per_req=pages, num_pages=pages)
+                ctx2 = oscar.oscar_create(cfg2)
+                try:
+                    c2 = oscar.alloc_cache(cfg2)
+                    c2["page_table"][0] = torch.arange(pages, dtype=torch.int32)
+                    oscar.oscar_import_tokens(ctx2, 0, c2, K[None], V[None], 1, r.L)
+                    torch.cuda.synchronize()
+                    assert oscar.oscar_get_error(ctx2) == 0 and int(c2["seq_lens"][0]) == r.L
+                    assert torch.equal(c2["sink_k"][0, :, :min(64, r.L)], K[:, :64])
+                finally:
+                    oscar.oscar_destroy(ctx2)
+                seen["exports"] += 1
+
+    try:
+        rope = dict(table=table, gamma_q=gam[0], gamma_k=gam[1], eps=1e-6)
+        backend = Backend(fmt, ctx, cfg, cache, draw, on_step=on_step, budget=budget, on_evict=on_evict, rope=rope,
+                          prompt_chunk=chunk, on_prompt=on_prompt, max_gen=8)
+        sched = serving.Scheduler(serving.PagePool(pool_pages), max_batch, backend, mpr, need)
+        for r in reqs:
+            sched.submit(r)
+        done = sched.run()
+        assert oscar.oscar_get_error(ctx) == 0
+        assert sorted(r.rid for r in done) == list(range(len(reqs))) and sched.pool.available == pool_pages
+        assert seen["chunks"] > 4 and seen["exports"] > 0 and (budget is None or seen["evictions"] > 0)
+        with pytest.raises(ValueError):
+            serving.DeviceBackend("bf16", ctx, cfg, cache, draw, rope=rope)
+        with pytest.raises(ValueError):
+            serving.DeviceBackend(fmt, ctx, cfg, cache, draw, rope=rope, prompt_chunk=0)
+    finally:
+        torch.cuda.synchronize()
+        oscar.oscar_destroy(ctx)
+
+
 def test_refusals():
     p = Pair(oscar.KV8_INT8, 2, 2, 2, 4, weights=False)
     try:
-        T, bad = 3, oscar.ERR_INVALID_ARG
+        T, bad = 5, oscar.ERR_INVALID_ARG
         q = torch.zeros(2, T, 4, 128, dtype=torch.bfloat16, device="cuda")
         k = torch.zeros(2, T, 2, 128, dtype=torch.bfloat16, device="cuda")
         out, lse, sc = torch.full_like(q, 5.0), torch.zeros(2, T, 4, device="cuda"), scratch_of(p)
