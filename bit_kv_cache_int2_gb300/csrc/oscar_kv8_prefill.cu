@@ -520,16 +520,17 @@ struct Producer {
     const uint32_t base = saddr(smem + OFF_BUF);
 #pragma unroll 1
     for (int i = u.i0; i < end && ok; ++i, ++gt) {
-      const int after = far, item = 2 * gt + S, buf = item % NBUF;
-      far = entry(i + 3);
-      const int ahead = good(after, i + 2);
+      const int item = 2 * gt + S, buf = item % NBUF;
       if (!wait_empty(item)) return;
+      const int after = far;
+      far = entry(i + 3);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (S == 0) store_k<TYPE>(base + buf * BUF, c[j], 2 * wp + j, lane);
         else store_v<TYPE>(base + buf * BUF, c[j], 2 * wp + j, lane);
         load(next, i + 1, j);
       }
+      const int ahead = good(after, i + 2);
       fence_proxy_async();
       told(B_FULL + buf);
       now = next;
@@ -872,18 +873,18 @@ __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// Tokens of a tile that a row takes: `seen` first ones, and of those the blocks whose mark
+// Tokens of two blocks that a row takes: `seen` first ones, and of those the blocks whose mark
 // (a byte each) says so.  EVERY: all of them.
 struct Taken {
-  uint32_t marks[2];
+  uint32_t marks;
   int seen;
-  __device__ __forceinline__ bool operator()(int b, int j) const { return (marks[b >> 2] >> (8 * (b & 3)) & 1) && 16 * b + j < seen; }
-  __device__ __forceinline__ bool nan(int b) const { return marks[b >> 2] >> (8 * (b & 3)) & 2; }
+  __device__ __forceinline__ bool operator()(int b, int j) const { return (marks >> (8 * b) & 1) && 16 * b + j < seen; }
+  __device__ __forceinline__ bool nan(int b) const { return marks >> (8 * b) & 2; }
 };
 
-// P of block b from its S, and its sum into the state.
+// P of block b of two from its S, to `at`, and its sum into the state.
 template <bool F16, bool EVERY>
-__device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row& st, uint32_t sa, float cb, float lsv, const Taken& taken) {
+__device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row& st, uint32_t at, float cb, float lsv, const Taken& taken) {
   const float shift = max_nan(lsv - st.M, -st.m - FAR);
   const uint64_t cb2 = pair(cb, cb), shift2 = pair(shift, shift);
   uint64_t sum = 0;  // two zeros
@@ -905,7 +906,7 @@ __device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row
   float s0, s1;
   unpair(sum, s0, s1);
   st.l = fmaf(s0 + s1, ex2(-shift - st.m), st.l);
-  tmem_st8(sa + 8 * b, o);
+  tmem_st8(at, o);
 }
 
 // Largest of a block's taken logits, where not all are.
@@ -916,51 +917,39 @@ __device__ __forceinline__ float largest(const uint32_t (&r)[16], int b, const T
   return m;
 }
 
-// P of the tile to tensor memory, in two halves (said: tells of the first), sums into the
-// state.  S of the second half is read twice, as the registers do not hold all of it (and
-// a spilled one goes to the L2 here: shared memory has taken the L1).
+// P of the tile to tensor memory, in two halves (said(i): tells of one), sums into the
+// state.  S is read twice, the registers do not hold all of it.  Two blocks at a time, in loops that
+// are not unrolled: the loops of all roles then fit into the instruction caches together
+// (unrolled, warps stood for instructions as long as for shared memory: 16 requests with
+// 5 tokens 238 -> 228 us, 4 with 509 420 -> 355, a prompt of 8191 636 -> 594, 2048 tokens over
+// 100K 2820 -> 2720).  The largest of the history are found without a loop (with: 2720 -> 2840),
+// and the load behind its last pair is made and thrown away (2770 with a branch; BF16
+// tiles have the branch, without it the prompt takes 635).
 template <bool F16, bool EVERY, typename Said>
-__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, const Taken& taken, bool first, Said said) {
-  uint32_t r[4][16];
-  float mb[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld16_max(sa + 64 + 16 * i, r[i], mb[4 + i]);
+__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, int seen, bool first, Said said) {
+  uint32_t r[2][16];
   const float4* cs = (const float4*)f->cs;
+  const uint16_t* marks = (const uint16_t*)f->marks;
+  float4 sc;
   float mx = NONE, tx = NONE;
-  tmem_ld_wait();
+#pragma unroll (F16 ? 4 : 1)
+  for (int h = 3; h >= 0; --h) {
+    float mb[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) after_wait(r[i]);
-  if (!EVERY)
+    for (int i = 0; i < 2; ++i) tmem_ld16_max(sa + 32 * h + 16 * i, r[i], mb[i]);
+    sc = cs[h];
+    sc.x *= al, sc.z *= al;
+    const Taken taken = {EVERY ? 0u : marks[h], seen - 32 * h};
+    tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mb[4 + i] = largest(r[i], 4 + i, taken);
-  asm volatile("" : "+f"(mb[4]), "+f"(mb[5]), "+f"(mb[6]), "+f"(mb[7])::"memory");
+    for (int i = 0; i < 2; ++i) after_wait(r[i]);
+    if (!EVERY)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) tmem_ld16_max(sa + 16 * i, r[i], mb[i]);
-  float4 sc[2];
-#pragma unroll
-  for (int i = 2; i < 4; ++i) {
-    const float4 c = cs[i];
-    const float y = mb[2 * i] * (c.x * al), z = mb[2 * i + 1] * (c.z * al);
+      for (int i = 0; i < 2; ++i) mb[i] = largest(r[i], i, taken);
+    asm volatile("" : "+f"(mb[0]), "+f"(mb[1])::"memory");
+    const float y = mb[0] * sc.x, z = mb[1] * sc.z;
     mx = max3(mx, y, z);
-    tx = max3(tx, y + c.y, z + c.w);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sc[i] = cs[i];
-    sc[i].x *= al, sc[i].z *= al;
-  }
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) after_wait(r[i]);
-  if (!EVERY)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mb[i] = largest(r[i], i, taken);
-  asm volatile("" : "+f"(mb[0]), "+f"(mb[1]), "+f"(mb[2]), "+f"(mb[3])::"memory");
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float y = mb[2 * i] * sc[i].x, z = mb[2 * i + 1] * sc[i].z;
-    mx = max3(mx, y, z);
-    tx = max3(tx, y + sc[i].y, z + sc[i].w);
+    tx = max3(tx, y + sc.y, z + sc.w);
   }
   const float mn = fmaxf(st.m, mx);
   st.l *= ex2(st.m - mn);
@@ -980,25 +969,25 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
       tmem_st16(oa + c, v);
     }
   }
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    const Taken taken = {EVERY ? 0u : marks[h], seen - 32 * h};
+    const float4 nc = cs[(h + 1) & 3];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    exponentials<F16, EVERY>(r[b], b, st, sa, b & 1 ? sc[b >> 1].z : sc[b >> 1].x, b & 1 ? sc[b >> 1].w : sc[b >> 1].y, taken);
-    tmem_ld16_async(sa + 64 + 16 * b, r[b]);
+    for (int b = 0; b < 2; ++b) {
+      exponentials<F16, EVERY>(r[b], b, st, sa + 16 * h + 8 * b, b ? sc.z : sc.x, b ? sc.w : sc.y, taken);
+      if (F16 || h < 3) tmem_ld16_async(sa + 32 * ((h + 1) & 3) + 16 * b, r[b]);
+    }
+    sc = nc;
+    sc.x *= al, sc.z *= al;
+    if (h & 1) {
+      tmem_st_wait();
+      said(h >> 1);
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) after_wait(r[b]);
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sc[i] = cs[2 + i];
-    sc[i].x *= al, sc[i].z *= al;
-  }
-  tmem_st_wait();
-  said();
-  tmem_ld_wait();
-#pragma unroll
-  for (int b = 0; b < 4; ++b) after_wait(r[b]);
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    exponentials<F16, EVERY>(r[b], 4 + b, st, sa, b & 1 ? sc[b >> 1].z : sc[b >> 1].x, b & 1 ? sc[b >> 1].w : sc[b >> 1].y, taken);
-  tmem_st_wait();
 }
 
 __device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8], bool wide) {
@@ -1134,6 +1123,9 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
     const Unit* u = (const Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
     const int tiles = u->tiles, hist = u->hist, two = u->flags & U_TWO;
     const int urow = (two ? TILE * wg : 0) + row, line = u->line + (urow >> a.lg);
+    // What O has in rows behind the unit's last token is not written: a warp that has no other
+    // rows leaves its P as it is (16 requests with 5 tokens: 229 -> 200 us).
+    const bool rows = __any_sync(0xffffffffu, u->t0 + (urow >> a.lg) < u->t1);
     Row st = {NONE, 0.f, NONE};
     float al = 0.f;
     int cnt = 0;
@@ -1146,24 +1138,23 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
       ++ns;
       fence_after();
       const Info* f = (const Info*)(smem + OFF_INFO) + (tile & (NINFO - 1));
-      auto said = [&]() {
+      auto said = [&](int h) {
         fence_before();
         __syncwarp();
-        if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg));
+        if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg + h));
       };
-      if (i < hist) {
+      if (!rows) {
+        if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg)), arrive(barrier(B_P + 2 * wg + 1));
+      } else if (i < hist) {
         if (cnt == 0) al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
-        const Taken taken = {{((const uint32_t*)f->marks)[0], ((const uint32_t*)f->marks)[1]}, TILE};
-        if (taken.marks[0] == ALL_COUNT && taken.marks[1] == ALL_COUNT) weigh<true, true>(st, sa, oa, f, al, taken, cnt == 0, said);
-        else weigh<true, false>(st, sa, oa, f, al, taken, cnt == 0, said);
+        const uint32_t* marks = (const uint32_t*)f->marks;
+        if (marks[0] == ALL_COUNT && marks[1] == ALL_COUNT) weigh<true, true>(st, sa, oa, f, al, TILE, cnt == 0, said);
+        else weigh<true, false>(st, sa, oa, f, al, TILE, cnt == 0, said);
       } else {
-        const Taken taken = {{ALL_COUNT, ALL_COUNT}, line - (i - hist) * TILE};
-        if (__all_sync(0xffffffffu, taken.seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, taken, cnt == 0, said);
-        else weigh<false, false>(st, sa, oa, f, 1.f, taken, cnt == 0, said);
+        const int seen = line - (i - hist) * TILE;
+        if (__all_sync(0xffffffffu, seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, seen, cnt == 0, said);
+        else weigh<false, false>(st, sa, oa, f, 1.f, seen, cnt == 0, said);
       }
-      fence_before();
-      __syncwarp();
-      if ((tid & 31) == 0) arrive(barrier(B_P + 2 * wg + 1));
       ++cnt;
     }
     if (ok && cnt > 0) {
@@ -1175,7 +1166,7 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
     float lg = st.l == 0.f ? -INFINITY : st.m + log2f(st.l);
     if (!ok) break;
     if (two) {
-      write_row(a, u, urow, lg, st.M, oa, 1.f, 0, 0.f, bad_v);
+      if (rows) write_row(a, u, urow, lg, st.M, oa, 1.f, 0, 0.f, bad_v);
     } else {
       float2* other = (float2*)(smem + OFF_XCH) + row;
       if (wg == 1) {
@@ -1192,7 +1183,7 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
         const float2 x = *other;
         const bool one = x.y != -INFINITY;  // the other group had a tile
         const float M = cnt > 0 ? fmaxf(st.M, x.y) : x.y;
-        write_row(a, u, urow, add_logs(lg, x.x), M, oa, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
+        if (rows) write_row(a, u, urow, add_logs(lg, x.x), M, oa, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
                   one ? ex2(x.y - M) : 0.f, bad_v);
         fence_before();
         __syncwarp();
