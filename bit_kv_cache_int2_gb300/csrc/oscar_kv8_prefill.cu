@@ -123,18 +123,19 @@ __device__ __forceinline__ int part_of(long long W, int n, long long x) { return
 constexpr int UNIT_COST = 3;
 
 struct Lens {
-  int L, H, nh, w;  // tokens, history; history tiles; BF16 tokens in the cache
+  int L, H;  // tokens, history
   bool ok;
   __device__ void load(const CacheView& cv, int b) {
     const Kv8Req r = kv8_req(cv, b);
     L = r.L, H = r.H, ok = r.ok;
-    nh = (H + TILE - 1) / TILE;
-    w = L - H;
   }
+  // (Not kept: the producers have no register to spare.)
+  __device__ int nh() const { return (H + TILE - 1) / TILE; }  // history tiles
+  __device__ int w() const { return L - H; }                   // BF16 tokens in the cache
   // Places in the list: a unit has UNIT_COST empty ones and then its tiles.
-  __device__ long long before(const Kv8Prefill& a, int rt) const { return (long long)rt * (UNIT_COST + nh) + tiles_sum(w, rt, 8 - a.lg); }
+  __device__ long long before(const Kv8Prefill& a, int rt) const { return (long long)rt * (UNIT_COST + nh()) + tiles_sum(w(), rt, 8 - a.lg); }
   __device__ long long per_head(const Kv8Prefill& a) const {
-    return (long long)a.units * (UNIT_COST + nh) + tiles_sum(w, a.units - 1, 8 - a.lg) + ((long long)w + a.T + TILE - 1) / TILE;
+    return (long long)a.units * (UNIT_COST + nh()) + tiles_sum(w(), a.units - 1, 8 - a.lg) + ((long long)w() + a.T + TILE - 1) / TILE;
   }
 };
 
@@ -145,8 +146,6 @@ struct Walk {
   int at, len;     // where the unit begins, from the part's begin; the part's length
   int b, h, rt;
   int n, i0, i1;   // the unit's tiles, and those of them in the part
-  int t0, t1;      // its tokens
-  bool two;        // two row tiles
   __device__ Walk(const Kv8Prefill& args, const Misc* m)
       : a(args), at((int)(m->at - m->lo)), len((int)(m->hi - m->lo)), b(m->b), h(m->h), rt(m->rt) {
     if (more()) {
@@ -156,11 +155,11 @@ struct Walk {
     }
   }
   __device__ bool more() const { return at < len; }
+  __device__ int t0() const { return rt << (8 - a.lg); }  // its tokens t0 .. t1 - 1
+  __device__ int t1() const { return min(t0() + (ROWS >> a.lg), a.T); }
+  __device__ bool two() const { return ((t1() - t0()) << a.lg) > TILE; }  // two row tiles
   __device__ void unit() {
-    t0 = rt << (8 - a.lg);
-    t1 = min(t0 + (ROWS >> a.lg), a.T);
-    two = ((t1 - t0) << a.lg) > TILE;
-    n = r.nh + (r.w + t1 + TILE - 1) / TILE;
+    n = r.nh() + (r.w() + t1() + TILE - 1) / TILE;
     const int first = at + UNIT_COST;
     i0 = max(-first, 0);
     i1 = min(len - first, n);
@@ -179,8 +178,8 @@ struct Walk {
       if (more()) unit();
     } while (more() && i0 >= i1);
   }
-  __device__ int hist_end() const { return i1 < r.nh ? i1 : r.nh; }  // tiles i0 .. here are history
-  __device__ int line_begin() const { return i0 > r.nh ? i0 : r.nh; }
+  __device__ int hist_end() const { return min(i1, r.nh()); }  // tiles i0 .. here are history
+  __device__ int line_begin() const { return max(i0, r.nh()); }
 };
 
 // By warp 0: the CTA's part, and (splits) the unit that begins in it and ends in a later
@@ -245,7 +244,7 @@ __device__ void plan(const Kv8Prefill& a, Misc* m, long long* pre, int lane) {
     m->at = begin;
   } else {
     const int t1 = min((rt + 1) << (8 - a.lg), a.T);
-    const long long first = begin + UNIT_COST, end = first + r.nh + (r.w + t1 + TILE - 1) / TILE;
+    const long long first = begin + UNIT_COST, end = first + r.nh() + (r.w() + t1 + TILE - 1) / TILE;
     a.splits[blockIdx.x] = make_int4(b, h, rt, first >= lo && first < hi && end > hi ? part_of(W, parts, end - 1) : -1);
   }
 }
@@ -469,14 +468,14 @@ struct Producer {
 
   // Rows of the unit, 16 lanes a row: token and head of row i, 16-byte piece t & 15.
   __device__ const uint4* q_piece(const Walk& u, int row, bool& on) const {
-    const int G = a.cv.G, tok = u.t0 + (row >> a.lg);
-    on = tok < u.t1;
-    return (const uint4*)(a.q + (((size_t)u.b * a.T + (on ? tok : u.t0)) * a.cv.Hq + u.h * G + (on ? row & (G - 1) : 0)) * D) + (t & 15);
+    const int G = a.cv.G, tok = u.t0() + (row >> a.lg);
+    on = tok < u.t1();
+    return (const uint4*)(a.q + (((size_t)u.b * a.T + (on ? tok : u.t0())) * a.cv.Hq + u.h * G + (on ? row & (G - 1) : 0)) * D) + (t & 15);
   }
   // The unit's rows of Q on their way to their places, as they are.
   __device__ bool copy_q(const Walk& u) {
     if (qn > 0 && !wait(B_QEMPTY, qn - 1)) return false;
-    const int rows = u.two ? ROWS : TILE;
+    const int rows = u.two() ? ROWS : TILE;
 #pragma unroll 4
     for (int row = t >> 4; row < rows; row += 16) {
       bool on;
@@ -513,7 +512,7 @@ struct Producer {
     load(now, u.i0, 1);
     next = good(next, u.i0 + 1);
     copies_wait<0>();
-    convert_q(saddr(smem + OFF_Q), (int8_t*)(smem + OFF_ALPHA) + qn % NALPHA * ROWS, t, u.two ? ROWS : TILE);
+    convert_q(saddr(smem + OFF_Q), (int8_t*)(smem + OFF_ALPHA) + qn % NALPHA * ROWS, t, u.two() ? ROWS : TILE);
     ++qn;
     fence_proxy_async();
     arrive(barrier(B_QFULL));
@@ -547,9 +546,9 @@ struct Producer {
     Copies copies;
     push(copies, {B_QFULL, 0, 0, 0});
     const size_t head = (size_t)u.b * cv.Hkv + u.h;
-    const int nsink = u.r.L < SINK ? u.r.L : SINK, all = u.r.w + u.t1;
+    const int nsink = u.r.L < SINK ? u.r.L : SINK, all = u.r.w() + u.t1();
     for (int i = u.line_begin(); i < u.i1 && ok; ++i, ++gt) {
-      const int s0 = (i - u.r.nh) * TILE;
+      const int s0 = (i - u.r.nh()) * TILE;
       const int item = 2 * gt + side, buf = item % NBUF;
       if (!wait_empty(item, copies)) return;
       const __nv_bfloat16* sink = (side ? cv.sink_v : cv.sink_k) + head * SINK * D;
@@ -562,12 +561,12 @@ struct Producer {
         const int tok = 8 * j + (t % SIDE >> 4), s = s0 + tok;
         const bool on = s < all;
         const __nv_bfloat16* p = s < nsink   ? sink + (size_t)s * D
-                                 : s < u.r.w ? ring + (size_t)((u.r.H + s - nsink) & (RECENT - 1)) * D
-                                             : fresh + (size_t)(on ? s - u.r.w : 0) * cv.Hkv * D;
+                                 : s < u.r.w() ? ring + (size_t)((u.r.H + s - nsink) & (RECENT - 1)) * D
+                                             : fresh + (size_t)(on ? s - u.r.w() : 0) * cv.Hkv * D;
         copy16(to + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4), p + 8 * ch, on);
       }
       // tokens that only some of the unit's rows see: chunk tokens behind its first
-      const int from = u.r.w + u.t0 + 1 - s0, cut_to = all - s0 < TILE ? all - s0 : TILE;
+      const int from = u.r.w() + u.t0() + 1 - s0, cut_to = all - s0 < TILE ? all - s0 : TILE;
       push(copies, {B_FULL + buf, buf, side ? (from > 0 ? from : 0) : 0, side ? cut_to : 0});
     }
     flush(copies);
@@ -625,11 +624,11 @@ __device__ void scout(const Kv8Prefill& a, int lane) {
         Unit* x = (Unit*)(smem + OFF_UNIT) + (un & (NUNIT - 1));
         x->tiles = u.i1 - u.i0;
         x->hist = max(end - u.i0, 0);
-        const int s0 = (u.line_begin() - u.r.nh) * TILE;
-        x->line = u.r.w + u.t0 + 1 - s0;
-        x->flags = (u.two ? U_TWO : 0) | (u.i0 == 0 ? U_BEGINS : 0) | (u.i1 == u.n ? U_ENDS : 0);
-        x->b = u.b, x->h = u.h, x->t0 = u.t0, x->t1 = u.t1;
-        x->c0 = s0 - u.r.w, x->c1 = (u.i1 - u.r.nh) * TILE - u.r.w;
+        const int s0 = (u.line_begin() - u.r.nh()) * TILE;
+        x->line = u.r.w() + u.t0() + 1 - s0;
+        x->flags = (u.two() ? U_TWO : 0) | (u.i0 == 0 ? U_BEGINS : 0) | (u.i1 == u.n ? U_ENDS : 0);
+        x->b = u.b, x->h = u.h, x->t0 = u.t0(), x->t1 = u.t1();
+        x->c0 = s0 - u.r.w(), x->c1 = (u.i1 - u.r.nh()) * TILE - u.r.w();
       }
       Info* f = (Info*)(smem + OFF_INFO) + (gt & (NINFO - 1));
       const bool hist = i < end, bad = now >= 0 && sc.y != sc.y;
@@ -638,7 +637,7 @@ __device__ void scout(const Kv8Prefill& a, int lane) {
         f->marks[lane] = (uint8_t)(!hist ? 1 : now < 0 ? 0 : bad ? 3 : 1);
       }
       if (lane == 0)
-        f->flags = (hist ? F_HIST : 0) | (u.two ? F_TWO : 0) | (i == u.i0 || i == end ? F_NEWQ : 0) |
+        f->flags = (hist ? F_HIST : 0) | (u.two() ? F_TWO : 0) | (i == u.i0 || i == end ? F_NEWQ : 0) |
                    (i + 1 == end || i + 1 == u.i1 ? F_ENDQ : 0) | (i + 1 == u.i1 ? F_ENDU : 0);
       __syncwarp();
       if (lane == 0) {
@@ -882,10 +881,9 @@ struct Taken {
   __device__ __forceinline__ bool nan(int b) const { return marks >> (8 * b) & 2; }
 };
 
-// P of block b of two from its S, to `at`, and its sum into the state.
+// P of block b of two from its S, to `at`; its sum.
 template <bool F16, bool EVERY>
-__device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row& st, uint32_t at, float cb, float lsv, const Taken& taken) {
-  const float shift = max_nan(lsv - st.M, -st.m - FAR);
+__device__ __forceinline__ uint64_t exponentials(const uint32_t (&r)[16], int b, uint32_t at, float cb, float shift, const Taken& taken) {
   const uint64_t cb2 = pair(cb, cb), shift2 = pair(shift, shift);
   uint64_t sum = 0;  // two zeros
   uint32_t o[8];
@@ -903,10 +901,14 @@ __device__ __forceinline__ void exponentials(const uint32_t (&r)[16], int b, Row
     if (!EVERY && taken.nan(b)) y = z = NAN;
     o[j / 2] = pack2<F16>(y, z);
   }
+  tmem_st8(at, o);
+  return sum;
+}
+// Adds a sum of P to the state.
+__device__ __forceinline__ void add_sum(Row& st, uint64_t sum, float shift) {
   float s0, s1;
   unpair(sum, s0, s1);
   st.l = fmaf(s0 + s1, ex2(-shift - st.m), st.l);
-  tmem_st8(at, o);
 }
 
 // Largest of a block's taken logits, where not all are.
@@ -937,9 +939,11 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
     float mb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) tmem_ld16_max(sa + 32 * h + 16 * i, r[i], mb[i]);
-    sc = cs[h];
-    sc.x *= al, sc.z *= al;
-    const Taken taken = {EVERY ? 0u : marks[h], seen - 32 * h};
+    if (F16) {
+      sc = cs[h];
+      sc.x *= al, sc.z *= al;
+    }
+    const Taken taken = {EVERY ? 0u : F16 ? marks[h] : 0x0101u, seen - 32 * h};
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < 2; ++i) after_wait(r[i]);
@@ -947,10 +951,15 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
 #pragma unroll
       for (int i = 0; i < 2; ++i) mb[i] = largest(r[i], i, taken);
     asm volatile("" : "+f"(mb[0]), "+f"(mb[1])::"memory");
-    const float y = mb[0] * sc.x, z = mb[1] * sc.z;
-    mx = max3(mx, y, z);
-    tx = max3(tx, y + sc.y, z + sc.w);
+    if (F16) {
+      const float y = mb[0] * sc.x, z = mb[1] * sc.z;
+      mx = max3(mx, y, z);
+      tx = max3(tx, y + sc.y, z + sc.w);
+    } else {
+      mx = max3(mx, mb[0] * C0, mb[1] * C0);
+    }
   }
+  if (!F16) tx = mx;
   const float mn = fmaxf(st.m, mx);
   st.l *= ex2(st.m - mn);
   st.m = mn;
@@ -969,17 +978,27 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
       tmem_st16(oa + c, v);
     }
   }
+  const float line_shift = max_nan(-st.M, -st.m - FAR);
+  uint64_t sum = 0;
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
-    const Taken taken = {EVERY ? 0u : marks[h], seen - 32 * h};
-    const float4 nc = cs[(h + 1) & 3];
+    const Taken taken = {EVERY ? 0u : F16 ? marks[h] : 0x0101u, seen - 32 * h};
+    float4 nc;
+    if (F16) nc = cs[(h + 1) & 3];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      exponentials<F16, EVERY>(r[b], b, st, sa + 16 * h + 8 * b, b ? sc.z : sc.x, b ? sc.w : sc.y, taken);
+      if (F16) {
+        const float shift = max_nan((b ? sc.w : sc.y) - st.M, -st.m - FAR);
+        add_sum(st, exponentials<F16, EVERY>(r[b], b, sa + 16 * h + 8 * b, b ? sc.z : sc.x, shift, taken), shift);
+      } else {
+        sum = add2(sum, exponentials<F16, EVERY>(r[b], b, sa + 16 * h + 8 * b, C0, line_shift, taken));
+      }
       if (F16 || h < 3) tmem_ld16_async(sa + 32 * ((h + 1) & 3) + 16 * b, r[b]);
     }
-    sc = nc;
-    sc.x *= al, sc.z *= al;
+    if (F16) {
+      sc = nc;
+      sc.x *= al, sc.z *= al;
+    }
     if (h & 1) {
       tmem_st_wait();
       said(h >> 1);
@@ -988,6 +1007,7 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
 #pragma unroll
     for (int b = 0; b < 2; ++b) after_wait(r[b]);
   }
+  if (!F16) add_sum(st, sum, line_shift);
 }
 
 __device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t (&w)[8], bool wide) {
@@ -1087,8 +1107,8 @@ __device__ __noinline__ void abandon(const Kv8Prefill& a, const Misc* m, int un,
   const int G = a.cv.G;
   int i = 0;
   for (Walk u(a, m); u.more(); u.next(), ++i) {
-    const int urow = (u.two ? TILE * wg : 0) + row, tok = u.t0 + (urow >> a.lg);
-    if (i < un || (!u.two && wg == 1) || tok >= u.t1) continue;
+    const int urow = (u.two() ? TILE * wg : 0) + row, tok = u.t0() + (urow >> a.lg);
+    if (i < un || (!u.two() && wg == 1) || tok >= u.t1()) continue;
     if (u.i0 > 0 || u.i1 < u.n) {
       Record(a, blockIdx.x, u.i0 == 0 ? 1 : 0).lg(urow) = NAN;
       continue;
