@@ -7,18 +7,18 @@
 // the BF16 tokens, which are one line: sink, window, chunk.  All tiles of all
 // units, in order, are one list that is cut into equal parts, one for each CTA
 // (one per SM); units that a cut goes through leave partial records, which
-// merge_kernel joins.
+// join_kernel joins.
 //
 // S = Q·K^T and O += P·V are tcgen05.mma with fp32 accumulators in tensor memory
 // (S of each row tile 128 columns, P over the first half of its S, O 128), Q, K, V
 // in shared memory, 128-byte swizzled.  Warps:
 //   0-7   softmax, four for each row tile, a thread per row
-//   8-15  producers, four for keys and four for values: history codes from global memory through registers to FP16
-//         tiles (both code types are exact there), BF16 tokens by cp.async as they
-//         are; K and V tiles alternate in a ring of five
-//   17    goes ahead of them: what a tile is, its scales, pages into the L2
+//   8-15  producers, four for keys and four for values: history codes from global
+//         memory through registers to FP16 tiles (both code types are exact there),
+//         BF16 tokens by cp.async as they are; K and V tiles alternate in a ring of five
 //   16    the MMAs: S of the step after next is issued behind O of this one, so the
 //         tensor cores work on one row tile while the other's softmax runs
+//   17    goes ahead of them all: what a tile is, its scales, pages into the L2
 // Steps (a row tile and a token tile) go to the two softmax groups in turn.  A unit
 // of at most 128 rows has one row tile: then its token tiles go to the groups in
 // turn, each with its own S and O, joined at the end.
@@ -34,6 +34,21 @@
 // their values have): the operands of an MMA have one type, and BF16 values do not
 // fit FP16's range.  Q is FP16 (times a power of two, exact) for the history and is
 // loaded again as BF16 for the rest.
+//
+// What bounds it.  The MMAs of a step take 1024 cycles, the softmax some 1600 to 1900,
+// and each waits for the other's barriers (a look at shared memory takes 250 to 300
+// cycles while MMAs read their operands there: S = Q·K^T takes all of its
+// bandwidth).  Two row tiles in flight hide part of that, tensor memory has no place for a
+// third.  Measured (one GB300, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8
+// heads, 2720 to 2740 us, 1240 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191 541 us,
+// 1020 TFLOP/s of the causal half; 64 tokens over 100K 116 us, 4 x 509 tokens over 0.3K to
+// 9K 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 189 us (3.5 TB/s; the
+// conversion of the codes and the chain S, softmax, O of a tile), 5 tokens over 1K 18 us (two
+// launches, the list, three dependent trips to memory, instructions that are not in the
+// caches).
+//
+// One MMA warp, not one a row tile (prompt 631 -> 584 at the time, but 2048 tokens over 100K
+// 3090 -> 3580).  Token tiles of 128, not 64: an MMA with N = 64 takes as long.
 #include "oscar_kv8.cuh"
 #include "oscar_tcgen05.cuh"
 
@@ -46,7 +61,8 @@ using namespace tcgen05;
 constexpr int ROWS = 256, TILE = 128;
 constexpr int PROD = 256, SIDE = 128;  // producer threads: 128 for K, 128 for V
 constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 18, 19 fill the group up
-// Registers a thread: 256·136 + 256·80 + 128·40, within the 640·96 of the launch.
+// Registers a thread: 256·136 + 256·88 + 128·32 are the 640·96 of the launch.  (128 for the softmax and
+// 96 for the producers: prompt 572 -> 616 us, 2048 tokens over 100K 2745 -> 2800.)
 constexpr int REGS_SOFTMAX = 136, REGS_PROD = 88, REGS_MMA = 32;
 constexpr int NBUF = 5, REGION = 16384, BUF = 2 * REGION;  // a tile: two regions of 64 channels, [128 rows][128 B]
 constexpr int NINFO = 4, NALPHA = 3, NUNIT = 8;
@@ -119,7 +135,8 @@ __device__ __forceinline__ long long tiles_sum(int w, long long n, int lc) {
 __device__ __forceinline__ long long part_begin(long long W, int n, int i) { return quotient(i * W, n); }
 __device__ __forceinline__ int part_of(long long W, int n, long long x) { return (int)(quotient((x + 1) * n + W - 1, W) - 1); }
 
-// Loading Q and writing the rows takes a unit about as long as so many tiles.
+// Loading Q and writing the rows takes a unit about as long as so many tiles.  (4 x 509 tokens
+// over a history / prompt of 8191: with 2 367 / 564 us, 3 348 / 560, 4 346 / 570, 6 341 / 582.)
 constexpr int UNIT_COST = 3;
 
 struct Lens {
@@ -346,8 +363,8 @@ __device__ __forceinline__ uint32_t q_place(uint32_t q, int t, int row) {
 
 // Q, copied as it is, to FP16 in its place, by 256 threads with the pieces that each copied: a
 // row times the power of two that takes its largest finite value to [2^14, 2^15) (not
-// beyond 2^125).  What is lost lies 2^38 below it.  (A call of its own: inlined, it takes
-// registers from the loop behind it.)
+// beyond 2^125).  What is lost lies 2^38 below it.  (Two or four rows at a time take registers
+// from the loop behind it: 16 requests with 5 tokens 188 -> 195 to 213 us.)
 __device__ __forceinline__ void convert_q(uint32_t q, int8_t* al, int t, int rows) {
 #pragma unroll 1
   for (int row = t >> 4; row < rows; row += 16) {
@@ -653,7 +670,6 @@ __device__ void scout(const Kv8Prefill& a, int lane) {
   }
 }
 
-
 // -------------------------------------------------------------------- MMA issue
 // A whole warp, one lane elected for the instructions: with every value the same in
 // all lanes (`same` tells the compiler so) an MMA takes the 64 cycles of its
@@ -754,8 +770,9 @@ __device__ void issue(const Kv8Prefill& a) {
   };
   // S runs up to two steps ahead of O, but waits for K or Q only when there is no O left to
   // issue: K may need the buffer of a V, and Q's loading may not hold up a unit's end.
-  // A look at shared memory takes some 250 cycles beside the MMAs, so it is taken before
-  // P is awaited where possible.
+  // A look at shared memory takes some 250 cycles beside the MMAs, so it is taken before the
+  // second half of P is awaited, where S can follow O at once (4 x 509 tokens 359 -> 354 us, 2048 over
+  // 100K 2790 -> 2735; not in BF16 tiles: prompt 560 -> 541).
   bool ok = true;
   while (ok && p.tile < total) {
     while (s.tile < total && s.step - p.step < 2) {
@@ -774,7 +791,7 @@ __device__ void issue(const Kv8Prefill& a) {
     if (!ok) break;
     fence_after();
     values(0);
-    const bool more = s.tile < total && s.step - p.step < 3 && learn_s(true);
+    const bool more = (p.flags & F_HIST) && s.tile < total && s.step - p.step < 3 && learn_s(true);
     ok = wait(B_P + 2 * w + 1, phase);
     if (!ok) break;
     fence_after();
@@ -1283,7 +1300,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }
 
 // Joins the records of the unit that begins in part blockIdx.x, 16 rows a CTA; a thread has
-// four channels of a row.
+// four channels of a row.  (64 tokens over 100K: 41 MB of records; joining in the last CTA of a unit
+// would need counters that are zero before the call, which the scratch does not have.)
 constexpr int JOIN_ROWS = 16;
 __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Prefill a) {
   __shared__ float s[KV8_PREFILL_MAX_GRID][JOIN_ROWS];

@@ -45,6 +45,9 @@ __device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t* w) {
                : "memory");
 }
 
+// Bound by memory, most of it written (one GB300): 100,000 tokens of 8 kv heads in 94.7 us (90.6 at
+// the measured copy rate), 32 requests with 8K to 32K in 600 (582).  A block a warp, in both orders:
+// its rows are whole 256-byte lines of the output.
 template <int TYPE>
 __global__ void __launch_bounds__(VW * 32) read_kernel(Kv8Read a) {
   pdl_wait();
