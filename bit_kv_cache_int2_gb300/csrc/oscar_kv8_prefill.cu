@@ -16,9 +16,9 @@
 //   8-15  producers, four for keys and four for values: history codes from global
 //         memory through registers to FP16 tiles (both code types are exact there),
 //         BF16 tokens by cp.async as they are; K and V tiles alternate in a ring of five
-//   16    the MMAs: S of the step after next is issued behind O of this one, so the
+//   18    goes ahead of them: what a tile is, its scales, pages into the L2
+//   19    the MMAs: S of the step after next is issued behind O of this one, so the
 //         tensor cores work on one row tile while the other's softmax runs
-//   17    goes ahead of them all: what a tile is, its scales, pages into the L2
 // Steps (a row tile and a token tile) go to the two softmax groups in turn.  A unit
 // of at most 128 rows has one row tile: then its token tiles go to the groups in
 // turn, each with its own S and O, joined at the end.
@@ -42,8 +42,9 @@
 // third.  Measured (one GB300, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8
 // heads, 2720 to 2740 us, 1240 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191 541 us,
 // 1020 TFLOP/s of the causal half; 64 tokens over 100K 116 us, 4 x 509 tokens over 0.3K to
-// 9K 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 189 us (3.5 TB/s; the
-// conversion of the codes and the chain S, softmax, O of a tile), 5 tokens over 1K 18 us (two
+// 9K 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 182 us (3.7 TB/s; the
+// FP16 tiles are written to shared memory and read by MMAs of 128 rows, which with the waits
+// takes most of its cycles), 5 tokens over 1K 18 us (two
 // launches, the list, three dependent trips to memory, instructions that are not in the
 // caches).
 //
@@ -60,7 +61,9 @@ using namespace tcgen05;
 
 constexpr int ROWS = 256, TILE = 128;
 constexpr int PROD = 256, SIDE = 128;  // producer threads: 128 for K, 128 for V
-constexpr int PROD0 = 256, MMA_WARP = 16, THREADS = 640;  // warps 18, 19 fill the group up
+// Warps 16, 17 fill the last group up.  With few rows warps 0 and 4 have all of the softmax: the MMAs
+// are issued on another quarter of the SM (16 requests with 5 tokens 189 -> 182 us).
+constexpr int PROD0 = 256, ISSUE0 = 16, SCOUT_WARP = 18, MMA_WARP = 19, THREADS = 640;
 // Registers a thread: 256·136 + 256·88 + 128·32 are the 640·96 of the launch.  (128 for the softmax and
 // 96 for the producers: prompt 572 -> 616 us, 2048 tokens over 100K 2745 -> 2800.)
 constexpr int REGS_SOFTMAX = 136, REGS_PROD = 88, REGS_MMA = 32;
@@ -1279,10 +1282,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   __syncthreads();
   fence_after();
   const uint32_t tmem = misc->tmem;
-  if (warp >= MMA_WARP) {
+  if (warp >= ISSUE0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_MMA));
     if (warp == MMA_WARP) issue(a);
-    if (warp == MMA_WARP + 1) scout(a, tid & 31);
+    if (warp == SCOUT_WARP) scout(a, tid & 31);
   } else if (tid >= PROD0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(REGS_PROD));
     Producer<TYPE>(a, tid).run();

@@ -600,6 +600,7 @@ oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* we
  * 0..t), one softmax over all of them per (token, query head): a few drafted
  * tokens, a chunk, or a whole prompt over an empty cache.  The chunk is NOT
  * stored: oscar_append_kv8 does that, with the same k and v, afterwards.
+ * Block weights are the decode's alone: this call neither reads nor adds to them.
  *   q    : device bf16 [batch][T][num_q_heads][128]
  *   k, v : device bf16 [batch][T][num_kv_heads][128], the chunk's keys and values
  *   T    : 0 .. 2^24, the same for every request.  With T = 0 or batch = 0 nothing is
