@@ -37,16 +37,15 @@
 //
 // What bounds it.  The MMAs of a step take 1024 cycles, the softmax some 1600 to 1900,
 // and each waits for the other's barriers (a look at shared memory takes 250 to 300
-// cycles while MMAs read their operands there: S = Q·K^T takes all of its
-// bandwidth).  Two row tiles in flight hide part of that, tensor memory has no place for a
-// third.  Measured (one GB300, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8
-// heads, 2720 to 2740 us, 1240 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191 541 us,
-// 1020 TFLOP/s of the causal half; 64 tokens over 100K 115 us, 4 x 509 tokens over 0.3K to
-// 9K 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 182 us (3.7 TB/s; the
-// FP16 tiles are written to shared memory and read by MMAs of 128 rows, which with the waits
-// takes most of its cycles), 5 tokens over 1K 18 us (two
-// launches, the list, three dependent trips to memory, instructions that are not in the
-// caches).
+// cycles while MMAs read their operands there: S = Q·K^T takes all of its bandwidth).
+// Two row tiles in flight hide part of that, tensor memory has no place for a third.
+// Measured (one GB300, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8 heads,
+// 2720 to 2740 us, 1240 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191 541 us, 1020
+// TFLOP/s of the causal half; 64 tokens over 100K 115 us, 4 x 509 tokens over 0.3K to 9K
+// 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 182 us (3.7 TB/s; the FP16
+// tiles are written to shared memory and read by MMAs of 128 rows, which with the waits
+// takes most of its cycles), 5 tokens over 1K 18 us (two launches, the list, three
+// dependent trips to memory, instructions that are not in the caches).
 //
 // One MMA warp, not one a row tile (prompt 631 -> 584 at the time, but 2048 tokens over 100K
 // 3090 -> 3580).  Token tiles of 128, not 64: an MMA with N = 64 takes as long.
@@ -83,8 +82,8 @@ struct Info {
 constexpr uint32_t ALL_COUNT = 0x01010101u;  // four marks
 // What the MMA warp needs to know of a token tile.
 enum { F_HIST = 1, F_TWO = 2, F_NEWQ = 4, F_ENDQ = 8, F_ENDU = 16 };
-// A unit, as the softmax needs it (one producer follows the work list for all: its
-// state does not fit into the registers of a softmax thread).
+// A unit, as the softmax needs it (the scout follows the work list for it: its state does
+// not fit into the registers of a softmax thread).
 struct alignas(16) Unit {
   int tiles, hist;  // its tiles in this part, the first of them history
   int line;         // of the BF16 tokens in its first other tile, those that its first row sees
@@ -1305,7 +1304,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }
 
 // Joins the records of the unit that begins in part blockIdx.x, 16 rows a CTA; a thread has
-// four channels of a row.  (64 tokens over 100K: 41 MB of records; joining in the last CTA of a unit
+// four channels of a row.  (64 tokens over 100K: 20 MB of records, some 5 of 115 us with the launch.  Joining in the last CTA of a unit
 // would need counters that are zero before the call, which the scratch does not have.)
 constexpr int JOIN_ROWS = 16;
 __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Prefill a) {
@@ -1314,6 +1313,10 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Pr
   pdl_launch_dependents();
   const int4 d = a.splits[blockIdx.x];
   if (d.w < 0) return;
+  // (In bounds whatever another call may have put there meanwhile, should two share a scratch.)
+  if (d.w <= (int)blockIdx.x || d.w >= (int)gridDim.x || (unsigned)d.x >= (unsigned)a.B || (unsigned)d.y >= (unsigned)a.cv.Hkv ||
+      (unsigned)d.z >= (unsigned)a.units)
+    return;
   const int r16 = threadIdx.x % JOIN_ROWS, group = threadIdx.x / JOIN_ROWS, row = blockIdx.y * JOIN_ROWS + r16, G = a.cv.G;
   const int tok = d.z * (ROWS / G) + row / G;
   if (d.z * (ROWS / G) + (int)blockIdx.y * JOIN_ROWS / G >= a.T) return;  // none of the CTA's rows

@@ -803,7 +803,9 @@ def alloc_scratch_kv8(cfg: oscar_config, device="cuda", prefill=False):
     oscar_prefill_kv8 (one call at a time)."""
     import torch
 
-    n = lib().oscar_prefill_kv8_scratch_bytes(ctypes.byref(cfg)) if prefill else oscar_layout_kv8(cfg).scratch_bytes
+    n = oscar_layout_kv8(cfg).scratch_bytes  # raises for a configuration without an 8-bit cache
+    if prefill:
+        n = lib().oscar_prefill_kv8_scratch_bytes(ctypes.byref(cfg))
     return torch.empty((n + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 

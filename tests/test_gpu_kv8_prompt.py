@@ -414,6 +414,50 @@ def test_captured_replayed_and_on_two_streams(kind=oscar.KV8_E4M3):
         p.close()
 
 
+def test_two_graphs_at_once(kind=oscar.KV8_INT8):
+    """Two captured passes over one cache (positions, attention, reading back), each with its own scratch,
+    replayed together, equal the same calls alone."""
+    p = Pair(kind, 2, 4, 2, 40, seed=22, weights=False)
+    try:
+        p.append(1700, oracle=False)
+        table = oscar.make_rope(oscar.ROPE_INTERLEAVED, 64, 1e4)
+        pos = torch.tensor([1700, 40], dtype=torch.int32, device="cuda")
+        runs = []
+        for T in (5, 90):
+            x, sc = torch.randn(2, T, 12, 128, generator=p.g).bfloat16().cuda(), scratch_of(p)
+            q, k, v, out = (torch.zeros(2, T, H, 128, dtype=torch.bfloat16, device="cuda") for H in (8, 2, 2, 8))
+            lse = torch.zeros(2, T, 8, device="cuda")
+            K, V = (torch.zeros(2, 2, 600, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+            def run():
+                oscar.oscar_rope(p.ctx, table, x, pos, T, q, k, v, 2)
+                oscar.oscar_prefill_kv8(p.ctx, p.cache, kind, q, k, v, T, out, lse, sc, 2)
+                oscar.oscar_read_kv8(p.ctx, p.cache, kind, 50, 600, K, V, 2)
+
+            run()
+            torch.cuda.synchronize()
+            got = (q, k, v, out, lse, K, V)
+            want = [y.clone() for y in got]
+            st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=st):
+                run()
+            runs.append((st, graph, got, want, (x, sc)))  # a graph reads its input and writes its scratch: held with it
+        for _ in range(6):
+            for _, _, got, _, _ in runs:
+                for y in got:
+                    y.fill_(float("nan"))
+            torch.cuda.synchronize()
+            for st, graph, _, _, _ in runs:
+                with torch.cuda.stream(st):
+                    graph.replay()
+            torch.cuda.synchronize()
+            for _, _, got, want, _ in runs:
+                assert all(torch.equal(y, z) for y, z in zip(got, want))
+        ok(p)
+    finally:
+        p.close()
+
+
 def test_calls_without_a_pause(kind=oscar.KV8_INT8):
     """Chunks, appends and decodes back to back equal the same calls one at a time."""
     runs = []

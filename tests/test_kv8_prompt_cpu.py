@@ -34,6 +34,8 @@ def test_scratch_size(lib):
     cfg = oscar.make_config(1, 32, 8, max_batch=4, max_pages_per_req=100, num_pages=400)
     cfg.head_dim = 64
     assert lib.oscar_prefill_kv8_scratch_bytes(ctypes.byref(cfg)) == 0
+    with pytest.raises(oscar.OscarError):
+        oscar.alloc_scratch_kv8(cfg, "cpu", prefill=True)
 
 
 @pytest.mark.parametrize("kind", [0, 1])
