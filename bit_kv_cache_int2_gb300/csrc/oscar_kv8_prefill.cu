@@ -1304,8 +1304,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }
 
 // Joins the records of the unit that begins in part blockIdx.x, 16 rows a CTA; a thread has
-// four channels of a row.  (64 tokens over 100K: 20 MB of records, some 5 of 115 us with the launch.  Joining in the last CTA of a unit
-// would need counters that are zero before the call, which the scratch does not have.)
+// four channels of a row.  (64 tokens over 100K: 20 MB of records, some 5 of 115 us with the
+// launch.  Joining in the last CTA of a unit would need counters that are zero before the
+// call, which the scratch does not have.)
 constexpr int JOIN_ROWS = 16;
 __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Prefill a) {
   __shared__ float s[KV8_PREFILL_MAX_GRID][JOIN_ROWS];
