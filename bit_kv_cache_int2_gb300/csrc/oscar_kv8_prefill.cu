@@ -1066,7 +1066,9 @@ struct Record {
 };
 
 // A row of a unit (lg: its log2 of the sum of exponentials), or its record where the
-// unit is not whole here.  O = g0·[oa] + g1·[ob].
+// unit is not whole here.  O = g0·[oa] + g1·[ob], either address 0 where there is no such part.  (Addresses are
+// the same for the warp, factors are not: a tensor-memory load is the whole warp's, so no
+// branch around one may look at a row's factor.)
 __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, int row, float lg, float M, uint32_t oa, float g0,
                                           uint32_t ob, float g1, bool bad_v) {
   const int G = a.cv.G, tok = u->t0 + (row >> a.lg);
@@ -1081,7 +1083,7 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, in
 #pragma unroll
     for (int j = 0; j < 32; ++j) o[j] = 0.f;
     uint32_t v[32];
-    if (g0 != 0.f) {
+    if (oa) {
       tmem_ld32(oa + c, v);
       tmem_ld_wait_regs(v);
 #pragma unroll
@@ -1222,9 +1224,9 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
         if (!ok) break;
         fence_after();
         const float2 x = *other;
-        const bool one = x.y != -INFINITY;  // the other group had a tile
+        const bool one = __any_sync(0xffffffffu, x.y != -INFINITY);  // the other group had a tile (the same for all rows)
         const float M = cnt > 0 ? fmaxf(st.M, x.y) : x.y;
-        if (rows) write_row(a, u, urow, add_logs(lg, x.x), M, oa, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
+        if (rows) write_row(a, u, urow, add_logs(lg, x.x), M, cnt > 0 ? oa : 0, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
                   one ? ex2(x.y - M) : 0.f, bad_v);
         fence_before();
         __syncwarp();
