@@ -119,7 +119,9 @@ struct Kv8Prefill {
   int4* splits;                    // scratch [grid]: the unit that begins in a CTA's part and ends in a later one's
   float* part;                     // scratch [grid][2][256][PART_STRIDE]: m, l, M, o (oscar_kv8_prefill.cu)
   int B, T, grid, wait_polls;
-  int lg, units;  // log2 of G; units of 256 rows of a (request, kv head) (set by launch_kv8_prefill)
+  // set by launch_kv8_prefill: log2 of G; units of 256 rows of a (request, kv head); M of BF16 tokens above their logits
+  int lg, units;
+  float room;
 };
 constexpr int KV8_PREFILL_MAX_GRID = 160;  // CTAs (one per SM) that the scratch has records for
 struct Kv8PrefillScratch {

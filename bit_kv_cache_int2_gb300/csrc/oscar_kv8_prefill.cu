@@ -30,10 +30,14 @@
 // Σ of a block's P times 2^(M - log2 s_V - m); a block whose scale is so small
 // that P would underflow (2^-60 below what counts) is taken as larger, P then is
 // 0 in FP16 all the same.  So P keeps 11 bits for whatever counts in O, whatever the
-// scales.  BF16 tokens take the same road with s_V = 1 and P in BF16 (8 bits, as
-// their values have): the operands of an MMA have one type, and BF16 values do not
-// fit FP16's range.  Q is FP16 (times a power of two, exact) for the history and is
-// loaded again as BF16 for the rest.
+// scales.  For BF16 tokens P is BF16 (8 bits, as their values have): the operands
+// of an MMA have one type, and BF16 values do not fit FP16's range.  Their values
+// are taken as they are and may be as large as fp32 goes, so P is kept small
+// instead: M lies `room` above m, P then adds up to 1 or less over all tokens that a row can
+// see, and O stays below the largest value.  (Nothing is lost to that: BF16 reaches
+// 2^-126, a row's largest P is 2^-room, some 2^-23, or at least 2^-32 of that.  A unit with
+// both kinds of token has its O taken to the new M once.)  Q is FP16 (times a power of
+// two, exact) for the history and is loaded again as BF16 for the rest.
 //
 // What bounds it.  The MMAs of a step take 1024 cycles, the softmax some 1600 to 1900,
 // and each waits for the other's barriers (a look at shared memory takes 250 to 300
@@ -106,7 +110,7 @@ static_assert(NBARS * 8 <= 240 && sizeof(Info) == 80 && sizeof(Unit) == 48 && OF
 static_assert(SMEM <= 227 * 1024, "shared memory");
 constexpr int S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float C0 = INV_SQRT_D * LOG2E;
-constexpr float NONE = -1e30f, LAZY = 6.f, HEAD = 8.f, FAR = 60.f;
+constexpr float NONE = -1e30f, LAZY = 6.f, HEAD = 8.f, FAR = 60.f, SPARE = 32.f;
 // D fp32, M = N = 128; operand type 0: FP16, 1: BF16; bit 16: V is MN-major
 constexpr uint32_t idesc(int type, int mn) {
   return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)mn << 16) | ((uint32_t)(TILE >> 3) << 17) |
@@ -949,7 +953,7 @@ __device__ __forceinline__ float largest(const uint32_t (&r)[16], int b, const T
 // and the load behind its last pair is made and thrown away (2770 with a branch; BF16
 // tiles have the branch, without it the prompt takes 635).
 template <bool F16, bool EVERY, typename Said>
-__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, int seen, bool first, Said said) {
+__device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const Info* f, float al, int seen, bool first, float room, Said said) {
   uint32_t r[2][16];
   const float4* cs = (const float4*)f->cs;
   const uint16_t* marks = (const uint16_t*)f->marks;
@@ -980,14 +984,17 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
       mx = max3(mx, mb[0] * C0, mb[1] * C0);
     }
   }
-  if (!F16) tx = mx;
   const float mn = fmaxf(st.m, mx);
   st.l *= ex2(st.m - mn);
   st.m = mn;
+  // M, were it chosen now; BF16 tokens also lower what a history of large values has left
+  const float aim = F16 ? tx - HEAD : mn + room;
+  const bool off = aim > st.M + LAZY || (!F16 && st.M > aim + SPARE);
   if (first) {
-    st.M = tx - HEAD;
-  } else if (__any_sync(0xffffffffu, tx > st.M + (HEAD + LAZY))) {
-    const float Mn = fmaxf(st.M, tx - HEAD), g = ex2(st.M - Mn);
+    st.M = aim;
+  } else if (__any_sync(0xffffffffu, off)) {
+    const float Mn = F16 ? fmaxf(st.M, aim) : off ? aim : st.M;
+    const float g = ex2(0.5f * (st.M - Mn));  // twice: from small scales to BF16 tokens it is 2^-150
     st.M = Mn;
     // S of this step is complete, so is every MMA issued before it: O has all steps before
 #pragma unroll 1
@@ -995,11 +1002,11 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
       uint32_t v[16];
       tmem_ld16(oa + c, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * g);
+      for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * g * g);
       tmem_st16(oa + c, v);
     }
   }
-  const float line_shift = max_nan(-st.M, -st.m - FAR);
+  const float line_shift = -st.M;
   uint64_t sum = 0;
 #pragma unroll 1
   for (int h = 0; h < 4; ++h) {
@@ -1066,11 +1073,11 @@ struct Record {
 };
 
 // A row of a unit (lg: its log2 of the sum of exponentials), or its record where the
-// unit is not whole here.  O = g0·[oa] + g1·[ob], either address 0 where there is no such part.  (Addresses are
+// unit is not whole here.  O = h0²·[oa] + h1²·[ob], either address 0 where there is no such part.  (Addresses are
 // the same for the warp, factors are not: a tensor-memory load is the whole warp's, so no
 // branch around one may look at a row's factor.)
-__device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, int row, float lg, float M, uint32_t oa, float g0,
-                                          uint32_t ob, float g1, bool bad_v) {
+__device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, int row, float lg, float M, uint32_t oa, float h0,
+                                          uint32_t ob, float h1, bool bad_v) {
   const int G = a.cv.G, tok = u->t0 + (row >> a.lg);
   const bool on = tok < u->t1, whole = (u->flags & (U_BEGINS | U_ENDS)) == (U_BEGINS | U_ENDS);
   const size_t at = ((size_t)u->b * a.T + (on ? tok : u->t0)) * a.cv.Hq + u->h * G + (row & (G - 1));
@@ -1087,13 +1094,13 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, in
       tmem_ld32(oa + c, v);
       tmem_ld_wait_regs(v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[j]) * g0;
+      for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(v[j]) * h0 * h0;
     }
     if (ob) {
       tmem_ld32(ob + c, v);
       tmem_ld_wait_regs(v);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(v[j]), g1, o[j]);
+      for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(v[j]) * h1, h1, o[j]);
     }
     if (bad_v && on) {
       float x[32];
@@ -1191,12 +1198,12 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
       } else if (i < hist) {
         if (cnt == 0) al = pow2i(((const int8_t*)(smem + OFF_ALPHA))[qn % NALPHA * ROWS + urow]);
         const uint32_t* marks = (const uint32_t*)f->marks;
-        if (marks[0] == ALL_COUNT && marks[1] == ALL_COUNT) weigh<true, true>(st, sa, oa, f, al, TILE, cnt == 0, said);
-        else weigh<true, false>(st, sa, oa, f, al, TILE, cnt == 0, said);
+        if (marks[0] == ALL_COUNT && marks[1] == ALL_COUNT) weigh<true, true>(st, sa, oa, f, al, TILE, cnt == 0, a.room, said);
+        else weigh<true, false>(st, sa, oa, f, al, TILE, cnt == 0, a.room, said);
       } else {
         const int seen = line - (i - hist) * TILE;
-        if (__all_sync(0xffffffffu, seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, seen, cnt == 0, said);
-        else weigh<false, false>(st, sa, oa, f, 1.f, seen, cnt == 0, said);
+        if (__all_sync(0xffffffffu, seen >= TILE)) weigh<false, true>(st, sa, oa, f, 1.f, seen, cnt == 0, a.room, said);
+        else weigh<false, false>(st, sa, oa, f, 1.f, seen, cnt == 0, a.room, said);
       }
       ++cnt;
     }
@@ -1226,8 +1233,8 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
         const float2 x = *other;
         const bool one = __any_sync(0xffffffffu, x.y != -INFINITY);  // the other group had a tile (the same for all rows)
         const float M = cnt > 0 ? fmaxf(st.M, x.y) : x.y;
-        if (rows) write_row(a, u, urow, add_logs(lg, x.x), M, cnt > 0 ? oa : 0, cnt > 0 ? ex2(st.M - M) : 0.f, one ? oa + TILE : 0,
-                  one ? ex2(x.y - M) : 0.f, bad_v);
+        if (rows) write_row(a, u, urow, add_logs(lg, x.x), M, cnt > 0 ? oa : 0, ex2(0.5f * (st.M - M)), one ? oa + TILE : 0,
+                  ex2(0.5f * (x.y - M)), bad_v);
         fence_before();
         __syncwarp();
         if ((tid & 31) == 0) arrive(barrier(B_TAKEN));
@@ -1375,6 +1382,9 @@ cudaError_t launch_kv8_prefill(Kv8Prefill a, int type, cudaStream_t st, Profiler
   a.lg = 0;
   while (1 << a.lg < a.cv.G) ++a.lg;
   a.units = (int)((((long long)a.T << a.lg) + ROWS - 1) / ROWS);
+  const long long most = SINK + RECENT + (long long)a.cv.max_pages_per_req * PAGE + a.T;  // tokens that a row can see
+  a.room = LAZY;
+  for (long long n = 1; n < most; n *= 2) a.room += 1.f;
   prof_begin(prof, OSCAR_KERNEL_PREFILL_ATTN, st);
   cudaError_t e = type == OSCAR_KV8_E4M3 ? launch_attend<OSCAR_KV8_E4M3>(a, st) : launch_attend<OSCAR_KV8_INT8>(a, st);
   prof_end(prof, OSCAR_KERNEL_PREFILL_ATTN, st);

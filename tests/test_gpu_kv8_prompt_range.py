@@ -71,3 +71,67 @@ def test_rows_that_count_in_some_tiles_only(kind, lead, G, T, L):
         ok(p)
     finally:
         p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("L,T", [(0, 5), (0, 300), (40, 70), (700, 5), (700, 130), (3000, 300)])
+@pytest.mark.parametrize("sizes", [(120, 120, 120, 120), (110, 110, 110, 110), (120, 0, 0, 0), (0, 0, 120, 0), (0, 0, 0, 120), (80, 80, 80, 80)])
+def test_large_values(kind, L, T, sizes):
+    """Finite values give finite rows: near-equal logits of values of one sign add up without an overflow."""
+    for keys, sign in ((0.05, True), (1.0, False)):
+        p = Pair(kind, 2, 4, 1, L // 64 + 2, seed=1, weights=False)
+        try:
+            q, k, v = sized(p, L, T, sizes, keys, sign)
+            out, lse = prefill(p, q, k, v)
+            assert bool(torch.isfinite(out).all())
+            check_chunk_dense(p, q, k, v, out, lse)
+            ok(p)
+        finally:
+            p.close()
+
+
+def test_large_values_of_a_long_prompt(kind=oscar.KV8_INT8):
+    p = Pair(kind, 1, 2, 1, 2, seed=1, weights=False)
+    try:
+        q, k, v = sized(p, 0, 8191, (0, 0, 0, 119), 0.05, True)
+        out, lse = prefill(p, q, k, v)
+        assert bool(torch.isfinite(out).all())
+        check_chunk_dense(p, q, k, v, out, lse)
+        ok(p)
+    finally:
+        p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sizes", [(0, 100, 0, 0), (0, 120, 0, 0), (60, 100, -60, 110), (-60, 110, 0, -60), (110, -60, 60, -60),
+                                   (-60, 0, 110, 0), (0, 100, 100, -60), (60, 0, -60, 120)])
+def test_values_of_sizes_very_far_apart(kind, sizes):
+    """Each row within its own rounding, also where it looks at one region alone, by 2^300."""
+    for (L, T), lead in (((700, 70), 210.0), ((700, 70), 40.0), ((2000, 5), 210.0), ((0, 40), 0.0), ((333, 40), 60.0)):
+        p = Pair(kind, 1, 4, 1, L // 64 + 2, seed=2, weights=False)
+        try:
+            q, k, v = sized(p, L, T, sizes, 0.3, False, lead)
+            out, lse = prefill(p, q, k, v)
+            check_chunk_dense(p, q, k, v, out, lse)
+            ok(p)
+        finally:
+            p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [9, 64])
+@pytest.mark.parametrize("sizes", [(120, 120, 120, 120), (80, 100, 80, 80), (0, 100, 100, -60), (0, 120, 0, 0), (0, 0, 120, 120),
+                                   (100, -60, -60, -60), (-60, -60, 110, 0), (-60, 110, -60, 100)])
+def test_whole_units(kind, T, sizes):
+    """Enough requests for units that one CTA has whole: history and BF16 tokens in one running state."""
+    for keys, sign, lead in ((0.05, True, 0.0), (0.3, False, 210.0), (0.3, False, 40.0)):
+        p = Pair(kind, 8, 4, 38, 12, seed=3, weights=False)
+        try:
+            q, k, v = sized(p, 700, T, sizes, keys, sign, lead)
+            out, lse = prefill(p, q, k, v)
+            assert bool(torch.isfinite(out).all())
+            n = slice(0, 3)
+            check_chunk_dense(p, q[n], k[n], v[n], out[n], lse[n])
+            ok(p)
+        finally:
+            p.close()
