@@ -1083,7 +1083,8 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, in
   const size_t at = ((size_t)u->b * a.T + (on ? tok : u->t0)) * a.cv.Hq + u->h * G + (row & (G - 1));
   const Record rec(a, blockIdx.x, u->flags & U_BEGINS ? 1 : 0);
   const bool wide = ((uintptr_t)a.out & 31) == 0;
-  const float f = lg == -INFINITY ? 0.f : ex2(M - lg);  // nothing seen: zeros, and -infinity as the lse
+  // The factor's root, taken twice: for values of 2^-100 it is below 2^-126.  Nothing seen: zeros, and -infinity as the lse.
+  const float f = lg == -INFINITY ? 0.f : ex2(0.5f * (M - lg));
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
@@ -1117,7 +1118,7 @@ __device__ __forceinline__ void write_row(const Kv8Prefill& a, const Unit* u, in
       for (int j = 0; j < 32; j += 16) {
         uint32_t x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = pack2<false>(o[j + 2 * i] * f, o[j + 2 * i + 1] * f);
+        for (int i = 0; i < 8; ++i) x[i] = pack2<false>(o[j + 2 * i] * f * f, o[j + 2 * i + 1] * f * f);
         store32(a.out + at * D + c + j, x, wide);
       }
     }
@@ -1344,7 +1345,8 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Pr
   for (int k = 0; k < n; ++k) L += none ? 0.f : ex2(s[k][r16] - m);
   const float lg = nan ? NAN : none ? -INFINITY : m + log2f(L);
   __syncthreads();
-  for (int k = group; k < n; k += 32) s[k][r16] = none && !nan ? 0.f : on ? ex2(Record(a, first + k, k == 0).M(row) - lg) : 0.f;
+  for (int k = group; k < n; k += 32)  // roots, taken twice
+    s[k][r16] = none && !nan ? 0.f : on ? ex2(0.5f * (Record(a, first + k, k == 0).M(row) - lg)) : 0.f;
   __syncthreads();
   if (!on) return;
   float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1352,10 +1354,10 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Kv8Pr
   for (int k = 0; k < n; ++k) {
     const float f = s[k][r16];
     const float4 x = *Record(a, first + k, k == 0).o(group, row);
-    o[0] = fmaf(x.x, f, o[0]);
-    o[1] = fmaf(x.y, f, o[1]);
-    o[2] = fmaf(x.z, f, o[2]);
-    o[3] = fmaf(x.w, f, o[3]);
+    o[0] = fmaf(x.x * f, f, o[0]);
+    o[1] = fmaf(x.y * f, f, o[1]);
+    o[2] = fmaf(x.z * f, f, o[2]);
+    o[3] = fmaf(x.w * f, f, o[3]);
   }
   const size_t at = ((size_t)d.x * a.T + tok) * a.cv.Hq + d.y * G + row % G;
   *(uint2*)(a.out + at * D + 4 * group) = make_uint2(pack2<false>(o[0], o[1]), pack2<false>(o[2], o[3]));

@@ -135,3 +135,37 @@ def test_whole_units(kind, T, sizes):
             ok(p)
         finally:
             p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("L,T,batch", [(700, 9, 38), (700, 64, 38), (700, 9, 1), (3000, 130, 1), (100000, 4, 1)])
+@pytest.mark.parametrize("size", [-90, -100])
+def test_small_values(kind, L, T, batch, size):
+    """The whole history (the others' values 0, or as small), in whole units and in split ones; near-equal logits."""
+    for sizes in ((size,) * 4, (-140, size, -140, -140)):
+        p = Pair(kind, 8 if batch > 1 else 1, 4, batch, L // 64 + 2, seed=4, weights=False)
+        try:
+            q, k, v = sized(p, L, T, sizes, 0.05, True)
+            out, lse = prefill(p, q, k, v)
+            n = slice(0, 3)
+            check_chunk_dense(p, q[n], k[n], v[n], out[n], lse[n])
+            ok(p)
+        finally:
+            p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("T", [9, 64])
+@pytest.mark.parametrize("sizes", [(-100, 110, -100, -100), (110, -100, 60, -60), (-60, -100, 110, 0), (0, 100, 100, -100),
+                                   (-100, 0, -60, 120), (-100, -100, -100, 0), (0, -100, -100, -100)])
+def test_small_values_beside_others(kind, T, sizes):
+    for batch, lead in ((38, 210.0), (38, 40.0), (1, 210.0)):
+        p = Pair(kind, 8, 4, batch, 12, seed=5, weights=False)
+        try:
+            q, k, v = sized(p, 700, T, sizes, 0.3, False, lead)
+            out, lse = prefill(p, q, k, v)
+            n = slice(0, 2)
+            check_chunk_dense(p, q[n], k[n], v[n], out[n], lse[n])
+            ok(p)
+        finally:
+            p.close()
