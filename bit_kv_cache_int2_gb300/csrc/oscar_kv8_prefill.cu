@@ -993,7 +993,7 @@ __device__ __forceinline__ void weigh(Row& st, uint32_t sa, uint32_t oa, const I
   if (first) {
     st.M = aim;
   } else if (__any_sync(0xffffffffu, off)) {
-    const float Mn = F16 ? fmaxf(st.M, aim) : off ? aim : st.M;
+    const float Mn = F16 || !off ? fmaxf(st.M, aim) : aim;
     const float g = ex2(0.5f * (st.M - Mn));  // twice: from small scales to BF16 tokens it is 2^-150
     st.M = Mn;
     // S of this step is complete, so is every MMA issued before it: O has all steps before
