@@ -110,7 +110,10 @@ static_assert(NBARS * 8 <= 240 && sizeof(Info) == 80 && sizeof(Unit) == 48 && OF
 static_assert(SMEM <= 227 * 1024, "shared memory");
 constexpr int S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float C0 = INV_SQRT_D * LOG2E;
-constexpr float NONE = -1e30f, LAZY = 6.f, HEAD = 8.f, FAR = 60.f, SPARE = 32.f;
+// From here on (base 2) a logit has a bit of fraction left in 32 bits, and what one rounding more or less, of the
+// exponent, the maximum and M, adds up to would soon be more than FP16 has room for above P: the row is NaN.
+constexpr float TOO_LARGE = 4194304.f;
+constexpr float NONE = -3.402823466e38f, LAZY = 6.f, HEAD = 8.f, FAR = 60.f, SPARE = 32.f;
 // D fp32, M = N = 128; operand type 0: FP16, 1: BF16; bit 16: V is MN-major
 constexpr uint32_t idesc(int type, int mn) {
   return (1u << 4) | ((uint32_t)type << 7) | ((uint32_t)type << 10) | ((uint32_t)mn << 16) | ((uint32_t)(TILE >> 3) << 17) |
@@ -1214,7 +1217,7 @@ __device__ void softmax(const Kv8Prefill& a, int tid) {
       fence_after();
     }
     const bool bad_v = *(volatile int*)&misc->bad_v != 0 && tiles > hist;
-    float lg = st.l == 0.f ? -INFINITY : st.m + log2f(st.l);
+    float lg = st.m != NONE && fabsf(st.m) >= TOO_LARGE ? NAN : st.l == 0.f ? -INFINITY : st.m + log2f(st.l);
     if (!ok) break;
     if (two) {
       if (rows) write_row(a, u, urow, lg, st.M, oa, 1.f, 0, 0.f, bad_v);

@@ -612,7 +612,9 @@ oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* we
  *          256-byte aligned, no initial contents needed; not to be shared by
  *          calls that may overlap, also of two captured graphs
  * q, k, v, out are device memory, 16-byte aligned.  A value that is not finite
- * shows in the rows that see its token and in no other.
+ * shows in the rows that see its token and in no other.  Logits are held in fp32: a row
+ * that sees tokens with logits beyond 2^21 in magnitude may be NaN (out and lse), and one
+ * whose largest logit lies beyond 2^22 is.
  * A request whose lengths no append can have left (OSCAR_ERR_STATE) counts as
  * empty: its tokens see the chunk alone.  Other device errors:
  * OSCAR_ERR_NO_PAGE / OSCAR_ERR_RANGE for a missing or bad history page, whose

@@ -12,7 +12,7 @@ from bit_kv_cache_int2_gb300 import oscar
 
 pytestmark = pytest.mark.gpu
 
-from kv8_scenario import Pair  # noqa: E402
+from kv8_scenario import Pair, dense  # noqa: E402
 from test_gpu_kv8_prompt import check_chunk_dense, ok, prefill  # noqa: E402
 
 KINDS = [oscar.KV8_E4M3, oscar.KV8_INT8]
@@ -169,3 +169,58 @@ def test_small_values_beside_others(kind, T, sizes):
             ok(p)
         finally:
             p.close()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("a", [8, 9.5, 11, 12, 13, 14, 20, 45, 60])
+@pytest.mark.parametrize("top", [0, 1, 2, 3, None])
+def test_large_logits(kind, a, top):
+    """Queries and keys with one channel, s 2^a and c 2^a: a logit is s c 2^2a / sqrt(128), c a quarter or more apart or
+    the same.  Ties have the same weight, the others nothing (2^-2000).  A tie's weight has one rounding of P
+    (BF16: 2^-8), the output another; the logit of the sum of exponentials, by which a row is divided, one of 2^-24
+    of itself in 32 bits and the lse some more (scale, its product with two constants, the logit's, its own).
+    Beyond 2^22 a row is NaN; where only some of its logits are beyond 2^21, it may be."""
+    for batch, L, T in ((1, 700, 40), (19, 700, 9), (19, 420, 64), (1, 0, 130), (1, 3000, 5)):
+        for positive in (False, True):
+            g = torch.Generator().manual_seed(L + T)
+            p = Pair(kind, 2 if batch == 1 else 8, 4, batch, L // 64 + 2, seed=6, weights=False)
+            try:
+                n, shape = L + T, (batch, L + T, p.Hkv)
+                c = torch.randint(-4, 5, shape, generator=g).float()
+                (h0, h1), places = regions(L, T)[1], regions(L, T)
+                if h1 > h0:  # in the history a block has one key, of sizes that no other token has
+                    c[:, h0:h1] = (torch.randint(-2, 3, (batch, (h1 - h0) // 16, p.Hkv), generator=g) * 2.5).repeat_interleave(16, 1)
+                if top is not None and places[top][1] > places[top][0]:
+                    b0, b1 = places[top]
+                    c[:, b0:b1] = torch.where(c[:, b0:b1].abs() >= 4, c[:, b0:b1].sign() * 6, c[:, b0:b1])
+                if positive:
+                    c = c.abs() + 1
+                    c[:, h0:h1] += 0.25
+                k = torch.zeros(*shape, 128)
+                k[..., 0] = c * 2.0 ** a if a % 1 == 0 else c * 2.0 ** (a - 0.5) * 1.5
+                v = torch.randn(*shape, 128, generator=g)
+                q = torch.zeros(batch, T, p.Hkv * 4, 128)
+                q[..., 0] = (torch.randint(0, 2, q.shape[:3], generator=g) * 2 - 1) * 2.0 ** int(a)
+                k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+                if L:
+                    p.append(L, (k[:, :L].contiguous(), v[:, :L].contiguous()), oracle=False)
+                k, v = k[:, L:].contiguous(), v[:, L:].contiguous()
+                out, lse = prefill(p, q, k, v)
+                hide = torch.arange(n, device="cuda") > L + torch.arange(T, device="cuda")[:, None, None]
+                for h in range(p.Hkv):
+                    K, V = (torch.cat([x, y[0, :, h].cuda().double()]) for x, y in zip(dense(p, 0, h), (k, v)))
+                    mine = slice(4 * h, 4 * h + 4)
+                    z = (q[0, :, mine].cuda().double() @ K.T / 128 ** 0.5).masked_fill(hide, -float("inf"))
+                    w, rl = torch.softmax(z, 2), torch.logsumexp(z, 2)
+                    o, ls = out[0, :, mine].double(), lse[0, :, mine].double()
+                    nan = torch.isnan(ls)
+                    assert torch.equal(torch.isnan(o).all(-1), nan) and torch.equal(torch.isnan(o).any(-1), nan)
+                    assert bool(nan[rl.abs() > 2.0 ** 22].all())
+                    size = z.masked_fill(hide, 0).abs().amax(2)
+                    assert not bool(nan[size < 2.0 ** 21].any())
+                    lim = (2.0 ** -7 + 2.0 ** -14 + 2.0 ** -22 * rl.abs())[..., None] * (w @ V.abs())
+                    assert bool(((o - w @ V).abs() <= lim)[~nan].all()), h
+                    assert bool(((ls - rl).abs() <= 2.0 ** -21 * rl.abs() + 2.0 ** -18)[~nan].all()), h
+                ok(p)
+            finally:
+                p.close()
