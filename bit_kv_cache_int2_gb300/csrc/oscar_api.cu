@@ -1104,7 +1104,7 @@ oscar_status oscar_make_rope(const oscar_rope_config* c, oscar_rope_table* out) 
   if (c->scaling == OSCAR_ROPE_YARN) {
     const auto pair_of = [&](double turns) { return dims * log(c->trained / (turns * 2.0 * pi)) / (2.0 * log(theta)); };
     a = fmax(floor(pair_of(high)), 0.0);
-    b = fmin(ceil(pair_of(low)), n - 1.0);
+    b = fmin(ceil(pair_of(low)), dims - 1.0);  // (of the head's channels, not of the pairs: the ramp may end behind the last one)
   }
   oscar_rope_table t = {};
   for (int i = 0; i < n; ++i) {

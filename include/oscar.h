@@ -659,7 +659,7 @@ oscar_status oscar_read_kv8(oscar_ctx* ctx, const oscar_cache* cache, int type, 
  *   OSCAR_ROPE_NTK     w_i with theta·f^(dims / (dims - 2)) for theta
  *   OSCAR_ROPE_BANDS   (1 - c) w_i / f + c w_i, c = (t_i - low) / (high - low) in 0..1
  *   OSCAR_ROPE_YARN    the same with c = 1 - (i - a) / max(b - a, 0.001) in 0..1,
- *                      a = max(floor(i(high)), 0), b = min(ceil(i(low)), n - 1) and
+ *                      a = max(floor(i(high)), 0), b = min(ceil(i(low)), dims - 1) and
  *                      i(t) = dims ln(trained / 2πt) / (2 ln theta), the (real) pair
  *                      that makes t turns */
 typedef enum {

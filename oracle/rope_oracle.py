@@ -25,7 +25,7 @@ def speeds(dims, theta, scaling=PLAIN, factor=1.0, trained=0.0, low=0.0, high=0.
             keep = (trained * w / (2 * np.pi) - low) / (high - low)
         else:
             pair = lambda t: dims * np.log(trained / (2 * np.pi * t)) / (2 * np.log(theta))  # noqa: E731
-            a, b = max(np.floor(pair(high)), 0.0), min(np.ceil(pair(low)), n - 1.0)
+            a, b = max(np.floor(pair(high)), 0.0), min(np.ceil(pair(low)), dims - 1.0)
             keep = 1.0 - (np.arange(n) - a) / max(b - a, 0.001)
         keep = np.clip(keep, 0.0, 1.0)
         return w / factor * (1 - keep) + w * keep
