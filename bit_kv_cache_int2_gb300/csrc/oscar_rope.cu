@@ -110,7 +110,27 @@ __global__ void __launch_bounds__(RW * 32, NORM ? 5 : 6) rope_kernel(const __gri
         ss += __shfl_xor_sync(0xffffffffu, ss, 1);
         ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-        const float n = rsqrtf(ss * (1.f / D) + a.eps);
+        float n = rsqrtf(ss * (1.f / D) + a.eps);
+        // Squares that leave fp32's range: the head times the power of two that takes its largest magnitude, or the
+        // root of eps where that is larger, to 1 .. 2.
+        const bool rare = in && !value && !(ss + D * a.eps >= 0x1p-60f && ss < 0x1p120f);
+        if (__any_sync(0xffffffffu, rare)) {
+          float m = sqrtf(a.eps), sq = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+          for (int d = 1; d < 8; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const int e = min(max((int)(__float_as_uint(m) >> 23), 1), 253);
+          const float s = rare ? pow2i(127 - e) : 1.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            f[i] *= s;
+            sq = fmaf(f[i], f[i], sq);
+          }
+#pragma unroll
+          for (int d = 1; d < 8; d *= 2) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+          if (rare) n = rsqrtf(sq * (1.f / D) + a.eps * s * s);
+        }
         const bool isq = h < a.Hq;
         float w[8];
         unpack8(isq ? wq[0] : wk[0], w);
