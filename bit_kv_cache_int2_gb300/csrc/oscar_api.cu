@@ -1024,10 +1024,10 @@ oscar_status oscar_prefill_kv8(oscar_ctx* ctx, const oscar_cache* cache, int typ
   if (s != OSCAR_OK) return s;
   if (type != OSCAR_KV8_E4M3 && type != OSCAR_KV8_INT8) return OSCAR_ERR_INVALID_ARG;
   if (T < 0 || T > (1 << 24)) return OSCAR_ERR_INVALID_ARG;
+  if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address, nor need scratch
   const int grid = ctx->num_sms < KV8_PREFILL_MAX_GRID ? ctx->num_sms : KV8_PREFILL_MAX_GRID;
   const Kv8PrefillScratch sl = kv8_prefill_scratch(grid);
   if (!scratch || !aligned(scratch, 256) || scratch_bytes < sl.total) return OSCAR_ERR_INVALID_ARG;
-  if (T == 0 || batch == 0) return OSCAR_OK;  // an array without elements may have no address
   if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
       (lse && !aligned(lse, 4)))
     return OSCAR_ERR_INVALID_ARG;

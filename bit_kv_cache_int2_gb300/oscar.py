@@ -239,6 +239,10 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -635,7 +639,7 @@ def oscar_prefill_kv8(ctx, cache: dict, kv_type, q, k, v, T, out, lse, scratch, 
     cache with 8-bit history and causally to one another.  The chunk is not stored."""
     cs = _cache_struct(cache)
     _check(lib().oscar_prefill_kv8(ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(k), _ptr(v), T, _ptr(out), _ptr(lse),
-                                   _ptr(scratch), scratch.numel() * scratch.element_size(), batch, _stream(stream)),
+                                   _ptr(scratch), _bytes(scratch), batch, _stream(stream)),
            "oscar_prefill_kv8")
 
 
@@ -644,7 +648,7 @@ def bind_prefill_kv8(ctx, cache: dict, kv_type, q, k, v, T, out, lse, scratch, b
     no-argument callable."""
     cs = _cache_struct(cache)
     args = (ctx, ctypes.byref(cs), kv_type, _ptr(q), _ptr(k), _ptr(v), T, _ptr(out), _ptr(lse), _ptr(scratch),
-            scratch.numel() * scratch.element_size(), batch, _stream(stream))
+            _bytes(scratch), batch, _stream(stream))
     fn = lib().oscar_prefill_kv8
 
     def call():
