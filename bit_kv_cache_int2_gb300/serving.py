@@ -30,6 +30,7 @@ effect, not a model.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 import time
 
@@ -294,21 +295,30 @@ class DeviceBackend:
                 by_token = self.kind is not None  # [1][P][Hkv][128]; else [1][Hkv][P][128]
                 Kp = (K[:, :P].transpose(0, 1) if by_token else K[:, :P]).unsqueeze(0).contiguous()
                 Vp = (V[:, :P].transpose(0, 1) if by_token else V[:, :P]).unsqueeze(0).contiguous()
-            if self.import_events is not None:
-                ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
-                ev[0].record()
             w = self.weights[slot:slot + 1] if self.weights is not None else None
             if self.rope is not None:
                 self._prompt(slot, req, rows, view, w)
-            elif self.kind is not None:
-                oscar.oscar_append_kv8(self.ctx, view, self.kind, Kp, Vp, P, 1, weights=w)
-            elif self.fmt == "int2":
-                oscar.oscar_import_tokens(self.ctx, 0, view, Kp, Vp, 1, P)
-            else:
-                oscar.oscar_import_bf16_history(self.ctx, view, Kp, Vp, 1, P)
-            if self.import_events is not None:
-                ev[1].record()
-                self.import_events.append(ev)
+                return
+            with self._timed(self.import_events):
+                if self.kind is not None:
+                    oscar.oscar_append_kv8(self.ctx, view, self.kind, Kp, Vp, P, 1, weights=w)
+                elif self.fmt == "int2":
+                    oscar.oscar_import_tokens(self.ctx, 0, view, Kp, Vp, 1, P)
+                else:
+                    oscar.oscar_import_bf16_history(self.ctx, view, Kp, Vp, 1, P)
+
+    @contextlib.contextmanager
+    def _timed(self, events):
+        """Events around what is launched inside, added to the list (None: not timed)."""
+        import torch
+
+        if events is not None:
+            ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
+            ev[0].record()
+        yield
+        if events is not None:
+            ev[1].record()
+            events.append(ev)
 
     def _turn(self, rows, place, T, batch):
         """Queries, keys and values [batch][T][..][128] of projection rows; the first token of each is at `place`."""
@@ -327,13 +337,15 @@ class DeviceBackend:
         place = self.place[slot:slot + 1]
         for at in range(0, req.prefix, self.prompt_chunk):
             T = min(self.prompt_chunk, req.prefix - at)
-            q, k, v = self._turn(rows[at:at + T].unsqueeze(0), place, T, 1)
-            out = torch.empty_like(q)
-            oscar.oscar_prefill_kv8(self.ctx, view, self.kind, q, k, v, T, out, None, self.chunk_scratch, 1)
+            with self._timed(self.import_events):
+                q, k, v = self._turn(rows[at:at + T].unsqueeze(0), place, T, 1)
+                out = torch.empty_like(q)
+                oscar.oscar_prefill_kv8(self.ctx, view, self.kind, q, k, v, T, out, None, self.chunk_scratch, 1)
             if self.on_prompt is not None:
                 self.on_prompt(req, at, out[0])
-            oscar.oscar_append_kv8(self.ctx, view, self.kind, k, v, T, 1, weights=weights)
-            place += T
+            with self._timed(self.import_events):
+                oscar.oscar_append_kv8(self.ctx, view, self.kind, k, v, T, 1, weights=weights)
+                place += T
 
     def export(self, slot):
         """The cached keys and values of a slot (8-bit history), bf16 [Hkv][n][128] in cache
@@ -360,25 +372,20 @@ class DeviceBackend:
         self.kept[dst] = self.kept.pop(src)
 
     def step(self, active):
-        import torch
-
         n = len(active)
         sl, ps = self.slots[:n], self.pos[:n]
         if self.rope is not None:
-            q, k, v = self._turn(self.rows[sl, ps].unsqueeze(1), self.place[:n], 1, n)
-            q = q[:, 0]
-            self.place[:n] += 1
+            rows = self.rows[sl, ps].unsqueeze(1)
         else:
             k = self.kbuf[sl, ps]
             v = self.vbuf[sl, ps]
             q = self.qbuf[sl, ps]
-        if self.step_events is not None:
-            ev = (torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True))
-            ev[0].record()
-        self.call(k.data_ptr(), v.data_ptr(), q.data_ptr(), n)
-        if self.step_events is not None:
-            ev[1].record()
-            self.step_events.append(ev)
+        with self._timed(self.step_events):
+            if self.rope is not None:
+                q, k, v = self._turn(rows, self.place[:n], 1, n)
+                q = q[:, 0]
+                self.place[:n] += 1
+            self.call(k.data_ptr(), v.data_ptr(), q.data_ptr(), n)
         self.pos[:n] += 1
         if self.on_step is not None:
             self.on_step(active, q, self.out[:n])
@@ -421,13 +428,16 @@ class DeviceBackend:
 
 
 def step_seconds(backend):
-    """Device time of the decode steps (append + attention), summed, when the
+    """Device time of the decode steps (append + attention, from projections
+    their positions too; not the gathering of the slots' tokens), summed, when the
     backend was made with time_steps=True."""
     return sum(a.elapsed_time(b) for a, b in backend.step_events) * 1e-3
 
 
 def import_seconds(backend):
-    """Device time of the prefix imports, summed (time_steps=True)."""
+    """Device time of the prefix imports, summed (time_steps=True); from
+    projections that of the prompts: positions, attention and append of each
+    chunk, without on_prompt."""
     return sum(a.elapsed_time(b) for a, b in backend.import_events) * 1e-3
 
 
