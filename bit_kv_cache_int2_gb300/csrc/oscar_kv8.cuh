@@ -117,7 +117,8 @@ struct Kv8Prefill {
   __nv_bfloat16* out;              // [B][T][Hq][128]
   float* lse;                      // [B][T][Hq] or null
   int4* splits;                    // scratch [grid]: the unit that begins in a CTA's part and ends in a later one's
-  float* part;                     // scratch [grid][2][256][PART_STRIDE]: m, l, M, o (oscar_kv8_prefill.cu)
+  float* part;                     // scratch [grid][2] records of 256·PART_STRIDE floats: o [32][256] of 4 channels,
+                                   //   log2 of the sum of exponentials [256], M [256] (oscar_kv8_prefill.cu)
   int B, T, grid, wait_polls;
   // set by launch_kv8_prefill: log2 of G; units of 256 rows of a (request, kv head); M of BF16 tokens above their logits
   int lg, units;

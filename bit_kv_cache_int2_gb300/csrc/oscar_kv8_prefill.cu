@@ -685,7 +685,7 @@ __device__ void scout(const Kv8Prefill& a, int lane) {
 // A whole warp, one lane elected for the instructions: with every value the same in
 // all lanes (`same` tells the compiler so) an MMA takes the 64 cycles of its
 // arithmetic, issued from a divergent branch 150.  It learns what a tile is from
-// the producers' flags: anything slower than the MMAs would hold them up.
+// the scout's flags: anything slower than the MMAs would hold them up.
 __device__ __forceinline__ uint64_t desc(uint32_t lo, uint64_t hi) { return hi | lo; }
 __device__ __forceinline__ uint32_t same(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool elect() {
