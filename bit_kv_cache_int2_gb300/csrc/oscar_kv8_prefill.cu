@@ -43,12 +43,12 @@
 // and each waits for the other's barriers (a look at shared memory takes 250 to 300
 // cycles while MMAs read their operands there: S = Q·K^T takes all of its bandwidth).
 // Two row tiles in flight hide part of that, tensor memory has no place for a third.
-// Measured (one GB300, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8 heads,
-// 2720 to 2740 us, 1240 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191 541 us, 1020
-// TFLOP/s of the causal half; 64 tokens over 100K 115 us, 4 x 509 tokens over 0.3K to 9K
-// 354 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 182 us (3.7 TB/s; the FP16
+// Measured (several GB300s, bf16 burst peak 1894 TFLOP/s): 2048 tokens over 100K, 32/8 heads,
+// 2660 to 2820 us by the card, 1270 to 1200 TFLOP/s; 1024 over 50K 715 us; a prompt of 8191
+// 550 us, 1000 TFLOP/s of the causal half; 64 tokens over 100K 114 us, 4 x 509 tokens over 0.3K
+// to 9K 361 us.  Few rows: 16 requests with 5 tokens over 8K to 32K 181 us (3.7 TB/s; the FP16
 // tiles are written to shared memory and read by MMAs of 128 rows, which with the waits
-// takes most of its cycles), 5 tokens over 1K 18 us (two launches, the list, three
+// takes most of its cycles), 5 tokens over 1K 17 us (two launches, the list, three
 // dependent trips to memory, instructions that are not in the caches).
 //
 // One MMA warp, not one a row tile (prompt 631 -> 584 at the time, but 2048 tokens over 100K

@@ -44,8 +44,9 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // with four pairs.  A warp takes heads 4·part, 4·(part + parts), .. of its token; the
 // next heads are on their way while it works on these.
 // Bound by memory: what a token reads it writes.  100,003 tokens of 32/8 heads (2.46 GB in
-// and out) take 378 us, 6.5 TB/s; with norms 410, as registers leave 20 warps an SM (24 with
-// spills: 430; heads loaded when their turn came: 556).
+// and out) take 378 us, 6.5 TB/s; with norms 417 to 422, as registers leave 20 warps an SM (24 with
+// spills: 430; heads loaded when their turn came: 556) and a warp votes on whether one of its
+// heads is out of the squares' range (7 of these).
 template <int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(RW * 32, NORM ? 5 : 6) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ uint64_t turn[64];

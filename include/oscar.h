@@ -612,8 +612,11 @@ oscar_status oscar_evict_kv8(oscar_ctx* ctx, const oscar_cache* cache, float* we
  *          256-byte aligned, no initial contents needed; not to be shared by
  *          calls that may overlap, also of two captured graphs
  * q, k, v, out are device memory, 16-byte aligned.  A value that is not finite
- * shows in the rows that see its token and in no other.  Logits are held in fp32: a row
- * that sees tokens with logits beyond 2^21 in magnitude may be NaN (out and lse), and one
+ * shows in the rows that see its token and in no other.  Softmax weights are fp32, and are
+ * rounded for the product with the values: those of history tokens to FP16, those of
+ * sink, window and chunk to BF16 (8 bits; oscar_decode_kv8 keeps 16 there), where
+ * weights below 2^-60 of a row's largest may count as 0.  Logits are fp32: a row that
+ * sees tokens with logits beyond 2^21 in magnitude may be NaN (out and lse), and one
  * whose largest logit lies beyond 2^22 is.
  * A request whose lengths no append can have left (OSCAR_ERR_STATE) counts as
  * empty: its tokens see the chunk alone.  Other device errors:
