@@ -1086,7 +1086,7 @@ oscar_status oscar_make_rope(const oscar_rope_config* c, oscar_rope_table* out) 
   if (c->dims < 16 || c->dims > D || c->dims % 16) return OSCAR_ERR_UNSUPPORTED;
   const bool scaled = c->scaling != OSCAR_ROPE_PLAIN;
   const bool by_turns = c->scaling == OSCAR_ROPE_BANDS || c->scaling == OSCAR_ROPE_YARN;
-  if (!(std::isfinite(c->theta) && c->theta > 1.0) || !std::isfinite(c->size)) return OSCAR_ERR_INVALID_ARG;
+  if (!(std::isfinite(c->theta) && c->theta > 1.0) || !std::isfinite((float)c->size)) return OSCAR_ERR_INVALID_ARG;
   if (scaled && !(std::isfinite(c->factor) && c->factor > 0.0)) return OSCAR_ERR_INVALID_ARG;
   double low = c->low, high = c->high;
   if (by_turns) {

@@ -686,7 +686,7 @@ typedef struct {
   double factor;    /* > 0; not used by OSCAR_ROPE_PLAIN                             */
   double trained;   /* > 0; used by OSCAR_ROPE_BANDS and OSCAR_ROPE_YARN             */
   double low, high; /* turns, 0 < low < high; 0, 0: 1 and 4 (BANDS), 1 and 32 (YARN) */
-  double size;      /* what cosine and sine are multiplied by; 0: 1, for OSCAR_ROPE_YARN
+  double size;      /* what cosine and sine are multiplied by (in fp32); 0: 1, for OSCAR_ROPE_YARN
                        0.1 ln(factor) + 1 (1 where factor < 1)                       */
 } oscar_rope_config;
 

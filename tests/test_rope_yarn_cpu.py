@@ -44,3 +44,11 @@ def test_table_is_the_oracles(dims, theta, trained):
     t = oscar.make_rope(oscar.ROPE_HALF, dims, theta, oscar.ROPE_YARN, factor=4.0, trained=trained)
     for i, w in enumerate(R.speeds(dims, theta, R.YARN, 4.0, trained)):
         assert abs(t.turn[i] / 2.0 ** 64 - w / (2 * math.pi)) <= 2.0 ** -44 * max(w / (2 * math.pi), 2.0 ** -20), i
+
+
+@pytest.mark.parametrize("size", [1e39, -1e300, 3.5e38])
+def test_a_size_that_32_bits_do_not_hold_is_refused(size):
+    with pytest.raises(oscar.OscarError) as e:
+        oscar.make_rope(size=size)
+    assert e.value.status == oscar.ERR_INVALID_ARG
+    assert oscar.make_rope(size=3e38).size == pytest.approx(3e38, rel=1e-6)
